@@ -13,6 +13,16 @@ from ._build import LIB
 
 _c_int, _c_i64, _c_size, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
+
+
+class FFNWeightsStruct(ctypes.Structure):
+    """``moe_ffn_weights`` of include/moe.h."""
+
+    _fields_ = [("format", ctypes.c_int32), ("w13", _vp), ("w13_scales", _vp),
+                ("w13_tensor_scale", _vp), ("w2", _vp), ("w2_scales", _vp),
+                ("w2_tensor_scale", _vp)]
+
+
 # name -> (restype, argtypes), mirroring include/moe.h
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_c_int]),
@@ -39,6 +49,14 @@ SIGNATURES = {
     "moe_grouped_ffn_w8a8": (_c_int, [_vp, _vp, _c_i64, _vp, _c_int, _vp, _vp, _c_int, _c_int,
                                       _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_int, _vp,
                                       _c_size, _vp, _vp]),
+    "moe_pack_ffn_weights_fp4": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _vp]),
+    "moe_grouped_ffn_fp4_workspace_bytes": (_c_size, [_c_i64, _c_int, _c_int, _c_int]),
+    "moe_grouped_ffn_fp4": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_i64,
+                                     _c_int, _vp, _c_size, _vp, _vp]),
+    "moe_decode_workspace_bytes": (_c_size, [_c_int] * 6),
+    "moe_decode": (_c_int, [_vp, _vp, _vp] + [_c_int] * 8 + [_vp, _vp, _vp, _vp, _c_int, _vp, _vp,
+                                                            _c_size, _vp, _vp]),
     "moe_fake_quant_rows": (_c_int, [_vp, _vp, _c_i64, _c_int, _vp, _c_int, _c_int, _vp, _vp,
                                      _vp, _vp]),
     "moe_scale_from_amax": (_c_int, [_vp, _vp, _c_int, _vp]),

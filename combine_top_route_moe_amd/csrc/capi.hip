@@ -38,6 +38,16 @@ int launch_grouped_ffn_w8a8(const uint8_t*, const float*, int64_t, const int32_t
                             const int32_t*, const int32_t*, int, int, int, const uint8_t*, const float*, const uint8_t*,
                             const float*, const float*, uint16_t*, int64_t, int, void*, int32_t*,
                             hipStream_t);
+int launch_pack_weights_fp4(const uint16_t*, const uint16_t*, int, int, int, int, const float*,
+                            const float*, uint8_t*, uint8_t*, uint8_t*, uint8_t*, hipStream_t);
+size_t grouped_ffn_fp4_workspace_bytes(int64_t, int, int);
+int launch_grouped_ffn_fp4(const uint16_t*, const int32_t*, const int32_t*, int, int, int,
+                           const moe_ffn_weights*, const float*, uint16_t*, int64_t, int, void*,
+                           int32_t*, hipStream_t);
+size_t decode_workspace_bytes(int, int, int, int, int);
+int launch_decode(const float*, const uint8_t*, const uint16_t*, int, int, int, int, int, int, int,
+                  int, int32_t*, float*, const moe_ffn_weights*, const moe_ffn_weights*, int,
+                  uint16_t*, void*, int32_t*, hipStream_t);
 
 // Each workgroup copies runs of 4 x 256 vectors: the four loads of a thread
 // are in flight together, and both sides stream past the caches
@@ -92,7 +102,7 @@ const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size or bad flag)";
-    case MOE_ERR_UNSUPPORTED: return "unsupported shape (H and I must be multiples of 128; E, G <= 1024; K <= 32)";
+    case MOE_ERR_UNSUPPORTED: return "unsupported shape (H and I must be multiples of 128; E, G <= 1024; K <= 32; moe_decode: T <= 64)";
     case MOE_ERR_WORKSPACE: return "workspace smaller than the size query requires";
     case MOE_ERR_HIP: return "HIP runtime error or kernel launch failure";
     case MOE_ERR_DEVICE: return "the current device is not a gfx950 (MI355X-class) GPU";
@@ -327,6 +337,100 @@ int moe_pack_ffn_weights_fp8(const uint16_t* w13, const uint16_t* w2, int num_gr
     return MOE_ERR_INVALID_ARG;
   return launch_pack_weights_fp8(w13, w2, num_groups, H, I, w13q, w13_scales, w2q, w2_scales,
                                  (flags & MOE_FP8_LAYOUT_K128) ? 1 : 0, as_stream(stream));
+}
+
+int moe_pack_ffn_weights_fp4(const uint16_t* w13, const uint16_t* w2, int num_groups, int H,
+                             int I, int mode, const float* w13_tensor_scale,
+                             const float* w2_tensor_scale, uint8_t* w13q, uint8_t* w13_scales,
+                             uint8_t* w2q, uint8_t* w2_scales, void* stream) {
+  if (num_groups < 1 || H < 1 || I < 1) return MOE_ERR_INVALID_ARG;
+  if (mode != MOE_FQ_MXFP4 && mode != MOE_FQ_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (H % 128 || I % 128) return MOE_ERR_UNSUPPORTED;
+  if (!w13 != !w13q || !w13 != !w13_scales || !w2 != !w2q || !w2 != !w2_scales)
+    return MOE_ERR_INVALID_ARG;
+  if (mode == MOE_FQ_NVFP4 && ((w13 && !w13_tensor_scale) || (w2 && !w2_tensor_scale)))
+    return MOE_ERR_INVALID_ARG;
+  if ((w13 && (!aligned16(w13) || !aligned16(w13q) || !aligned16(w13_scales))) ||
+      (w2 && (!aligned16(w2) || !aligned16(w2q) || !aligned16(w2_scales))))
+    return MOE_ERR_INVALID_ARG;
+  return launch_pack_weights_fp4(w13, w2, num_groups, H, I, mode, w13_tensor_scale,
+                                 w2_tensor_scale, w13q, w13_scales, w2q, w2_scales,
+                                 as_stream(stream));
+}
+
+// The pointers that `stages` of the FFN read in a weights struct.
+static bool weights_ok(const moe_ffn_weights* w, int stages) {
+  if (!w || w->format < MOE_W_BF16 || w->format > MOE_W_NVFP4) return false;
+  auto matrix = [&](const void* codes, const void* scales, const float* tensor_scale) {
+    if (!codes || !aligned16(codes)) return false;
+    if (w->format != MOE_W_BF16 && (!scales || !aligned16(scales))) return false;
+    return w->format != MOE_W_NVFP4 || tensor_scale != nullptr;
+  };
+  return (!(stages & MOE_FFN_GATE_UP) || matrix(w->w13, w->w13_scales, w->w13_tensor_scale)) &&
+         (!(stages & MOE_FFN_DOWN) || matrix(w->w2, w->w2_scales, w->w2_tensor_scale));
+}
+
+size_t moe_grouped_ffn_fp4_workspace_bytes(int64_t capacity, int num_groups, int H, int I) {
+  (void)H;
+  if (capacity < 0 || num_groups < 1 || I < 1) return 0;
+  return grouped_ffn_fp4_workspace_bytes(capacity, num_groups, I);
+}
+
+int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int32_t* counts,
+                        int num_groups, int H, int I, const moe_ffn_weights* weights,
+                        const float* row_scale, uint16_t* y, int64_t capacity, int flags,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                        void* stream) {
+  if (num_groups < 1 || H < 1 || I < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
+  if ((flags & ~MOE_FFN_ALL) || !(flags & MOE_FFN_ALL)) return MOE_ERR_INVALID_ARG;
+  if (H % 128 || I % 128 || num_groups > 1024) return MOE_ERR_UNSUPPORTED;
+  if (capacity > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (!weights || (weights->format != MOE_W_MXFP4 && weights->format != MOE_W_NVFP4))
+    return MOE_ERR_INVALID_ARG;
+  if (capacity == 0) return MOE_OK;   // no rows: nothing to read or write
+  if (!cu_seqlens || !counts || !weights_ok(weights, flags)) return MOE_ERR_INVALID_ARG;
+  if (((flags & MOE_FFN_GATE_UP) && !x) || ((flags & MOE_FFN_DOWN) && !y))
+    return MOE_ERR_INVALID_ARG;
+  if ((x && !aligned16(x)) || (y && !aligned16(y))) return MOE_ERR_INVALID_ARG;
+  const size_t need = grouped_ffn_fp4_workspace_bytes(capacity, num_groups, I);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return launch_grouped_ffn_fp4(x, cu_seqlens, counts, num_groups, H, I, weights, row_scale, y,
+                                capacity, flags, workspace, dev_error, as_stream(stream));
+}
+
+size_t moe_decode_workspace_bytes(int T, int H, int I, int K, int num_local_experts,
+                                  int shared_I) {
+  (void)H;
+  if (T < 0 || I < 1 || K < 1 || num_local_experts < 1 || shared_I < 0) return 0;
+  return decode_workspace_bytes(T, I, K, num_local_experts, shared_I);
+}
+
+int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hidden, int T,
+               int H, int I, int num_experts, int K, int expert_begin, int num_local_experts,
+               int flags, int32_t* topk_idx, float* topk_w, const moe_ffn_weights* weights,
+               const moe_ffn_weights* shared, int shared_I, uint16_t* out, void* workspace,
+               size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (T < 0 || H < 1 || I < 1 || num_experts < 1 || K < 1 || K > num_experts || shared_I < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (expert_begin < 0 || num_local_experts < 1 ||
+      (int64_t)expert_begin + num_local_experts > (int64_t)num_experts)
+    return MOE_ERR_INVALID_ARG;
+  if (flags & ~MOE_ROUTE_RENORM) return MOE_ERR_INVALID_ARG;
+  if (!shared != !shared_I) return MOE_ERR_INVALID_ARG;
+  if (T > 64 || K > 32 || num_experts > 1024 || H % 128 || I % 128 || shared_I % 128)
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!hidden || !topk_idx || !topk_w || !out || !weights_ok(weights, MOE_FFN_ALL))
+    return MOE_ERR_INVALID_ARG;
+  if (shared && (!weights_ok(shared, MOE_FFN_ALL) || shared->format != weights->format))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(out) || hidden == out) return MOE_ERR_INVALID_ARG;
+  const size_t need = decode_workspace_bytes(T, I, K, num_local_experts, shared_I);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  return launch_decode(logits, row_valid, hidden, T, H, I, num_experts, K, expert_begin,
+                       num_local_experts, (flags & MOE_ROUTE_RENORM) ? 1 : 0, topk_idx, topk_w,
+                       weights, shared, shared_I, out, workspace, dev_error, as_stream(stream));
 }
 
 int moe_fake_quant_rows(const uint16_t* in, uint16_t* out, int64_t n_rows, int H,

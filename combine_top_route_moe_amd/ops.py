@@ -8,12 +8,13 @@ Outputs that the caller does not pass are allocated here with
 
 from __future__ import annotations
 
-from dataclasses import dataclass
+import ctypes
+from dataclasses import dataclass, field
 from typing import Optional
 
 import torch
 
-from ._lib import load, check
+from ._lib import FFNWeightsStruct, load, check
 
 MOE_ROUTE_RENORM = 1
 MOE_PERMUTE_PAD_POW2 = 1
@@ -23,6 +24,8 @@ MOE_FQ_PER_TENSOR, MOE_FQ_BLOCK, MOE_FQ_NVFP4, MOE_FQ_MXFP4 = 0, 1, 2, 3
 MOE_DEVERR_ROW_RANGE, MOE_DEVERR_CAPACITY, MOE_DEVERR_LAYOUT, MOE_DEVERR_EXPERT_RANGE = 1, 2, 3, 4
 MOE_ERR_SCRATCH = -6
 MOE_FP8_LAYOUT_K128 = 1
+MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4, MOE_W_NVFP4 = 0, 1, 2, 3
+MOE_DECODE_MAX_TOKENS = 64
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -351,6 +354,250 @@ def moe_grouped_ffn_w8a8(xq: torch.Tensor, x_scales: torch.Tensor, cu_seqlens: t
         _ptr(w13q), _ptr(w13_scales), _ptr(w2q), _ptr(w2_scales), _ptr(row_scale), _ptr(y),
         capacity, flags, _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(stream)))
     return y
+
+
+@dataclass
+class FFNWeights:
+    """Packed expert weights in one format (``MOE_W_*``): what ``moe_decode``
+    and ``moe_grouped_ffn_fp4`` take.  Built by ``ffn_weights``, or from the
+    outputs of the pack functions."""
+
+    format: int
+    num_groups: int
+    H: int
+    I: int
+    w13: torch.Tensor
+    w2: torch.Tensor
+    w13_scales: Optional[torch.Tensor] = None
+    w2_scales: Optional[torch.Tensor] = None
+    w13_tensor_scale: Optional[torch.Tensor] = None
+    w2_tensor_scale: Optional[torch.Tensor] = None
+    _c: FFNWeightsStruct = field(init=False, repr=False)
+
+    def __post_init__(self):
+        G, H, I = self.num_groups, self.H, self.I
+        fp4 = self.format in (MOE_W_MXFP4, MOE_W_NVFP4)
+        if self.format not in (MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4, MOE_W_NVFP4):
+            raise ValueError(f"unknown weight format {self.format!r}")
+        half, code = (2, torch.uint8) if fp4 else (1, torch.uint8)
+        if self.format == MOE_W_BF16:
+            code = torch.bfloat16
+        group = {MOE_W_MXFP4: 32, MOE_W_NVFP4: 16}.get(self.format)
+        want = {"w13": ((G, 2 * I, H // half), code), "w2": ((G, H, I // half), code)}
+        if self.format == MOE_W_FP8:
+            want |= {"w13_scales": ((G, 2 * I // 128, H // 128), torch.float32),
+                     "w2_scales": ((G, H // 128, I // 128), torch.float32)}
+        if fp4:
+            want |= {"w13_scales": ((G, 2 * I, H // group), torch.uint8),
+                     "w2_scales": ((G, H, I // group), torch.uint8)}
+        if self.format == MOE_W_NVFP4:
+            want |= {"w13_tensor_scale": ((G,), torch.float32),
+                     "w2_tensor_scale": ((G,), torch.float32)}
+        for name, (shape, dtype) in want.items():
+            t = getattr(self, name)
+            if t is None:
+                raise ValueError(f"{name} is missing")
+            _want(t, dtype, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+            if t.device != self.w13.device:
+                raise ValueError(f"{name}: not on the device of w13")
+        self._c = FFNWeightsStruct(self.format, *(
+            _ptr(getattr(self, n)) if n in want else None
+            for n in ("w13", "w13_scales", "w13_tensor_scale", "w2", "w2_scales",
+                      "w2_tensor_scale")))
+
+
+def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
+                w13_tensor_scale: Optional[torch.Tensor] = None,
+                w2_tensor_scale: Optional[torch.Tensor] = None, stream=None) -> FFNWeights:
+    """Pack bf16 w13 [G,2I,H] / w2 [G,H,I] once into ``fmt``: "bf16", "fp8",
+    "mxfp4" or "nvfp4" (its tensor scales [G] from the weights' amax where
+    they are not given)."""
+    _want(w13, torch.bfloat16, "w13")
+    _want(w2, torch.bfloat16, "w2")
+    G, two_i, H = w13.shape
+    I = two_i // 2
+    if tuple(w2.shape) != (G, H, I) or two_i % 2:
+        raise ValueError("w13 must be [G, 2I, H] and w2 [G, H, I]")
+    if fmt == "bf16":
+        p13, p2 = moe_pack_ffn_weights(w13, w2, stream=stream)
+        return FFNWeights(MOE_W_BF16, G, H, I, p13, p2)
+    if fmt == "fp8":
+        q13, s13, q2, s2 = moe_pack_ffn_weights_fp8(w13, w2, stream=stream)
+        return FFNWeights(MOE_W_FP8, G, H, I, q13, q2, s13, s2)
+    if fmt not in ("mxfp4", "nvfp4"):
+        raise ValueError(f"unknown weight format {fmt!r}")
+    mode = MOE_FQ_MXFP4 if fmt == "mxfp4" else MOE_FQ_NVFP4
+    q13, s13, g13, q2, s2, g2 = moe_pack_ffn_weights_fp4(w13, w2, mode, w13_tensor_scale,
+                                                         w2_tensor_scale, stream=stream)
+    return FFNWeights(MOE_W_MXFP4 if fmt == "mxfp4" else MOE_W_NVFP4, G, H, I, q13, q2, s13, s2,
+                      g13, g2)
+
+
+def _tensor_scales(w: torch.Tensor, stream=None) -> torch.Tensor:
+    """The NVFP4 tensor scale amax / 2688 of every group of w [G, N, K]."""
+    G = w.shape[0]
+    amax = torch.zeros(G, dtype=torch.float32, device=w.device)
+    scale = torch.empty(G, dtype=torch.float32, device=w.device)
+    for g in range(G):
+        moe_fake_quant_rows(w[g], mode=MOE_FQ_NVFP4, block=16, amax_out=amax[g:g + 1],
+                            stream=stream)
+        moe_scale_from_amax(amax[g:g + 1], scale[g:g + 1], stream=stream, mode=MOE_FQ_NVFP4)
+    return scale
+
+
+def moe_pack_ffn_weights_fp4(w13: Optional[torch.Tensor], w2: Optional[torch.Tensor],
+                             mode: int = MOE_FQ_MXFP4,
+                             w13_tensor_scale: Optional[torch.Tensor] = None,
+                             w2_tensor_scale: Optional[torch.Tensor] = None, stream=None):
+    """Quantize w13 [G,2I,H] / w2 [G,H,I] to 4-bit codes with group scales in
+    the packed order of moe_grouped_ffn_fp4 and moe_decode.  ``mode``:
+    MOE_FQ_MXFP4 or MOE_FQ_NVFP4 (whose tensor scales [G] are taken from the
+    weights' amax where they are not given).  Returns ``(w13q, w13_scales,
+    w13_tensor_scale, w2q, w2_scales, w2_tensor_scale)`` (None for an absent
+    input, and for MXFP4's tensor scales)."""
+    if mode not in (MOE_FQ_MXFP4, MOE_FQ_NVFP4):
+        raise ValueError("mode must be MOE_FQ_MXFP4 or MOE_FQ_NVFP4")
+    group = 32 if mode == MOE_FQ_MXFP4 else 16
+    if w13 is not None:
+        _want(w13, torch.bfloat16, "w13")
+        G, two_i, H = w13.shape
+        I = two_i // 2
+    if w2 is not None:
+        _want(w2, torch.bfloat16, "w2")
+        if w13 is not None and tuple(w2.shape) != (G, H, I):
+            raise ValueError("w13 must be [G, 2I, H] and w2 [G, H, I]")
+        G, H, I = w2.shape
+    elif w13 is None:
+        raise ValueError("w13 and w2 are both absent")
+
+    def one(w, g):
+        if w is None:
+            return None, None, None
+        if mode == MOE_FQ_MXFP4:
+            g = None
+        elif g is None:
+            g = _tensor_scales(w, stream)
+        else:
+            _want(g, torch.float32, "tensor_scale")
+            if tuple(g.shape) != (G,):
+                raise ValueError(f"tensor scales: expected shape ({G},), got {tuple(g.shape)}")
+        N, Kd = w.shape[1:]
+        return (torch.empty(G, N, Kd // 2, dtype=torch.uint8, device=w.device),
+                torch.empty(G, N, Kd // group, dtype=torch.uint8, device=w.device), g)
+
+    q13, s13, g13 = one(w13, w13_tensor_scale)
+    q2, s2, g2 = one(w2, w2_tensor_scale)
+    check("moe_pack_ffn_weights_fp4", load().moe_pack_ffn_weights_fp4(
+        _ptr(w13), _ptr(w2), G, H, I, mode, _ptr(g13), _ptr(g2), _ptr(q13), _ptr(s13), _ptr(q2),
+        _ptr(s2), _stream(stream)))
+    return q13, s13, g13, q2, s2, g2
+
+
+def moe_grouped_ffn_fp4_workspace_bytes(capacity: int, num_groups: int, H: int, I: int) -> int:
+    return load().moe_grouped_ffn_fp4_workspace_bytes(capacity, num_groups, H, I)
+
+
+def moe_grouped_ffn_fp4(x: torch.Tensor, cu_seqlens: torch.Tensor, counts: torch.Tensor,
+                        weights: FFNWeights, row_scale: Optional[torch.Tensor] = None,
+                        y: Optional[torch.Tensor] = None, flags: int = MOE_FFN_ALL,
+                        workspace: Optional[torch.Tensor] = None,
+                        dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The grouped FFN with 4-bit weights (``ffn_weights(..., "mxfp4")`` or
+    "nvfp4")."""
+    _want(x, torch.bfloat16, "x")
+    _want(cu_seqlens, torch.int32, "cu_seqlens")
+    _want(counts, torch.int32, "counts")
+    if row_scale is not None:
+        _want(row_scale, torch.float32, "row_scale")
+    capacity, H = x.shape
+    G, I = weights.num_groups, weights.I
+    if H != weights.H:
+        raise ValueError("weight shapes do not match x")
+    if counts.numel() != G or cu_seqlens.numel() != G + 1:
+        raise ValueError("counts / cu_seqlens do not match the number of groups")
+    if row_scale is not None and row_scale.numel() < capacity:
+        raise ValueError("row_scale is shorter than x")
+    if y is None:
+        y = torch.empty(capacity, H, dtype=torch.bfloat16, device=x.device)
+    else:
+        _want(y, torch.bfloat16, "y")
+        if tuple(y.shape) != (capacity, H):
+            raise ValueError("y does not match x")
+    lib = load()
+    if workspace is None:
+        need = lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    check("moe_grouped_ffn_fp4", lib.moe_grouped_ffn_fp4(
+        _ptr(x), _ptr(cu_seqlens), _ptr(counts), G, H, I, ctypes.addressof(weights._c),
+        _ptr(row_scale), _ptr(y), capacity, flags, _ptr(workspace), workspace.numel(),
+        _ptr(dev_error), _stream(stream)))
+    return y
+
+
+def moe_decode_workspace_bytes(T: int, H: int, I: int, K: int, num_local_experts: int,
+                               shared_I: int = 0) -> int:
+    return load().moe_decode_workspace_bytes(T, H, I, K, num_local_experts, shared_I)
+
+
+def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, weights: FFNWeights,
+               row_valid: Optional[torch.Tensor] = None, renormalize: bool = True,
+               expert_begin: int = 0, num_experts: Optional[int] = None,
+               shared: Optional[FFNWeights] = None, topk_idx: Optional[torch.Tensor] = None,
+               topk_w: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None,
+               dev_error: Optional[torch.Tensor] = None, stream=None):
+    """The whole layer for up to 64 tokens: ``(out, topk_idx, topk_w)``.  With
+    ``logits`` None the routes ``topk_idx`` / ``topk_w`` are inputs and
+    ``num_experts`` is the layer's expert count (by default the end of the
+    local range); else they are written.  ``weights``: the local experts',
+    starting at ``expert_begin``; ``shared``: the shared expert's (one group,
+    the same format)."""
+    T, H = hidden.shape
+    dev = hidden.device
+    _want(hidden, torch.bfloat16, "hidden")
+    if logits is not None:
+        _want(logits, torch.float32, "logits")
+        if logits.shape[0] != T or num_experts not in (None, logits.shape[1]):
+            raise ValueError("logits must be [T, num_experts]")
+        num_experts = logits.shape[1]
+    elif topk_idx is None or topk_w is None:
+        raise ValueError("without logits, topk_idx and topk_w are needed")
+    elif num_experts is None:
+        num_experts = expert_begin + weights.num_groups
+    if topk_idx is None:
+        topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+    _want(topk_idx, torch.int32, "topk_idx")
+    _want(topk_w, torch.float32, "topk_w")
+    if tuple(topk_idx.shape) != (T, k) or tuple(topk_w.shape) != (T, k):
+        raise ValueError("topk_idx and topk_w must be [T, k]")
+    if row_valid is not None:
+        _want(row_valid, torch.uint8, "row_valid")
+        if row_valid.numel() != T:
+            raise ValueError("row_valid must be [T]")
+    if weights.H != H or (shared is not None and (shared.H != H or shared.num_groups != 1)):
+        raise ValueError("weight shapes do not match hidden")
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _want(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (T, H):
+            raise ValueError("out does not match hidden")
+    lib = load()
+    shared_I = shared.I if shared is not None else 0
+    if workspace is None:
+        need = lib.moe_decode_workspace_bytes(T, H, weights.I, k, weights.num_groups, shared_I)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    check("moe_decode", lib.moe_decode(
+        _ptr(logits), _ptr(row_valid), _ptr(hidden), T, H, weights.I, num_experts, k, expert_begin,
+        weights.num_groups, MOE_ROUTE_RENORM if renormalize else 0, _ptr(topk_idx), _ptr(topk_w),
+        ctypes.addressof(weights._c), ctypes.addressof(shared._c) if shared is not None else None,
+        shared_I, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_error),
+        _stream(stream)))
+    return out, topk_idx, topk_w
 
 
 def moe_fake_quant_rows(inp: torch.Tensor, out: Optional[torch.Tensor] = None,

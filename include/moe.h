@@ -81,6 +81,29 @@ enum { MOE_FQ_PER_TENSOR = 0,         /* moe_fake_quant_rows modes         */
        MOE_FQ_MXFP4 = 3 };
 enum { MOE_FP8_LAYOUT_K128 = 1 };     /* moe_pack_ffn_weights_fp8: the FP8
                                          matrix-core GEMM's weight order     */
+enum { MOE_W_BF16 = 0,                /* expert-weight formats: bf16, packed  */
+       MOE_W_FP8 = 1,                 /* E4M3 codes, 128 x 128 tile scales    */
+       MOE_W_MXFP4 = 2,               /* E2M1 codes, E8M0 scales of 32        */
+       MOE_W_NVFP4 = 3 };             /* E2M1 codes, E4M3 scales of 16        */
+
+/* The packed weights of G experts (device pointers) in one of the formats
+ * above; the struct itself is host memory, read during the call only.
+ *   MOE_W_BF16   w13, w2 from moe_pack_ffn_weights; no scales
+ *   MOE_W_FP8    w13, w2 and their scales from moe_pack_ffn_weights_fp8
+ *                (flags 0)
+ *   MOE_W_MXFP4, MOE_W_NVFP4  w13, w2 and their scales from
+ *                moe_pack_ffn_weights_fp4; NVFP4 also the tensor scales that
+ *                call was given ([G] float32 each)
+ * Pointers the format does not name are ignored. */
+typedef struct {
+  int32_t format;
+  const void* w13;
+  const void* w13_scales;
+  const float* w13_tensor_scale;
+  const void* w2;
+  const void* w2_scales;
+  const float* w2_tensor_scale;
+} moe_ffn_weights;
 
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* moe_status_string(int status);
@@ -339,6 +362,93 @@ int moe_grouped_ffn_w8a8(const uint8_t* xq, const float* x_scales, int64_t scale
                          const float* w2_scales, const float* row_scale, uint16_t* y,
                          int64_t capacity, int flags, void* workspace, size_t workspace_bytes,
                          int32_t* dev_error, void* stream);
+
+/* ---- 4-bit expert weights with group scales -------------------------------
+ * [P4]'s test plan runs an MXFP4 expert path and [P1] names NVFP4 units; the
+ * formats are the published ones, with the arithmetic of
+ * moe_fake_quant_rows's FP4 modes applied to every weight row along its
+ * reduction dimension:
+ *   MOE_FQ_MXFP4: E2M1 codes, per 32 weights the power of two X as an E8M0
+ *     byte (an all-zero group: codes 0);
+ *   MOE_FQ_NVFP4: E2M1 codes, per 16 weights the E4M3 block scale b under
+ *     the group's float32 tensor scale g = tensor_scale[group] (for instance
+ *     moe_scale_from_amax of that expert's matrix).
+ * The weight a code stands for is the value the fake-quant writes:
+ * bf16(code * X), exact, or bf16(fl32(code * fl32(b * g))).  Packing values
+ * that are already such a quantization (an MXFP4 checkpoint, dequantized)
+ * gives the same values back; for NVFP4 with the same g, wherever a block's
+ * largest code is 6.
+ *   w13 [G, 2I, H], w2 [G, H, I] bf16; w13_tensor_scale, w2_tensor_scale [G]
+ *   float32 (NVFP4; NULL for MXFP4).  Outputs, in 64-row column tiles ct and
+ *   fragments f as in moe_pack_ffn_weights, 128-wide K-blocks kb:
+ *   w13q [G, 2I, H/2], w2q [G, H, I/2] uint8: 16-byte unit
+ *     (((g * (Kdim/128) + kb) * n_ct + ct) * 4 + f) * 64 + l, dword p = 0..3
+ *     of which holds weight row row0(ct, f) + l % 16, columns
+ *     128 kb + 32 p + 8 (l / 16) + j in bits 4j .. 4j + 3, j = 0..7;
+ *   w13_scales, w2_scales uint8, per such fragment (numbered as above without
+ *     l): MXFP4 [16 rows][4] bytes, byte p the scale of columns
+ *     128 kb + 32 p .. +32 ([G, 2I, H/32] and [G, H, I/32] bytes in all);
+ *     NVFP4 [2 halves h][16 rows][4] bytes, byte p the scale of columns
+ *     128 kb + 32 p + 16 h .. +16 ([G, 2I, H/16], [G, H, I/16]).
+ * Either matrix (its weights, codes and scales) may be NULL altogether.
+ * Pointers 16-byte aligned.  Runs once at load time.
+ * Requires H % 128 == 0, I % 128 == 0. */
+int moe_pack_ffn_weights_fp4(const uint16_t* w13, const uint16_t* w2, int num_groups, int H,
+                             int I, int mode, const float* w13_tensor_scale,
+                             const float* w2_tensor_scale, uint8_t* w13q, uint8_t* w13_scales,
+                             uint8_t* w2q, uint8_t* w2_scales, void* stream);
+
+/* moe_grouped_ffn with 4-bit weights (format MOE_W_MXFP4 or MOE_W_NVFP4): the
+ * same operation, segments, stage flags and errors, where every weight the
+ * products read is the value its code stands for; bf16 rows.  From a single
+ * row (the matrix-vector product, bound by the weight bytes) to prompt-sized
+ * segments.  With few rows per group the intermediate keeps 16 significant
+ * bits (two bf16 numbers), else it is rounded once to bf16 as in
+ * moe_grouped_ffn.  A DOWN-only call needs the workspace of a GATE_UP call
+ * with the same capacity, groups and segments.  Rows outside every segment
+ * are neither read nor written. */
+size_t moe_grouped_ffn_fp4_workspace_bytes(int64_t capacity, int num_groups, int H, int I);
+int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int32_t* counts,
+                        int num_groups, int H, int I, const moe_ffn_weights* weights,
+                        const float* row_scale, uint16_t* y, int64_t capacity, int flags,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                        void* stream);
+
+/* ---- the whole layer for a few tokens --------------------------------------
+ * Route, experts, weighting and combine of up to 64 tokens in three launches,
+ * with no permuted rows in between: for each token t with row_valid[t] != 0,
+ * over its chosen local experts e_k (slots as moe_route defines them, the
+ * local range as in moe_permute),
+ *   out[t] = bf16( sum_k w_k * W2[e_k] (silu(g_k) * u_k)  +  shared_t ),
+ *   g_k = W13[e_k][:I] x_t,  u_k = W13[e_k][I:] x_t,
+ * shared_t the shared expert's row for every token, padding ones included.
+ * Products, sums and weighting are float32 with one rounding to bf16 at the
+ * end (silu(g) * u keeps 16 significant bits); the sum runs over the experts
+ * in ascending order.  (The staged calls round each expert's row to bf16
+ * before the combine; this call does not, and has no row quantizers.)
+ * Repeated calls give the same bits.
+ *   logits [T, E] float32, row_valid [T] uint8 or NULL: topk_idx, topk_w
+ *     [T, K] are written, bit for bit as moe_route does;
+ *   logits NULL: topk_idx and topk_w are inputs (a router of the caller's);
+ *     a negative id is a padding slot, an id >= num_experts names no expert,
+ *     is skipped and raises MOE_DEVERR_EXPERT_RANGE; a token may name one
+ *     expert in several slots (their weights add up); row_valid still masks.
+ *   hidden [T, H], out [T, H] bf16 (out must not alias hidden)
+ *   weights  the local experts' (G = num_local_experts); shared NULL or the
+ *     shared expert's (G = 1, intermediate size shared_I, the same format;
+ *     shared_I must be 0 without it).
+ *   workspace of moe_decode_workspace_bytes(), contents on entry ignored.
+ * flags: MOE_ROUTE_RENORM.  A token without a local expert and without a
+ * shared row gets +0.  T = 0 enqueues nothing.
+ * Requires T <= 64, H % 128 == I % 128 == shared_I % 128 == 0,
+ * K <= min(num_experts, 32), num_experts <= 1024. */
+size_t moe_decode_workspace_bytes(int T, int H, int I, int K, int num_local_experts,
+                                  int shared_I);
+int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hidden, int T,
+               int H, int I, int num_experts, int K, int expert_begin, int num_local_experts,
+               int flags, int32_t* topk_idx, float* topk_w, const moe_ffn_weights* weights,
+               const moe_ffn_weights* shared, int shared_I, uint16_t* out, void* workspace,
+               size_t workspace_bytes, int32_t* dev_error, void* stream);
 
 /* ---- FP8 and FP4 fake-quant of bf16 rows -------------------------------
  * QDQ to OCP E4M3FN and back ([P1] PR summary and "How it works": the
