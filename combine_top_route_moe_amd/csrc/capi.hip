@@ -44,7 +44,7 @@ size_t grouped_ffn_fp4_workspace_bytes(int64_t, int, int);
 int launch_grouped_ffn_fp4(const uint16_t*, const int32_t*, const int32_t*, int, int, int,
                            const moe_ffn_weights*, const float*, uint16_t*, int64_t, int, void*,
                            int32_t*, hipStream_t);
-size_t decode_workspace_bytes(int, int, int, int, int);
+size_t decode_workspace_bytes(int, int, int, int, int, int);
 int launch_decode(const float*, const uint8_t*, const uint16_t*, int, int, int, int, int, int, int,
                   int, int32_t*, float*, const moe_ffn_weights*, const moe_ffn_weights*, int,
                   uint16_t*, void*, int32_t*, hipStream_t);
@@ -401,9 +401,9 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
 
 size_t moe_decode_workspace_bytes(int T, int H, int I, int K, int num_local_experts,
                                   int shared_I) {
-  (void)H;
-  if (T < 0 || I < 1 || K < 1 || num_local_experts < 1 || shared_I < 0) return 0;
-  return decode_workspace_bytes(T, I, K, num_local_experts, shared_I);
+  if (T < 0 || H < 1 || I < 1 || K < 1 || num_local_experts < 1 || shared_I < 0) return 0;
+  if (H % 128) return 0;
+  return decode_workspace_bytes(T, H, I, K, num_local_experts, shared_I);
 }
 
 int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hidden, int T,
@@ -426,7 +426,7 @@ int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hi
   if (shared && (!weights_ok(shared, MOE_FFN_ALL) || shared->format != weights->format))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(out) || hidden == out) return MOE_ERR_INVALID_ARG;
-  const size_t need = decode_workspace_bytes(T, I, K, num_local_experts, shared_I);
+  const size_t need = decode_workspace_bytes(T, H, I, K, num_local_experts, shared_I);
   if (!workspace || workspace_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   return launch_decode(logits, row_valid, hidden, T, H, I, num_experts, K, expert_begin,
                        num_local_experts, (flags & MOE_ROUTE_RENORM) ? 1 : 0, topk_idx, topk_w,

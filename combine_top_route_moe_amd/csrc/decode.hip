@@ -5,16 +5,22 @@
 //   h = W13[e_k] x_t,  a = silu(h[:I]) * h[I:],
 //   out_t = bf16( sum_k w_k W2[e_k] a  +  the shared expert's row )
 // With few tokens every product is a matrix times a handful of columns: the
-// time is that of reading the chosen experts' weights once.  So nothing is
-// permuted or written that a later launch would read back but `a`:
+// time is that of reading the chosen experts' weights once.  So no row is
+// permuted or copied; the launches are
 //   plan      (one workgroup) routes every token and lists, per expert that
 //             any token chose, its tokens in runs of at most 16 ("entries");
-//   gate_up   a workgroup owns 16 gate rows and the 16 matching up rows of
+//             for very few tokens gate_up does this itself;
+//   gate_up   a workgroup owns a tile of gate rows and the matching up rows of
 //             one entry's expert; its waves split H and add up through LDS;
-//   down      a workgroup owns 16 output columns of every token; its waves
-//             split the concatenated (entry, I) axis, each keeps all tokens'
-//             float32 sums in registers, and the waves add up through LDS in
-//             order: the combine needs no second pass and no atomics.
+//   down      a workgroup owns a tile of output columns of one entry, its waves
+//             split I; the rows go out unrounded, in float32;
+//   combine   weights and adds each token's rows in slot order, the shared
+//             expert's last, and rounds once.
+// (Down and combine in one launch were tried two ways.  A workgroup per 16
+// columns of all entries has too few workgroups to keep the memory busy: 1.6
+// TB/s at 13 tokens, 64 experts, H = 2048.  Splitting those and adding the
+// parts in the last workgroup to arrive needs a device-wide release in each:
+// writing back the L2s took 150 us at one token.)
 // The products run on the matrix cores with the weights as the A operand (16
 // weight rows) and the tokens as the B operand's 16 columns, so columns are
 // independent: a token sees its own experts only, whatever values the others
@@ -31,25 +37,24 @@ namespace moe {
 constexpr int kMaxTokens = 64;    // one bit of an expert's token mask each
 constexpr int kCols = 16;         // tokens (or rows) of an entry
 constexpr int kPlanThreads = 1024;
-constexpr int kFewWaves = 4;      // waves of a gate/up (or row-wise down) workgroup
-constexpr int kDownWaves = 8;     // waves of a down + combine workgroup
+constexpr int kGateWaves = 4;     // waves of a gate/up workgroup
+constexpr int kDownWaves = 4;     // waves of a down workgroup
+constexpr int kFusedTokens = 8;   // up to here gate/up routes by itself (and T * K <= 64, E <= 256)
 
 // A run of at most 16 tokens of one local expert.
 struct PlanEntry {
   int32_t e;       // local expert
   int32_t base;    // first compact row of the run
   int32_t cnt;     // rows of the run
-  int32_t sub;     // rows of the expert before the run
-  uint64_t mask;   // the expert's tokens
 };
 
-// The workspace: plan, then the intermediate rows (routed, then shared).
+// The workspace: plan, intermediate rows (routed, then shared), float32 rows.
 struct DecodeLayout {
-  size_t entries, row_tok, row_w, a_hi, a_lo, s_hi, s_lo, total;
+  size_t entries, row_tok, row_of, a_hi, a_lo, s_hi, s_lo, rows, s_rows, total;
   int64_t max_entries;
 };
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-static DecodeLayout decode_layout(int T, int I, int K, int El, int sI) {
+static DecodeLayout decode_layout(int T, int H, int I, int K, int El, int sI) {
   DecodeLayout L;
   const int64_t rows = (int64_t)T * K;
   L.max_entries = std::min<int64_t>(El, rows) + rows / kCols;
@@ -61,65 +66,204 @@ static DecodeLayout decode_layout(int T, int I, int K, int El, int sI) {
   };
   L.entries = put((size_t)L.max_entries * sizeof(PlanEntry));
   L.row_tok = put((size_t)rows * 4);
-  L.row_w = put((size_t)rows * 4);
+  L.row_of = put((size_t)rows * 4);
   L.a_hi = put((size_t)rows * I * 2);
   L.a_lo = put((size_t)rows * I * 2);
   L.s_hi = put((size_t)T * sI * 2);
   L.s_lo = put((size_t)T * sI * 2);
+  L.rows = put((size_t)rows * H * 4);
+  L.s_rows = put(sI ? (size_t)T * H * 4 : 0);
   L.total = o;
   return L;
 }
 
-size_t decode_workspace_bytes(int T, int I, int K, int El, int sI) {
-  return decode_layout(T, I, K, El, sI).total;
+size_t decode_workspace_bytes(int T, int H, int I, int K, int El, int sI) {
+  return decode_layout(T, H, I, K, El, sI).total;
+}
+
+// ---- top-k selection ----------------------------------------------------------
+// A logit as a signed integer in the same order (NaN as -inf, -0 as +0), and
+// back; every real logit lies above the integer minimum, which stands for "no
+// expert".
+__device__ __forceinline__ int order_key(float x) {
+  const int b = __float_as_int(rank_value(x) + 0.0f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_value(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+constexpr int kNoKey = (int)0x80000000;
+
+// Wave-wide integer maximum, uniform: register moves within 16 lanes, then
+// the four rows' maxima in scalar registers.
+__device__ __forceinline__ int wave_max_i32(int v) {
+  v = max(v, row16_dpp<0xB1>(v));
+  v = max(v, row16_dpp<0x4E>(v));
+  v = max(v, row16_dpp<0x141>(v));
+  v = max(v, row16_dpp<0x140>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
+// Keys of one token's logits, experts lane, lane + 64, .. (EPL a lane).
+template <int EPL>
+__device__ __forceinline__ void load_keys(const float* __restrict__ row, int E, int lane,
+                                          int* key) {
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int x = lane + j * kWave;
+    key[j] = x < E ? order_key(row[x]) : kNoKey;
+  }
+}
+
+// One token's K best experts by one wave (every lane active), the same choice
+// and order as route_row: lane k < K gets slot k's expert in sel_e and its
+// logit in sel_v.  Each lane first sorts its keys, so that a round compares
+// one head per lane: the wave maximum, the lanes that hold it (one, but for
+// ties), and the winner drops its head.  A round is about 15 instructions,
+// a fifth of route_row's (one workgroup's plan of 64 tokens, 64 experts: 17 ->
+// 9 us); sorting pays while a lane holds few experts.
+template <int EPL>
+__device__ __forceinline__ void select_topk(const int* key, int K, int lane, int& sel_e,
+                                            float& sel_v) {
+  int h[EPL], e[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    h[j] = key[j];
+    e[j] = lane + j * kWave;
+  }
+#pragma unroll
+  for (int i = 1; i < EPL; ++i)               // stable: equal keys keep the lower index first
+#pragma unroll
+    for (int j = EPL - 1; j >= i; --j) {
+      const bool sw = h[j] > h[j - 1] || (h[j] == h[j - 1] && e[j] < e[j - 1]);
+      const int a = h[j - 1], b = e[j - 1];
+      h[j - 1] = sw ? h[j] : a;
+      e[j - 1] = sw ? e[j] : b;
+      h[j] = sw ? a : h[j];
+      e[j] = sw ? b : e[j];
+    }
+  int best = kNoKey;
+  sel_e = -1;
+  for (int k = 0; k < K; ++k) {
+    const int mv = wave_max_i32(h[0]);
+    uint64_t at = __ballot(h[0] == mv);
+    int win = __builtin_amdgcn_readlane(e[0], __ffsll((unsigned long long)at) - 1);
+    for (at &= at - 1; at; at &= at - 1)      // ties: the lowest index
+      win = min(win, __builtin_amdgcn_readlane(e[0], __ffsll((unsigned long long)at) - 1));
+    sel_e = lane == k ? win : sel_e;
+    best = lane == k ? mv : best;
+    const bool mine = (win & 63) == lane;
+#pragma unroll
+    for (int j = 0; j + 1 < EPL; ++j) {
+      h[j] = mine ? h[j + 1] : h[j];
+      e[j] = mine ? e[j + 1] : e[j];
+    }
+    h[EPL - 1] = mine ? kNoKey : h[EPL - 1];
+  }
+  sel_v = key_value(best);
+}
+
+// The selected experts' weights (lane k < K: slot k's), as route_row's.
+template <int EPL>
+__device__ __forceinline__ float topk_weight(const int* key, int E, int K, int renorm, int lane,
+                                             float sel_v) {
+  const float lmax = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sel_v), 0));
+  double num = 0.0;
+  if (lane < K) num = weight_term(sel_v, lmax);
+  double den = 0.0;
+  if (renorm) {
+    den = sum_lanes_below(num, K);
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + j * kWave < E) den += weight_term(key_value(key[j]), lmax);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) den += __shfl_xor(den, off, kWave);
+  }
+  return (float)(num / den);
 }
 
 // ---- plan -------------------------------------------------------------------
 // One workgroup.  EPL 0: the routes are given (topk_idx, topk_w are inputs),
-// else experts per lane of the top-k selection.
+// else experts per lane of the top-k selection.  A wave selects for one token
+// after another; the weights' exponentials (double, as moe_route's) are then
+// taken by one thread per slot, not by a few lanes of each token's wave.
+struct DecodePlan {
+  int32_t* n_entries;
+  PlanEntry* entries;
+  int32_t* row_tok;   // token of a compact row
+  int32_t* row_of;    // compact row of a slot, -1: no local expert
+};
+
 template <int EPL>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
     const float* __restrict__ logits, const uint8_t* __restrict__ row_valid, int T, int E, int K,
     int renorm, int expert_begin, int El, int32_t* __restrict__ topk_idx,
-    float* __restrict__ topk_w, int32_t* __restrict__ n_entries, PlanEntry* __restrict__ entries,
-    int32_t* __restrict__ row_tok, float* __restrict__ row_w, int32_t* __restrict__ dev_error) {
+    float* __restrict__ topk_w, DecodePlan plan, int32_t* __restrict__ dev_error) {
+  constexpr bool kSort = EPL > 0 && EPL <= 4;
   __shared__ uint32_t mask[1024][2];
   __shared__ int sel_e[kMaxTokens * 32];
-  __shared__ float sel_w[kMaxTokens * 32];
+  __shared__ float sel_v[kSort ? kMaxTokens * 32 : 1];
+  __shared__ double term[kSort ? kMaxTokens * 32 : 1];
   __shared__ int base_of[1024];
   __shared__ int wave_sum[kPlanThreads / kWave];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  constexpr int kWaves = kPlanThreads / kWave;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   mask[tid][0] = 0u;
   mask[tid][1] = 0u;
   __syncthreads();
-  for (int t = wv; t < T; t += kPlanThreads / kWave) {
+  constexpr int kV = kSort ? EPL : 1;
+  int nv[kV];
+  if constexpr (kSort) {
+    if (wv < T) load_keys<EPL>(logits + (int64_t)wv * E, E, lane, nv);
+  }
+  for (int t = wv; t < T; t += kWaves) {
     const bool real = !row_valid || row_valid[t];
+    const int slot = t * K + lane;
     int e = -1;
-    float w = 0.0f;
-    if constexpr (EPL > 0) {
-      if (real) route_row<EPL>(logits + (int64_t)t * E, E, K, renorm, lane, e, w);
-      if (!real) {
-        e = -1;
-        w = 0.0f;
+    if constexpr (kSort) {
+      int v[kV];
+      float sv = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[j] = nv[j];
+      if (t + kWaves < T) load_keys<EPL>(logits + (int64_t)(t + kWaves) * E, E, lane, nv);
+      if (real) {
+        select_topk<EPL>(v, K, lane, e, sv);
+        if (!renorm) {
+          const float w = topk_weight<EPL>(v, E, K, renorm, lane, sv);
+          if (lane < K) topk_w[slot] = w;
+        }
       }
       if (lane < K) {
-        topk_idx[(int64_t)t * K + lane] = e;
-        topk_w[(int64_t)t * K + lane] = w;
+        topk_idx[slot] = e;
+        sel_v[slot] = sv;
+      }
+    } else if constexpr (EPL > 0) {
+      float w = 0.0f;
+      if (real) route_row<EPL>(logits + (int64_t)t * E, E, K, renorm, lane, e, w);
+      if (lane < K) {
+        topk_idx[slot] = e;
+        topk_w[slot] = w;
       }
     } else if (lane < K && real) {
-      e = topk_idx[(int64_t)t * K + lane];
-      w = topk_w[(int64_t)t * K + lane];
+      e = topk_idx[slot];
       if (e >= E) raise_error(dev_error, MOE_DEVERR_EXPERT_RANGE);
     }
     if (lane < K) {
       const bool here = e >= expert_begin && e < E && e - expert_begin < El;
       const int le = here ? e - expert_begin : -1;
-      sel_e[t * K + lane] = le;
-      sel_w[t * K + lane] = w;
+      // -2: no expert at all (a masked token's weight is 0)
+      sel_e[slot] = here ? le : e < 0 ? -2 : -1;
       if (here) atomicOr(&mask[le][t >> 5], 1u << (t & 31));
     }
   }
   __syncthreads();
+  if constexpr (kSort) {
+    for (int i = tid; i < T * K; i += kPlanThreads)
+      term[i] = weight_term(sel_v[i], sel_v[i / K * K]);
+  }
   // entries and compact rows before each expert: one scan of (entries, rows)
   // packed in one word (both totals stay below 2^15)
   const uint64_t m = (uint64_t)mask[tid][1] << 32 | mask[tid][0];
@@ -134,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   __syncthreads();
   int before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < kPlanThreads / kWave; ++i) {
+  for (int i = 0; i < kWaves; ++i) {
     if (i < wv) before += wave_sum[i];
     total += wave_sum[i];
   }
@@ -142,38 +286,43 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   const int ent0 = excl >> 16, base = excl & 0xffff;
   base_of[tid] = base;
   for (int v = 0; v < ne; ++v)
-    entries[ent0 + v] = PlanEntry{tid, base + v * kCols, min(kCols, c - v * kCols), v * kCols, m};
-  if (tid == 0) *n_entries = total >> 16;
+    plan.entries[ent0 + v] = PlanEntry{tid, base + v * kCols, min(kCols, c - v * kCols)};
+  if (tid == 0) *plan.n_entries = total >> 16;
   __syncthreads();
-  // each (token, expert) pair's compact row; a token that names one expert in
-  // several slots has one row there, with the slots' weights added
+  // each slot's compact row: a (token, expert) pair has one, also where the
+  // token names the expert in several slots
   for (int i = tid; i < T * K; i += kPlanThreads) {
-    const int e = sel_e[i];
-    if (e < 0) continue;
-    const int t = i / K;
-    float w = 0.0f;
-    bool first = true;
-    for (int j = t * K; j < (t + 1) * K; ++j)
-      if (sel_e[j] == e) {
-        first = first && j >= i;
-        w += sel_w[j];
+    const int e = sel_e[i], t = i / K;
+    if constexpr (kSort) {
+      if (renorm) {
+        double den = 0.0;
+        for (int j = t * K; j < (t + 1) * K; ++j) den += term[j];   // slot order
+        topk_w[i] = e == -2 ? 0.0f : (float)(term[i] / den);
+      } else if (e == -2) {
+        topk_w[i] = 0.0f;
       }
-    if (!first) continue;
-    const uint64_t em = (uint64_t)mask[e][1] << 32 | mask[e][0];
-    const int pos = base_of[e] + __popcll(em & ((1ull << t) - 1));
-    row_tok[pos] = t;
-    row_w[pos] = w;
+    }
+    int pos = -1;
+    if (e >= 0) {
+      const uint64_t em = (uint64_t)mask[e][1] << 32 | mask[e][0];
+      pos = base_of[e] + __popcll(em & ((1ull << t) - 1));
+      plan.row_tok[pos] = t;
+    }
+    plan.row_of[i] = pos;
   }
 }
 
 // ---- the streamed product ---------------------------------------------------
-// acc[f] += W_f[16 rows, blocks kb0, kb0 + step, ..] * B^T for NF weight
-// fragments and one 16-column B given as NB bf16 addends (b[i] is the lane's
-// column at its first element).  D blocks are in flight per wave; the loop
-// that refills is free of branches, so that each wait covers one block only.
-template <int FMT, int NF, int NB, int D>
-__device__ __forceinline__ void few_stream(const WStream<FMT>* ws, const uint16_t* const* b,
-                                           int kb0, int step, int nkb, f32x4_t* acc) {
+// acc[i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * B^T for NF weight
+// fragments of one column tile and one 16-column B given as NB bf16 addends
+// (buffers b[a], boff the lane's byte offset of its column's first element).
+// GU: the first half of the fragments are gate rows, the others the matching
+// up rows, two fragments on.  D blocks are in flight per wave; the loop that
+// refills is free of branches, so that each wait covers one block only.
+template <int FMT, int NF, int NB, int D, bool GU>
+__device__ __forceinline__ void few_stream(const WStream<FMT>& ws, const buffer_t* b,
+                                           uint32_t boff, int kb0, int step, int nkb,
+                                           f32x4_t* acc) {
   struct Buf {
     typename WStream<FMT>::Block w[NF];
     u32x4_t x[NB][4];
@@ -183,12 +332,15 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>* ws, const uint16_
   auto load = [&](Buf& t, int i) {
     const int kb = kb0 + i * step;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) ws[f].load(t.w[f], kb);
+    for (int f = 0; f < NF; ++f) {
+      const bool up = GU && f >= NF / 2;
+      ws.load(t.w[f], kb, up ? f - NF / 2 + 2 : f, up);
+    }
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
       for (int p = 0; p < 4; ++p)
-        t.x[a][p] = *reinterpret_cast<const u32x4_t*>(b[a] + kb * 128 + p * 32);
+        t.x[a][p] = load_b128<false>(b[a], boff + p * 64, kb * 256);
   };
   auto use = [&](const Buf& t) {
 #pragma unroll
@@ -223,12 +375,16 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>* ws, const uint16_
     if (i + D + d < n) use(buf[d]);
 }
 
-// Blocks in flight per wave, by the block's registers (two fragments of bf16
-// weights are 32 registers a block, of 4-bit ones 10).
+// The gate/up tile and its stream, by format: NF fragments a wave (half gate,
+// half up) and D blocks in flight.  bf16 blocks are large (4 KB a fragment):
+// 2 fragments, so that registers leave four waves to a SIMD; the narrower
+// formats take a whole 64-row column tile, which reads each row of x for four
+// fragments instead of two.
 template <int FMT>
-constexpr int few_depth() {
-  return FMT == MOE_W_BF16 ? 2 : FMT == MOE_W_FP8 ? 2 : 3;
-}
+struct GateShape {
+  static constexpr int NF = FMT == MOE_W_BF16 || FMT == MOE_W_FP8 ? 2 : 4;
+  static constexpr int D = 2;
+};
 
 // v as the sum of two bf16 numbers, high part first
 __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
@@ -236,293 +392,355 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) 
   lo = f32_to_bf16(v - bf16_to_f32(hi));
 }
 
-// One workgroup's gate/up tile: rows 16 rt .. of the gate half and of the up
-// half of expert g, for the cnt <= 16 rows whose x this lane's column is
-// xcol (columns past cnt repeat the last one and are not stored).  a rows
-// go to hi / lo + column * I.
+// One workgroup's gate/up tile: 8 NF intermediate columns, nt of expert g, for
+// the cnt <= 16 rows whose x this lane's column is at byte xoff of x (columns
+// past cnt repeat the last one and are not stored).  a rows go to hi / lo +
+// column * I.
 template <int FMT, int NW>
-__device__ __forceinline__ void few_gate_up(const WMat& W, int g, int rt, int H, int I,
-                                            const uint16_t* xcol, int cnt, uint16_t* hi,
-                                            uint16_t* lo, f32x4_t (*red)[2][kWave]) {
+__device__ __forceinline__ void few_gate_up(const WMat& W, int g, int nt, int H, int I,
+                                            buffer_t x, uint32_t xoff, int cnt,
+                                            uint16_t* hi, uint16_t* lo,
+                                            f32x4_t (*red)[GateShape<FMT>::NF][kWave]) {
+  constexpr int NF = GateShape<FMT>::NF, NH = NF / 2;   // NH gate and NH up fragments
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nkb = H / 128, ct = rt >> 1, f = rt & 1;
-  WStream<FMT> ws[2];
-  ws[0].init(W, g, ct, f, I / 32, nkb, 16 * rt, lane);
-  ws[1].init(W, g, ct, f + 2, I / 32, nkb, I + 16 * rt, lane);
-  f32x4_t acc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
-  const uint16_t* b[1] = {xcol + 8 * (lane >> 4)};
-  few_stream<FMT, 2, 1, few_depth<FMT>()>(ws, b, w, NW, nkb, acc);
-  red[w][0][lane] = acc[0];
-  red[w][1][lane] = acc[1];
+  const int nkb = H / 128, ct = nt * NH / 2, f0 = nt * NH % 2;
+  WStream<FMT> ws;
+  ws.init(W, g, ct, f0, I / 32, nkb, 32 * ct, I + 32 * ct, lane);
+  f32x4_t acc[NF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  few_stream<FMT, NF, 1, GateShape<FMT>::D, true>(ws, &x, xoff + 16 * (lane >> 4), w, NW, nkb, acc);
+#pragma unroll
+  for (int i = 0; i < NF; ++i) red[w][i][lane] = acc[i];
   __syncthreads();
-  if (w != 0) return;
-  f32x4_t gt = red[0][0][lane], up = red[0][1][lane];
+  if (w >= NH) return;
+  f32x4_t gt = red[0][w][lane], up = red[0][NH + w][lane];
 #pragma unroll
   for (int i = 1; i < NW; ++i) {
-    gt += red[i][0][lane];
-    up += red[i][1][lane];
+    gt += red[i][w][lane];
+    up += red[i][NH + w][lane];
   }
-  // lane holds rows 4 (l / 16) .. +4 of the tile for column l % 16
+  // lane holds rows 4 (l / 16) .. +4 of the fragment for column l % 16
   const int col = lane & 15;
   if (col >= cnt) return;
   uint32_t h[4], l[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) split_bf16(silu_f(gt[q]) * up[q], h[q], l[q]);
-  const int64_t o = (int64_t)col * I + rt * 16 + 4 * (lane >> 4);
+  const int64_t o = (int64_t)col * I + 32 * ct + 16 * (f0 + w) + 4 * (lane >> 4);
   *reinterpret_cast<uint2*>(hi + o) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   *reinterpret_cast<uint2*>(lo + o) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
+// ---- the plan of a few routed tokens, by every wave on its own ------------------
+// Lane i stands for slot i = t K + k < 64 and knows its local expert (-1: none).
+// Entries are the experts in the order of their first slots.
+struct SmallPlan {
+  uint64_t same;      // slots of this lane's expert
+  uint64_t leaders;   // first slots of the experts
+  int base;           // for a leader: compact rows of the experts before its own
+};
+__device__ __forceinline__ SmallPlan small_plan(int e, int n_slots, int T, int lane) {
+  SmallPlan p;
+  p.same = 1ull << lane;
+  if (T > 1) {
+    for (int s = 0; s < n_slots; ++s) {
+      const uint64_t b = __ballot(e == __builtin_amdgcn_readlane(e, s));
+      if (lane == s) p.same = b;
+    }
+  }
+  const bool leader = e >= 0 && !(p.same & ((1ull << lane) - 1));
+  p.leaders = __ballot(leader);
+  const int c = leader ? __popcll(p.same) : 0;
+  int incl = c;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(incl, off, kWave);
+    if (lane >= off) incl += y;
+  }
+  p.base = incl - c;
+  return p;
+}
+
 // ---- moe_decode: gate/up ------------------------------------------------------
 // Blocks [0, shared_blocks): the shared expert's tiles, 16 tokens a run; then
-// (entry, tile), the entries past the plan's leaving at once.
-template <int FMT, int NW>
+// (entry, tile), the entries past the plan's leaving at once.  EPL > 0: no plan
+// was made; every workgroup routes the (few) tokens itself, and one more at the
+// end of the grid writes the plan for the down kernel.  That saves a launch,
+// 5 us, and costs each workgroup about 1.
+template <int FMT, int NW, int EPL>
 __global__ void __launch_bounds__(NW * kWave, 4) decode_gate_up_kernel(
     const uint16_t* __restrict__ x, int T, int H, int I, WMat routed, WMat shared, int sI,
-    int shared_blocks, const int32_t* __restrict__ n_entries,
-    const PlanEntry* __restrict__ entries, const int32_t* __restrict__ row_tok,
-    uint16_t* __restrict__ a_hi, uint16_t* __restrict__ a_lo, uint16_t* __restrict__ s_hi,
-    uint16_t* __restrict__ s_lo) {
-  __shared__ f32x4_t red[NW][2][kWave];
-  const int col = threadIdx.x & 15;
+    int shared_blocks, DecodePlan plan, uint16_t* __restrict__ a_hi, uint16_t* __restrict__ a_lo,
+    uint16_t* __restrict__ s_hi, uint16_t* __restrict__ s_lo, const float* __restrict__ logits,
+    const uint8_t* __restrict__ row_valid, int E, int K, int renorm, int expert_begin, int El,
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+  constexpr int kTile = 8 * GateShape<FMT>::NF;   // intermediate columns of a workgroup
+  __shared__ f32x4_t red[NW][GateShape<FMT>::NF][kWave];
+  __shared__ int sel[64];
+  const int lane = threadIdx.x & 63, col = lane & 15;
+  const buffer_t xbuf = uniform_buffer(x, (int64_t)T * H * 2);
   int b = blockIdx.x;
   if (b < shared_blocks) {
-    const int nt = sI / 16, v = b / nt;
+    const int nt = sI / kTile, v = b / nt;
     const int t0 = v * kCols, cnt = min(kCols, T - t0);
-    const uint16_t* xc = x + (int64_t)(t0 + min(col, cnt - 1)) * H;
-    few_gate_up<FMT, NW>(shared, 0, b - v * nt, H, sI, xc, cnt, s_hi + (int64_t)t0 * sI,
+    few_gate_up<FMT, NW>(shared, 0, b - v * nt, H, sI, xbuf,
+                         (uint32_t)(t0 + min(col, cnt - 1)) * H * 2u, cnt, s_hi + (int64_t)t0 * sI,
                          s_lo + (int64_t)t0 * sI, red);
     return;
   }
   b -= shared_blocks;
-  const int nt = I / 16, j = b / nt;
-  if (j >= *n_entries) return;
-  const int base = entries[j].base, cnt = entries[j].cnt;
-  const uint16_t* xc = x + (int64_t)row_tok[base + min(col, cnt - 1)] * H;
-  few_gate_up<FMT, NW>(routed, entries[j].e, b - j * nt, H, I, xc, cnt, a_hi + (int64_t)base * I,
-                       a_lo + (int64_t)base * I, red);
+  const int nt = I / kTile, j = b / nt;
+  int g, base, cnt, tok = 0;
+  if constexpr (EPL > 0) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool writer = blockIdx.x == gridDim.x - 1;
+    for (int t = w; t < T; t += NW) {
+      int e = -1;
+      int v[EPL];
+      float sv = 0.0f, wt = 0.0f;
+      if (!row_valid || row_valid[t]) {
+        load_keys<EPL>(logits + (int64_t)t * E, E, lane, v);
+        select_topk<EPL>(v, K, lane, e, sv);
+        if (writer) wt = topk_weight<EPL>(v, E, K, renorm, lane, sv);
+      }
+      if (lane < K) {
+        if (writer) {
+          topk_idx[t * K + lane] = e;
+          topk_w[t * K + lane] = wt;
+        }
+        sel[t * K + lane] = e >= expert_begin && e - expert_begin < El ? e - expert_begin : -1;
+      }
+    }
+    __syncthreads();
+    const int e = lane < T * K ? sel[lane] : -1;
+    const SmallPlan p = small_plan(e, T * K, T, lane);
+    const int n = __popcll(p.leaders);
+    if (writer) {
+      if (w != 0) return;
+      if (lane == 0) *plan.n_entries = n;
+      const int lead = __ffsll((unsigned long long)p.same) - 1;
+      const int pos = __shfl(p.base, lead, kWave) + __popcll(p.same & ((1ull << lane) - 1));
+      if (lane < T * K) plan.row_of[lane] = e >= 0 ? pos : -1;
+      if (e >= 0) {
+        plan.row_tok[pos] = lane / K;
+        if (lead == lane)
+          plan.entries[__popcll(p.leaders & ((1ull << lane) - 1))] =
+              PlanEntry{e, p.base, (int)__popcll(p.same)};
+      }
+      return;
+    }
+    if (j >= n) return;
+    const bool it = ((p.leaders >> lane) & 1) && __popcll(p.leaders & ((1ull << lane) - 1)) == j;
+    const int src = __ffsll((unsigned long long)__ballot(it)) - 1;
+    g = __builtin_amdgcn_readlane(e, src);
+    base = __builtin_amdgcn_readlane(p.base, src);
+    uint64_t m = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(p.same >> 32), src) << 32 |
+                 (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)p.same, src);
+    cnt = __popcll(m);
+    for (int c = 0; m; m &= m - 1, ++c)   // columns past the last repeat it
+      if (col >= c) tok = (__ffsll((unsigned long long)m) - 1) / K;
+  } else {
+    if (j >= *plan.n_entries) return;
+    g = plan.entries[j].e;
+    base = plan.entries[j].base;
+    cnt = plan.entries[j].cnt;
+    tok = plan.row_tok[base + min(col, cnt - 1)];
+  }
+  few_gate_up<FMT, NW>(routed, g, b - j * nt, H, I, xbuf, (uint32_t)tok * H * 2u, cnt,
+                       a_hi + (int64_t)base * I, a_lo + (int64_t)base * I, red);
 }
 
-// ---- moe_decode: down + combine -----------------------------------------------
-// A workgroup owns output columns 16 rt .. +16 of all T tokens.  The blocks
-// of 128 intermediate columns of all entries (the shared expert's runs last)
-// form one axis, which the waves split evenly; a wave keeps every token's sum
-// over its stretch in registers: per entry an accumulator over compact rows,
-// which at the end of the entry is weighted and moved to the tokens' lanes.
-// TS: token subtiles of 16.
-template <int FMT, int TS, int NW>
-__global__ void __launch_bounds__(NW * kWave, 2) decode_down_kernel(
-    int T, int H, int I, WMat routed, WMat shared, int sI, int shared_runs,
-    const int32_t* __restrict__ n_entries, const PlanEntry* __restrict__ entries,
-    const float* __restrict__ row_w, const uint16_t* __restrict__ a_hi,
-    const uint16_t* __restrict__ a_lo, const uint16_t* __restrict__ s_hi,
-    const uint16_t* __restrict__ s_lo, uint16_t* __restrict__ out) {
-  constexpr int D = 2;
-  __shared__ f32x4_t red[NW][TS][kWave];
-  const int lane = threadIdx.x & 63, col = lane & 15, q8 = 8 * (lane >> 4);
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rt = blockIdx.x, ct = rt >> 2, f = rt & 3, n_ct = H / 64;
-  const int nb = I / 128, nbs = sI / 128;
-  const int n = *n_entries;
-  const int nr = n * nb, total = nr + shared_runs * nbs;
-  const int b0 = (int)((int64_t)total * w / NW), b1 = (int)((int64_t)total * (w + 1) / NW);
-  f32x4_t tok[TS];
-#pragma unroll
-  for (int s = 0; s < TS; ++s) tok[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+// ---- down ---------------------------------------------------------------------
+// 16-column fragments of a down tile, by format (bf16 blocks are large)
+template <int FMT>
+constexpr int down_frags() {
+  return FMT == MOE_W_BF16 ? 2 : 4;
+}
 
-  struct Buf {
-    typename WStream<FMT>::Block w;
-    u32x4_t hi[4], lo[4];
-    float rw;
-  } buf[D];
-  // a position on the axis: entry (or shared run) and block within it
-  struct Cursor {
-    int j, kb;
-  };
-  auto at = [&](int b) -> Cursor {
-    if (b < nr) return {b / nb, b % nb};
-    const int r = b - nr;
-    return {n + r / max(nbs, 1), r % max(nbs, 1)};
-  };
-  auto next = [&](Cursor& c) {
-    ++c.kb;
-    if (c.kb == (c.j < n ? nb : nbs)) {
-      c.kb = 0;
-      ++c.j;
-    }
-  };
-  auto load = [&](Buf& t, const Cursor& c) {
-    const int j = __builtin_amdgcn_readfirstlane(c.j), kb = __builtin_amdgcn_readfirstlane(c.kb);
-    const bool sh = j >= n;
-    const int jj = sh ? 0 : j;   // n may be 0
-    const int t0 = (j - n) * kCols;
-    const int base = sh ? t0 : entries[jj].base;
-    const int cnt = sh ? min(kCols, T - t0) : entries[jj].cnt;
-    const int g = sh ? 0 : entries[jj].e;
-    const int Ic = sh ? sI : I;
-    const WMat m = sh ? shared : routed;
-    WStream<FMT> ws;
-    ws.init(m, g, ct, f, n_ct, Ic / 128, 16 * rt, lane);
-    ws.load(t.w, kb);
-    const int row = base + min(col, cnt - 1);
-    const int64_t o = (int64_t)row * Ic + q8 + kb * 128;
-    const uint16_t* ph = (sh ? s_hi : a_hi) + o;
-    const uint16_t* pl = (sh ? s_lo : a_lo) + o;
+// One workgroup's down tile: 16 NF output columns of the cnt <= 16 rows of a
+// (high and low parts, row stride I), for expert g; store(fragment's first
+// column, row, four columns' sums) for every row.
+template <int FMT, int NW, typename Store>
+__device__ __forceinline__ void few_down(const WMat& W, int g, int tile, int H, int I,
+                                         const uint16_t* hi, const uint16_t* lo, int cnt,
+                                         f32x4_t (*red)[down_frags<FMT>()][kWave], Store store) {
+  constexpr int NF = down_frags<FMT>();
+  const int lane = threadIdx.x & 63, col = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WStream<FMT> ws;
+  ws.init(W, g, tile * NF / 4, tile * NF % 4, H / 64, I / 128, 16 * NF * tile, 0, lane);
+  f32x4_t acc[NF];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      t.hi[p] = *reinterpret_cast<const u32x4_t*>(ph + p * 32);
-      t.lo[p] = *reinterpret_cast<const u32x4_t*>(pl + p * 32);
-    }
-    const float rw = row_w[sh ? 0 : row];   // the load itself unconditional: no branch here
-    t.rw = sh ? 1.0f : rw;
-  };
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  Cursor cu = at(b0), cl = cu;
-  auto use = [&](const Buf& t, bool last) {
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t bytes = (int64_t)cnt * I * 2;
+  const buffer_t b[2] = {uniform_buffer(hi, bytes), uniform_buffer(lo, bytes)};
+  const uint32_t boff = (uint32_t)(min(col, cnt - 1) * I + 8 * (lane >> 4)) * 2u;
+  few_stream<FMT, NF, 2, 2, false>(ws, b, boff, w, NW, I / 128, acc);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const bf16x8_t wf = t.w.operand(p);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, t.hi[p]), acc,
-                                                    0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, t.lo[p]), acc,
-                                                    0, 0, 0);
-    }
-    const int j = __builtin_amdgcn_readfirstlane(cu.j);
-    next(cu);
-    if (last || cu.kb == 0) {   // the entry (or the wave's part of it) is done
-      const bool sh = j >= n;
-      const int jj = sh ? 0 : j;
-      const int sub = sh ? (j - n) * kCols : entries[jj].sub;
-      const uint64_t mask = sh ? ~0ull : entries[jj].mask;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q] *= t.rw;
-#pragma unroll
-      for (int s = 0; s < TS; ++s) {
-        const int tk = 16 * s + col;   // this lane's token
-        const int i = __popcll(mask & ((1ull << tk) - 1)) - sub;
-        const bool mine = ((mask >> tk) & 1) && i >= 0 && i < kCols;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float v = __shfl(acc[q], (lane & 48) | (i & 15), kWave);
-          tok[s][q] += mine ? v : 0.0f;
-        }
-      }
-      acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  const int cntb = b1 - b0;
-  if (cntb > 0) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      load(buf[d], cl);
-      if (d + 1 < cntb) next(cl);   // past the end: the last block again
-    }
-    int i = 0;
-    for (; i + 2 * D <= cntb; i += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        use(buf[d], false);
-        load(buf[d], cl);
-        if (i + d + D + 1 < cntb) next(cl);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (i + d < cntb) {
-        use(buf[d], i + d + 1 == cntb);
-        if (i + d + D < cntb) {
-          load(buf[d], cl);
-          if (i + d + D + 1 < cntb) next(cl);
-        }
-      }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (i + D + d < cntb) use(buf[d], i + D + d + 1 == cntb);
-  }
-#pragma unroll
-  for (int s = 0; s < TS; ++s) red[w][s][lane] = tok[s];
+  for (int f = 0; f < NF; ++f) red[w][f][lane] = acc[f];
   __syncthreads();
-  if (w >= TS) return;
-  f32x4_t v = red[0][w][lane];
+  for (int f = w; f < NF; f += NW) {
+    f32x4_t v = red[0][f][lane];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) v += red[i][w][lane];
-  const int t = 16 * w + col;
-  if (t >= T) return;
-  *reinterpret_cast<uint2*>(out + (int64_t)t * H + rt * 16 + 4 * (lane >> 4)) =
-      make_uint2(f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16,
-                 f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16);
+    for (int i = 1; i < NW; ++i) v += red[i][f][lane];
+    if (col < cnt) store(16 * (tile * NF + f) + 4 * (lane >> 4), col, v);
+  }
+}
+
+// moe_decode: the rows go out in float32, unweighted; blocks as in gate/up.
+template <int FMT, int NW>
+__global__ void __launch_bounds__(NW * kWave, 2) decode_down_kernel(
+    int T, int H, int I, WMat routed, WMat shared, int sI, int shared_blocks, DecodePlan plan,
+    const uint16_t* __restrict__ a_hi, const uint16_t* __restrict__ a_lo,
+    const uint16_t* __restrict__ s_hi, const uint16_t* __restrict__ s_lo, float* __restrict__ rows,
+    float* __restrict__ s_rows) {
+  __shared__ f32x4_t red[NW][down_frags<FMT>()][kWave];
+  const int nt = H / (16 * down_frags<FMT>());
+  int b = blockIdx.x;
+  if (b < shared_blocks) {
+    const int v = b / nt, t0 = v * kCols;
+    float* r = s_rows + (int64_t)t0 * H;
+    few_down<FMT, NW>(shared, 0, b - v * nt, H, sI, s_hi + (int64_t)t0 * sI,
+                      s_lo + (int64_t)t0 * sI, min(kCols, T - t0), red,
+                      [&](int c, int row, f32x4_t v4) {
+                        *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v4;
+                      });
+    return;
+  }
+  b -= shared_blocks;
+  const int j = b / nt;
+  if (j >= *plan.n_entries) return;
+  const int base = plan.entries[j].base;
+  float* r = rows + (int64_t)base * H;
+  few_down<FMT, NW>(routed, plan.entries[j].e, b - j * nt, H, I, a_hi + (int64_t)base * I,
+                    a_lo + (int64_t)base * I, plan.entries[j].cnt, red,
+                    [&](int c, int row, f32x4_t v4) {
+                      *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v4;
+                    });
+}
+
+// ---- moe_decode: combine --------------------------------------------------------
+// out[t] = bf16( sum over the slots in order of w * row, then the shared row ):
+// one thread per 4 columns of a token, 64-thread workgroups.
+__global__ void __launch_bounds__(64) decode_combine_kernel(
+    int H, int K, const int32_t* __restrict__ row_of, const float* __restrict__ topk_w,
+    const float* __restrict__ rows, const float* __restrict__ s_rows, uint16_t* __restrict__ out) {
+  const int t = blockIdx.y, c = (blockIdx.x * 64 + threadIdx.x) * 4;
+  if (c >= H) return;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  // 8 slots' rows in flight together; slots without a row read row 0 and drop it
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    int r[8];
+    float w[8];
+    f32x4_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = t * K + min(k0 + i, K - 1);
+      r[i] = k0 + i < K ? row_of[at] : -1;
+      w[i] = topk_w[at];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const f32x4_t*>(rows + (int64_t)max(r[i], 0) * H + c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r[i] < 0) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] += w[i] * v[i][q];
+    }
+  }
+  if (s_rows) acc += *reinterpret_cast<const f32x4_t*>(s_rows + (int64_t)t * H + c);
+  *reinterpret_cast<uint2*>(out + (int64_t)t * H + c) =
+      make_uint2(f32_to_bf16(acc[0]) | f32_to_bf16(acc[1]) << 16,
+                 f32_to_bf16(acc[2]) | f32_to_bf16(acc[3]) << 16);
+}
+
+// What launch_decode hands on, with the workspace laid out.
+struct DecodeArgs {
+  const float* logits;
+  const uint8_t* row_valid;
+  const uint16_t* x;
+  int T, H, I, E, K, expert_begin, El, renorm, sI;
+  int32_t* topk_idx;
+  float* topk_w;
+  WMat r13, r2, s13, s2;
+  uint16_t* out;
+  DecodeLayout L;
+  char* ws;
+};
+
+static DecodePlan plan_of(const DecodeArgs& d) {
+  return {reinterpret_cast<int32_t*>(d.ws), reinterpret_cast<PlanEntry*>(d.ws + d.L.entries),
+          reinterpret_cast<int32_t*>(d.ws + d.L.row_tok),
+          reinterpret_cast<int32_t*>(d.ws + d.L.row_of)};
 }
 
 template <int FMT>
-static void launch_decode_ffn(const uint16_t* x, int T, int H, int I, int K, const WMat* r13,
-                              const WMat* r2, const WMat* s13, const WMat* s2, int sI,
-                              const DecodeLayout& L, char* ws, uint16_t* out, hipStream_t stream) {
-  const int32_t* n_entries = reinterpret_cast<const int32_t*>(ws);
-  const PlanEntry* entries = reinterpret_cast<const PlanEntry*>(ws + L.entries);
-  const int32_t* row_tok = reinterpret_cast<const int32_t*>(ws + L.row_tok);
-  const float* row_w = reinterpret_cast<const float*>(ws + L.row_w);
-  uint16_t* a_hi = reinterpret_cast<uint16_t*>(ws + L.a_hi);
-  uint16_t* a_lo = reinterpret_cast<uint16_t*>(ws + L.a_lo);
-  uint16_t* s_hi = reinterpret_cast<uint16_t*>(ws + L.s_hi);
-  uint16_t* s_lo = reinterpret_cast<uint16_t*>(ws + L.s_lo);
-  const int runs = sI ? (T + kCols - 1) / kCols : 0;
-  const int shared_blocks = runs * (sI / 16);
-  const unsigned blocks = (unsigned)(shared_blocks + L.max_entries * (I / 16));
-  hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kFewWaves>), dim3(blocks),
-                     dim3(kFewWaves * kWave), 0, stream, x, T, H, I, *r13, *s13, sI, shared_blocks,
-                     n_entries, entries, row_tok, a_hi, a_lo, s_hi, s_lo);
-#define MOE_DECODE_DOWN(TS)                                                                    \
-  hipLaunchKernelGGL((decode_down_kernel<FMT, TS, kDownWaves>), dim3((unsigned)(H / 16)),        \
-                     dim3(kDownWaves * kWave), 0, stream, T, H, I, *r2, *s2, sI, runs, n_entries, \
-                     entries, row_w, a_hi, a_lo, s_hi, s_lo, out)
-  if (T <= 16) MOE_DECODE_DOWN(1);
-  else if (T <= 32) MOE_DECODE_DOWN(2);
-  else MOE_DECODE_DOWN(4);
-#undef MOE_DECODE_DOWN
+static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t stream) {
+  const DecodeLayout& L = d.L;
+  const DecodePlan plan = plan_of(d);
+  uint16_t* a_hi = reinterpret_cast<uint16_t*>(d.ws + L.a_hi);
+  uint16_t* a_lo = reinterpret_cast<uint16_t*>(d.ws + L.a_lo);
+  uint16_t* s_hi = reinterpret_cast<uint16_t*>(d.ws + L.s_hi);
+  uint16_t* s_lo = reinterpret_cast<uint16_t*>(d.ws + L.s_lo);
+  float* rows = reinterpret_cast<float*>(d.ws + L.rows);
+  float* s_rows = d.sI ? reinterpret_cast<float*>(d.ws + L.s_rows) : nullptr;
+  constexpr int kTile = 8 * GateShape<FMT>::NF;
+  const int runs = d.sI ? (d.T + kCols - 1) / kCols : 0;
+  const int sb = runs * (d.sI / kTile);
+  const unsigned gate = (unsigned)(sb + L.max_entries * (d.I / kTile) + (fused ? 1 : 0));
+#define MOE_DECODE_GATE(EPL)                                                                      \
+  hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kGateWaves, EPL>), dim3(gate),                     \
+                     dim3(kGateWaves * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI,   \
+                     sb, plan, a_hi, a_lo, s_hi, s_lo, d.logits, d.row_valid, d.E, d.K, d.renorm,   \
+                     d.expert_begin, d.El, d.topk_idx, d.topk_w)
+  if (!fused) MOE_DECODE_GATE(0);
+  else if (d.E <= 64) MOE_DECODE_GATE(1);
+  else MOE_DECODE_GATE(4);
+#undef MOE_DECODE_GATE
+  const int nt = d.H / (16 * down_frags<FMT>());
+  hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves>),
+                     dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
+                     stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a_hi, a_lo, s_hi,
+                     s_lo, rows, s_rows);
+  hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
+                     dim3(64), 0, stream, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
 }
 
 int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t* x, int T, int H,
                   int I, int E, int K, int expert_begin, int El, int renorm, int32_t* topk_idx,
                   float* topk_w, const moe_ffn_weights* routed, const moe_ffn_weights* shared,
                   int sI, uint16_t* out, void* workspace, int32_t* dev_error, hipStream_t stream) {
-  const DecodeLayout L = decode_layout(T, I, K, El, sI);
-  if ((int64_t)L.max_entries * (I / 16) + (int64_t)(T + kCols - 1) / kCols * (sI / 16) > 0x7fffffff)
-    return MOE_ERR_UNSUPPORTED;
-  char* ws = static_cast<char*>(workspace);
+  DecodeArgs d{logits, row_valid, x, T, H, I, E, K, expert_begin, El, renorm, sI, topk_idx, topk_w,
+               {routed->w13, routed->w13_scales, routed->w13_tensor_scale},
+               {routed->w2, routed->w2_scales, routed->w2_tensor_scale}, {}, {}, out,
+               decode_layout(T, H, I, K, El, sI), static_cast<char*>(workspace)};
+  if (shared) {
+    d.s13 = WMat{shared->w13, shared->w13_scales, shared->w13_tensor_scale};
+    d.s2 = WMat{shared->w2, shared->w2_scales, shared->w2_tensor_scale};
+  }
+  const int64_t most = d.L.max_entries + (T + kCols - 1) / kCols;
+  if (most * std::max(std::max(I, sI) / 16, H / 32) >= 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const bool fused = logits && T <= kFusedTokens && T * K <= 64 && E <= 256;
   const int epl = (E + kWave - 1) / kWave;
 #define MOE_PLAN(N)                                                                             \
   hipLaunchKernelGGL(plan_kernel<N>, dim3(1), dim3(kPlanThreads), 0, stream, logits, row_valid, T, \
-                     E, K, renorm, expert_begin, El, topk_idx, topk_w,                          \
-                     reinterpret_cast<int32_t*>(ws), reinterpret_cast<PlanEntry*>(ws + L.entries), \
-                     reinterpret_cast<int32_t*>(ws + L.row_tok),                                \
-                     reinterpret_cast<float*>(ws + L.row_w), dev_error)
-  if (!logits) MOE_PLAN(0);
-  else if (epl <= 1) MOE_PLAN(1);
-  else if (epl <= 2) MOE_PLAN(2);
-  else if (epl <= 4) MOE_PLAN(4);
-  else if (epl <= 8) MOE_PLAN(8);
-  else MOE_PLAN(16);
-#undef MOE_PLAN
-  const WMat r13{routed->w13, routed->w13_scales, routed->w13_tensor_scale};
-  const WMat r2{routed->w2, routed->w2_scales, routed->w2_tensor_scale};
-  WMat s13{}, s2{};
-  if (shared) {
-    s13 = WMat{shared->w13, shared->w13_scales, shared->w13_tensor_scale};
-    s2 = WMat{shared->w2, shared->w2_scales, shared->w2_tensor_scale};
+                     E, K, renorm, expert_begin, El, topk_idx, topk_w, plan_of(d), dev_error)
+  if (!fused) {
+    if (!logits) MOE_PLAN(0);
+    else if (epl <= 1) MOE_PLAN(1);
+    else if (epl <= 2) MOE_PLAN(2);
+    else if (epl <= 4) MOE_PLAN(4);
+    else if (epl <= 8) MOE_PLAN(8);
+    else MOE_PLAN(16);
   }
+#undef MOE_PLAN
   switch (routed->format) {
-    case MOE_W_BF16:
-      launch_decode_ffn<MOE_W_BF16>(x, T, H, I, K, &r13, &r2, &s13, &s2, sI, L, ws, out, stream);
-      break;
-    case MOE_W_FP8:
-      launch_decode_ffn<MOE_W_FP8>(x, T, H, I, K, &r13, &r2, &s13, &s2, sI, L, ws, out, stream);
-      break;
-    case MOE_W_MXFP4:
-      launch_decode_ffn<MOE_W_MXFP4>(x, T, H, I, K, &r13, &r2, &s13, &s2, sI, L, ws, out, stream);
-      break;
-    default:
-      launch_decode_ffn<MOE_W_NVFP4>(x, T, H, I, K, &r13, &r2, &s13, &s2, sI, L, ws, out, stream);
+    case MOE_W_BF16: launch_decode_ffn<MOE_W_BF16>(d, fused, stream); break;
+    case MOE_W_FP8: launch_decode_ffn<MOE_W_FP8>(d, fused, stream); break;
+    case MOE_W_MXFP4: launch_decode_ffn<MOE_W_MXFP4>(d, fused, stream); break;
+    default: launch_decode_ffn<MOE_W_NVFP4>(d, fused, stream);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -581,55 +799,43 @@ __global__ void __launch_bounds__(NW * kWave, 4) few_gate_up_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ cu_seqlens,
     const int32_t* __restrict__ counts, int G, int H, int I, WMat W, int64_t capacity,
     uint16_t* __restrict__ a_hi, uint16_t* __restrict__ a_lo, int32_t* __restrict__ dev_error) {
-  __shared__ f32x4_t red[NW][2][kWave];
-  const int nt = I / 16, j = blockIdx.x / nt;
+  __shared__ f32x4_t red[NW][GateShape<FMT>::NF][kWave];
+  const int nt = I / (8 * GateShape<FMT>::NF), j = blockIdx.x / nt;
   RowRun r;
   long long total;
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
   const int col = threadIdx.x & 15;
-  const uint16_t* xc = x + (int64_t)(r.row0 + min(col, r.cnt - 1)) * H;
-  few_gate_up<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I, xc, r.cnt, a_hi + (int64_t)r.row0 * I,
+  few_gate_up<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I,
+                       uniform_buffer(x + (int64_t)r.row0 * H, (int64_t)r.cnt * H * 2),
+                       (uint32_t)min(col, r.cnt - 1) * H * 2u, r.cnt, a_hi + (int64_t)r.row0 * I,
                        a_lo + (int64_t)r.row0 * I, red);
 }
 
-// One workgroup: 16 output columns of one run; its waves split I.
 template <int FMT, int NW>
-__global__ void __launch_bounds__(NW * kWave, 4) few_down_kernel(
+__global__ void __launch_bounds__(NW * kWave, 2) few_down_kernel(
     const uint16_t* __restrict__ a_hi, const uint16_t* __restrict__ a_lo,
     const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ counts, int G, int H,
     int I, WMat W, const float* __restrict__ row_scale, uint16_t* __restrict__ y,
     int64_t capacity, int64_t max_runs, int32_t* __restrict__ dev_error) {
-  __shared__ f32x4_t red[NW][kWave];
-  const int lane = threadIdx.x & 63, col = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nt = H / 16, j = blockIdx.x / nt, rt = blockIdx.x - j * nt;
+  __shared__ f32x4_t red[NW][down_frags<FMT>()][kWave];
+  const int nt = H / (16 * down_frags<FMT>()), j = blockIdx.x / nt;
   RowRun r;
   long long total;
-  if (blockIdx.x == 0 && w == 0) {
+  if (blockIdx.x == 0 && threadIdx.x < kWave) {
     // overlapping segments can hold more runs than the grid: said, not dropped silently
     if ((find_run(0x7fffffff, cu_seqlens, counts, G, capacity, dev_error, r, total) ||
-         total > max_runs) && lane == 0)
+         total > max_runs) && threadIdx.x == 0)
       raise_error(dev_error, MOE_DEVERR_ROW_RANGE);
   }
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
-  const int64_t row = r.row0 + min(col, r.cnt - 1);
-  WStream<FMT> ws[1];
-  ws[0].init(W, r.g, rt >> 2, rt & 3, H / 64, I / 128, 16 * rt, lane);
-  const int64_t o = row * I + 8 * (lane >> 4);
-  const uint16_t* b[2] = {a_hi + o, a_lo + o};
-  f32x4_t acc[1] = {f32x4_t{0.f, 0.f, 0.f, 0.f}};
-  few_stream<FMT, 1, 2, 2>(ws, b, w, NW, I / 128, acc);
-  red[w][lane] = acc[0];
-  __syncthreads();
-  if (w != 0) return;
-  f32x4_t v = red[0][lane];
-#pragma unroll
-  for (int i = 1; i < NW; ++i) v += red[i][lane];
-  if (col >= r.cnt) return;
-  const float sc = row_scale ? row_scale[row] : 1.0f;
-  *reinterpret_cast<uint2*>(y + row * H + rt * 16 + 4 * (lane >> 4)) =
-      make_uint2(f32_to_bf16(sc * v[0]) | f32_to_bf16(sc * v[1]) << 16,
-                 f32_to_bf16(sc * v[2]) | f32_to_bf16(sc * v[3]) << 16);
+  few_down<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I, a_hi + (int64_t)r.row0 * I,
+                    a_lo + (int64_t)r.row0 * I, r.cnt, red, [&](int c, int i, f32x4_t v) {
+                      const int64_t row = r.row0 + i;
+                      const float sc = row_scale ? row_scale[row] : 1.0f;
+                      *reinterpret_cast<uint2*>(y + row * H + c) =
+                          make_uint2(f32_to_bf16(sc * v[0]) | f32_to_bf16(sc * v[1]) << 16,
+                                     f32_to_bf16(sc * v[2]) | f32_to_bf16(sc * v[3]) << 16);
+                    });
 }
 
 // Runs that disjoint segments of `capacity` rows over G groups can hold.
@@ -643,15 +849,15 @@ static int launch_few_fmt(const uint16_t* x, const int32_t* cu, const int32_t* c
                           uint16_t* y, int64_t capacity, int flags, uint16_t* hi, uint16_t* lo,
                           int32_t* dev_error, hipStream_t stream) {
   const int64_t runs = max_row_runs(capacity, G);
-  const int64_t gu = runs * (I / 16), dn = runs * (H / 16);
+  const int64_t gu = runs * (I / (8 * GateShape<FMT>::NF)), dn = runs * (H / (16 * down_frags<FMT>()));
   if (gu > 0x7fffffff || dn > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   if (flags & MOE_FFN_GATE_UP)
-    hipLaunchKernelGGL((few_gate_up_kernel<FMT, kFewWaves>), dim3((unsigned)gu),
-                       dim3(kFewWaves * kWave), 0, stream, x, cu, counts, G, H, I, w13, capacity,
+    hipLaunchKernelGGL((few_gate_up_kernel<FMT, kGateWaves>), dim3((unsigned)gu),
+                       dim3(kGateWaves * kWave), 0, stream, x, cu, counts, G, H, I, w13, capacity,
                        hi, lo, dev_error);
   if (flags & MOE_FFN_DOWN)
-    hipLaunchKernelGGL((few_down_kernel<FMT, kFewWaves>), dim3((unsigned)dn),
-                       dim3(kFewWaves * kWave), 0, stream, hi, lo, cu, counts, G, H, I, w2,
+    hipLaunchKernelGGL((few_down_kernel<FMT, kDownWaves>), dim3((unsigned)dn),
+                       dim3(kDownWaves * kWave), 0, stream, hi, lo, cu, counts, G, H, I, w2,
                        row_scale, y, capacity, runs, dev_error);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

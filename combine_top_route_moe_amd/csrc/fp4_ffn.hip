@@ -131,7 +131,7 @@ int launch_pack_weights_fp4(const uint16_t* w13, const uint16_t* w2, int G, int 
 // fit one tile, so its weights are read once and stream past the caches.
 template <bool GATE_UP, int FMT, bool NT>
 __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
-                                              const WStream<FMT>* ws, const uint16_t* a_base,
+                                              const WStream<FMT>& ws, const uint16_t* a_base,
                                               const uint32_t* a_voff, int64_t a_sub_stride,
                                               int a_kb_stride, int w, int lane, int nkb,
                                               int nlive, f32x4_t (*acc)[4]) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
   Block cur[4], nxt[4];
   fill(0, 0);
 #pragma unroll
-  for (int f = 0; f < 4; ++f) ws[f].template load<NT>(nxt[f], 0);
+  for (int f = 0; f < 4; ++f) ws.template load<NT>(nxt[f], 0, f);
   for (int kb = 0; kb < nkb; ++kb) {
     const int buf = kb & 1;
     // everything in flight is block kb's: its DMA has landed in LDS after
@@ -166,7 +166,7 @@ __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
       // has finished
       fill(kb + 1, buf ^ 1);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) ws[f].template load<NT>(nxt[f], kb + 1);
+      for (int f = 0; f < 4; ++f) ws.template load<NT>(nxt[f], kb + 1, f);
       asm volatile("" ::: "memory");
     }
 #pragma unroll
@@ -234,9 +234,8 @@ __global__ void __launch_bounds__(kTileWaves * kWave, 2) fp4_tile_kernel(
   const int ct = ct_ok ? cb * kTileWaves + w : n_ct - 1;
   const int nkb = Kdim / 128;
 
-  WStream<FMT> ws[4];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) ws[f].init(W, g, ct, f, n_ct, nkb, 0, lane);
+  WStream<FMT> ws;
+  ws.init(W, g, ct, 0, n_ct, nkb, 0, 0, lane);
   // gate/up reads the rows themselves (rows past the end re-read the last);
   // down the gate/up kernel's output, in fragment order per m-tile: block
   // (subtile, K-step) of 64 lanes x 8 values

@@ -57,6 +57,29 @@ __device__ __forceinline__ bf16x8_t dequant8_fp8(u32x2_t c, float s) {
   return __builtin_bit_cast(bf16x8_t, w);
 }
 
+// A raw buffer over `bytes` bytes at the wave-uniform address p (loads past
+// them give 0), and loads from it at a uniform byte offset plus one per lane.
+// The whole address but the lane's offset stays in scalar registers: with
+// plain pointers the compiler keeps a 64-bit vector address per load of the
+// unrolled loops and spills.  NT: what is read once per call streams past the
+// caches (aux bit 1).
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t uniform_buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+template <bool NT>
+__device__ __forceinline__ u32x4_t load_b128(buffer_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_off, (int)off, NT ? 2 : 0);
+}
+template <bool NT>
+__device__ __forceinline__ u32x2_t load_b64(buffer_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, NT ? 2 : 0);
+}
+template <bool NT>
+__device__ __forceinline__ uint32_t load_b32(buffer_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, NT ? 2 : 0);
+}
+
 // One weight matrix stack [G, N, Kdim] in a packed format, as the kernels
 // take it (device pointers; scales and tensor_scale as the format needs).
 struct WMat {
@@ -65,19 +88,11 @@ struct WMat {
   const float* tensor_scale;
 };
 
-// NT: weights read once per call stream past the caches.
-template <bool NT, typename V>
-__device__ __forceinline__ V stream_load(const V* p) {
-  if constexpr (NT)
-    return __builtin_nontemporal_load(p);
-  else
-    return *p;
-}
-
-// A fragment's stream over the reduction dimension: load(kb) fetches block
-// kb's registers, operand(p) converts piece p.  g: expert, ct: column tile,
-// f: fragment within it, n_ct: column tiles, nkb: Kdim / 128, row0: the
-// fragment's first weight row (for the FP8 tile scales).
+// The stream of a column tile's fragments f0, f0 + 1, .. over the reduction
+// dimension: load(block, kb, f) fetches K-block kb of fragment f0 + f, and
+// Block::operand(p) converts piece p.  g: expert, ct: column tile, n_ct:
+// column tiles, nkb: Kdim / 128.  For w13 `up0` is the first weight row of
+// the tile's up half, whose fragments are 2 and 3 (FP8: the other tile scale).
 template <int FMT>
 struct WStream;
 
@@ -89,17 +104,20 @@ struct WStream<MOE_W_BF16> {
       return __builtin_bit_cast(bf16x8_t, v[p]);
     }
   };
-  const u32x4_t* base;
-  int stride;   // 16-byte units between K-steps
-  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f, int n_ct, int nkb,
-                                       int /*row0*/, int lane) {
-    stride = n_ct * 256;
-    base = static_cast<const u32x4_t*>(m.w) + ((int64_t)g * nkb * 4 * n_ct + ct) * 256 + f * 64 + lane;
+  buffer_t buf;
+  uint32_t stride, off;   // bytes between K-steps; the lane's
+  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
+                                       int /*row0*/, int /*up0*/, int lane) {
+    stride = n_ct * 4096;
+    const int64_t matrix = (int64_t)nkb * 4 * stride, at = ct * 4096 + f0 * 1024;
+    buf = uniform_buffer(static_cast<const char*>(m.w) + g * matrix + at, matrix - at);
+    off = (uint32_t)lane * 16u;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb) const {
+  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b.v[p] = stream_load<NT>(base + (int64_t)(4 * kb + p) * stride);
+    for (int p = 0; p < 4; ++p)
+      b.v[p] = load_b128<NT>(buf, off + f * 1024, (4 * kb + p) * stride);
   }
 };
 
@@ -110,20 +128,26 @@ struct WStream<MOE_W_FP8> {
     float s;
     __device__ __forceinline__ bf16x8_t operand(int p) const { return dequant8_fp8(v[p], s); }
   };
-  const u32x2_t* base;
+  buffer_t buf;
   const float* sc;
-  int stride;
-  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f, int n_ct, int nkb,
-                                       int row0, int lane) {
-    stride = n_ct * 256;
-    base = static_cast<const u32x2_t*>(m.w) + ((int64_t)g * nkb * 4 * n_ct + ct) * 256 + f * 64 + lane;
-    sc = static_cast<const float*>(m.scales) + ((int64_t)g * (n_ct / 2) + row0 / 128) * nkb;
+  const float* sc_up;
+  uint32_t stride, off;
+  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
+                                       int row0, int up0, int lane) {
+    stride = n_ct * 2048;
+    const int64_t matrix = (int64_t)nkb * 4 * stride, at = ct * 2048 + f0 * 512;
+    buf = uniform_buffer(static_cast<const char*>(m.w) + g * matrix + at, matrix - at);
+    off = (uint32_t)lane * 8u;
+    const float* s = static_cast<const float*>(m.scales) + (int64_t)g * (n_ct / 2) * nkb;
+    sc = s + (int64_t)(row0 / 128) * nkb;
+    sc_up = s + (int64_t)(up0 / 128) * nkb;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb) const {
+  __device__ __forceinline__ void load(Block& b, int kb, int f, bool up = false) const {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b.v[p] = stream_load<NT>(base + (int64_t)(4 * kb + p) * stride);
-    b.s = sc[kb];
+    for (int p = 0; p < 4; ++p)
+      b.v[p] = load_b64<NT>(buf, off + f * 512, (4 * kb + p) * stride);
+    b.s = up ? sc_up[kb] : sc[kb];
   }
 };
 
@@ -138,21 +162,23 @@ struct WStream<MOE_W_MXFP4> {
       return dequant8_mxfp4(v[p], e8m0_to_f32((s >> (8 * p)) & 0xffu));
     }
   };
-  const u32x4_t* base;
-  const uint32_t* sc;
-  int stride;   // fragments between K-blocks
-  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f, int n_ct, int nkb,
-                                       int /*row0*/, int lane) {
-    stride = n_ct * 4;
-    const int64_t frag = ((int64_t)g * nkb * n_ct + ct) * 4 + f;
-    base = static_cast<const u32x4_t*>(m.w) + frag * 64 + lane;
-    sc = static_cast<const uint32_t*>(m.scales) + frag * 16 + (lane & 15);
+  buffer_t buf, sbuf;
+  uint32_t stride;   // code bytes between K-blocks (scales: 1/16 of them)
+  uint32_t off, soff;
+  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
+                                       int /*row0*/, int /*up0*/, int lane) {
+    stride = n_ct * 4096;
+    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096 + f0 * 1024;
+    buf = uniform_buffer(static_cast<const char*>(m.w) + g * matrix + at, matrix - at);
+    sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (g * matrix + at) / 16,
+                          (matrix - at) / 16);
+    off = (uint32_t)lane * 16u;
+    soff = (uint32_t)(lane & 15) * 4u;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb) const {
-    const int64_t o = (int64_t)kb * stride;
-    b.v = stream_load<NT>(base + o * 64);
-    b.s = stream_load<NT>(sc + o * 16);
+  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
+    b.v = load_b128<NT>(buf, off + f * 1024, kb * stride);
+    b.s = load_b32<NT>(sbuf, soff + f * 64, kb * (stride / 16));
   }
 };
 
@@ -170,23 +196,25 @@ struct WStream<MOE_W_NVFP4> {
       return dequant8_nvfp4(v[p], b * g);
     }
   };
-  const u32x4_t* base;
-  const uint32_t* sc;
+  buffer_t buf, sbuf;
   float g;
-  int stride;
-  __device__ __forceinline__ void init(const WMat& m, int grp, int ct, int f, int n_ct, int nkb,
-                                       int /*row0*/, int lane) {
-    stride = n_ct * 4;
-    const int64_t frag = ((int64_t)grp * nkb * n_ct + ct) * 4 + f;
-    base = static_cast<const u32x4_t*>(m.w) + frag * 64 + lane;
-    sc = static_cast<const uint32_t*>(m.scales) + frag * 32 + (lane >> 5) * 16 + (lane & 15);
+  uint32_t stride;   // code bytes between K-blocks (scales: 1/8 of them)
+  uint32_t off, soff;
+  __device__ __forceinline__ void init(const WMat& m, int grp, int ct, int f0, int n_ct, int nkb,
+                                       int /*row0*/, int /*up0*/, int lane) {
+    stride = n_ct * 4096;
+    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096 + f0 * 1024;
+    buf = uniform_buffer(static_cast<const char*>(m.w) + grp * matrix + at, matrix - at);
+    sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (grp * matrix + at) / 8,
+                          (matrix - at) / 8);
+    off = (uint32_t)lane * 16u;
+    soff = (uint32_t)((lane >> 5) * 16 + (lane & 15)) * 4u;
     g = m.tensor_scale[grp];
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb) const {
-    const int64_t o = (int64_t)kb * stride;
-    b.v = stream_load<NT>(base + o * 64);
-    b.s = stream_load<NT>(sc + o * 32);
+  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
+    b.v = load_b128<NT>(buf, off + f * 1024, kb * stride);
+    b.s = load_b32<NT>(sbuf, soff + f * 128, kb * (stride / 8));
     b.g = g;
   }
 };

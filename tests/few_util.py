@@ -18,7 +18,7 @@ import numpy as np
 
 import oracle
 from oracle.ffn import silu
-from oracle.numerics import bf16_bits_to_f32, bf16_bits_to_f64, f32_to_bf16_bits
+from oracle.numerics import bf16_bits_to_f32, bf16_bits_to_f64, e4m3fn_round, f32_to_bf16_bits
 
 F32_SUM = 2.0 ** -23
 BF16_HALF = 2.0 ** -8
@@ -33,15 +33,38 @@ def tensor_scale(w_bits) -> np.float32:
     return oracle.nvfp4_tensor_scale(np.abs(bf16_bits_to_f32(w_bits)).max())
 
 
+def _e2m1(r) -> np.ndarray:
+    """E2M1 values of float32 r, |r| <= 6 (ties to the even code)."""
+    a = np.abs(r)
+    q = ((a > .25) * np.float32(.5) + (a >= .75) * np.float32(.5) + (a > 1.25) * np.float32(.5)
+         + (a >= 1.75) * np.float32(.5) + (a > 2.5) + (a >= 3.5) + (a > 5.0) * np.float32(2))
+    return np.copysign(q.astype(np.float32), r)
+
+
 def fake_quant(w_bits, fmt: str, g=None) -> np.ndarray:
-    """bf16 bits [N, K] of the values that ``fmt`` stores a matrix as."""
+    """bf16 bits [N, K] of the values that ``fmt`` stores a matrix as: the
+    oracle's fake-quantizers (4-bit ones restated here without their tables, a
+    hundred times faster; test_fp4_decode_host.py holds them to the oracle's)."""
     if fmt == "bf16":
         return w_bits
     if fmt == "fp8":
         return oracle.quantize_weight_blocks(w_bits)[2]
+    N, K = w_bits.shape
+    x = bf16_bits_to_f32(w_bits).reshape(N, -1, 32 if fmt == "mxfp4" else 16)
+    amax = np.abs(x).max(axis=2)
     if fmt == "mxfp4":
-        return oracle.fake_quant_mxfp4(w_bits)[0]
-    return oracle.fake_quant_nvfp4(w_bits, tensor_scale(w_bits) if g is None else g)[0]
+        e = np.clip(np.frexp(np.where(amax > 0, amax, 1))[1] - 3, -127, 127)
+        S = np.where(amax > 0, np.ldexp(np.float32(1), e), 0).astype(np.float32)[..., None]
+        r = np.ldexp(x, -e[..., None])
+    else:
+        g = np.float32(tensor_scale(w_bits) if g is None else g)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            q = amax / np.float32(np.float32(6) * g)
+        b = e4m3fn_round(np.minimum(np.where(np.isnan(q), 0, q).astype(np.float64), 448.0))
+        S = (b.astype(np.float32) * g)[..., None]
+        r = x / np.where(S > 0, S, np.float32(1))
+    v = np.where(S > 0, _e2m1(np.clip(r, -6, 6)) * S, np.float32(0))
+    return f32_to_bf16_bits(v.astype(np.float32)).reshape(N, K)
 
 
 def make_weights(rng, G: int, H: int, I: int, std: float = 0.06):

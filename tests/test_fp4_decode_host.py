@@ -4,10 +4,13 @@ device work (no GPU needed; the pointers are never read)."""
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 from combine_top_route_moe_amd import _lib, ops
+from tests import few_util as fu
 
 P = 1 << 20            # a 16-byte aligned address, never read
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
@@ -116,7 +119,8 @@ def test_size_queries(lib):
     need = ops.moe_decode_workspace_bytes(64, 7168, 2048, 8, 256, 2048)
     assert need >= 64 * 9 * 2048 * 4
     assert ops.moe_decode_workspace_bytes(-1, 128, 128, 1, 1, 0) == 0
-    assert _decode(lib, T=64, H=7168, I=2048, E=256, K=8, El=256, ws_bytes=need - 1 - 64 * 2048 * 4) == WORKSPACE
+    need = ops.moe_decode_workspace_bytes(64, 7168, 2048, 8, 256)
+    assert _decode(lib, T=64, H=7168, I=2048, E=256, K=8, El=256, ws_bytes=need - 1) == WORKSPACE
     assert ops.moe_grouped_ffn_fp4_workspace_bytes(1000, 4, 256, 128) >= 1000 * 128 * 2
     assert ops.moe_grouped_ffn_fp4_workspace_bytes(7, 4, 256, 128) >= 7 * 128 * 4
     assert ops.moe_grouped_ffn_fp4_workspace_bytes(0, 4, 256, 128) >= 0
@@ -142,3 +146,15 @@ def test_handles_check_their_tensors():
         ops.ffn_weights(w13.float(), w2, "bf16")
     with pytest.raises(ValueError):
         ops.moe_pack_ffn_weights_fp4(w13, w2, mode=ops.MOE_FQ_BLOCK)
+
+
+def test_fast_fake_quantizers_are_the_oracles():
+    rng = np.random.default_rng(0)
+    w = rng.standard_normal((64, 256)).astype(np.float32) * 0.1
+    w[0, :32], w[1, :32], w[2] = 0.0, -0.0, w[2] * 2.0 ** -110
+    w[3, :16] = [6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5, 0.5]
+    bits = fu.bf16(w)
+    np.testing.assert_array_equal(fu.fake_quant(bits, "mxfp4"), oracle.fake_quant_mxfp4(bits)[0])
+    g = fu.tensor_scale(bits)
+    np.testing.assert_array_equal(fu.fake_quant(bits, "nvfp4"), oracle.fake_quant_nvfp4(bits, g)[0])
+    np.testing.assert_array_equal(fu.fake_quant(bits, "nvfp4", 1e-3), oracle.fake_quant_nvfp4(bits, 1e-3)[0])

@@ -96,7 +96,7 @@ def test_a_model_sized_layer():
     whole result's error too: one rounding, at most 2^-8 relative, and the
     float32 sums' share, taken as 2^-12 (sums of a few thousand terms of
     random sign are off by far less than their worst case)."""
-    T, H, E, K, I, sI = 3, 4096, 8, 2, 1536, 1536
+    T, H, E, K, I, sI = 3, 4096, 3, 2, 1536, 1536
     rng = np.random.default_rng(3)
     for fmt in FMTS:
         L = Layer(4, fmt, E, H, I, sI)
