@@ -50,7 +50,7 @@ struct PlanEntry {
 
 // The workspace: plan, intermediate rows (routed, then shared), float32 rows.
 struct DecodeLayout {
-  size_t entries, row_tok, row_of, a_hi, a_lo, s_hi, s_lo, rows, s_rows, total;
+  size_t entries, row_tok, row_of, a, s_a, rows, s_rows, total;
   int64_t max_entries;
 };
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -67,10 +67,8 @@ static DecodeLayout decode_layout(int T, int H, int I, int K, int El, int sI) {
   L.entries = put((size_t)L.max_entries * sizeof(PlanEntry));
   L.row_tok = put((size_t)rows * 4);
   L.row_of = put((size_t)rows * 4);
-  L.a_hi = put((size_t)rows * I * 2);
-  L.a_lo = put((size_t)rows * I * 2);
-  L.s_hi = put((size_t)T * sI * 2);
-  L.s_lo = put((size_t)T * sI * 2);
+  L.a = put((size_t)rows * I * 4);
+  L.s_a = put((size_t)T * sI * 4);
   L.rows = put((size_t)rows * H * 4);
   L.s_rows = put(sI ? (size_t)T * H * 4 : 0);
   L.total = o;
@@ -120,9 +118,8 @@ __device__ __forceinline__ void load_keys(const float* __restrict__ row, int E, 
 // and order as route_row: lane k < K gets slot k's expert in sel_e and its
 // logit in sel_v.  Each lane first sorts its keys, so that a round compares
 // one head per lane: the wave maximum, the lanes that hold it (one, but for
-// ties), and the winner drops its head.  A round is about 15 instructions,
-// a fifth of route_row's (one workgroup's plan of 64 tokens, 64 experts: 17 ->
-// 9 us); sorting pays while a lane holds few experts.
+// ties), and the winner drops its head.  Sorting pays while a lane holds few
+// experts.
 template <int EPL>
 __device__ __forceinline__ void select_topk(const int* key, int K, int lane, int& sel_e,
                                             float& sel_v) {
@@ -136,7 +133,7 @@ __device__ __forceinline__ void select_topk(const int* key, int K, int lane, int
   for (int i = 1; i < EPL; ++i)               // stable: equal keys keep the lower index first
 #pragma unroll
     for (int j = EPL - 1; j >= i; --j) {
-      const bool sw = h[j] > h[j - 1] || (h[j] == h[j - 1] && e[j] < e[j - 1]);
+      const bool sw = h[j] > h[j - 1];
       const int a = h[j - 1], b = e[j - 1];
       h[j - 1] = sw ? h[j] : a;
       e[j - 1] = sw ? e[j] : b;
@@ -164,6 +161,60 @@ __device__ __forceinline__ void select_topk(const int* key, int K, int lane, int
   sel_v = key_value(best);
 }
 
+// Four tokens at once, 16 lanes each, for E <= 64 and K <= 16: lane i of a
+// token's row of lanes holds experts i, i + 16, .. and gets slot i.  Maximum
+// and lowest index come by register moves within the row, nothing passes
+// through scalar registers: 64 tokens of 64 experts, top-8, take the plan 5 us
+// instead of the 11 of a wave per token.
+__device__ __forceinline__ int row16_max(int v) {
+  v = max(v, row16_dpp<0xB1>(v));
+  v = max(v, row16_dpp<0x4E>(v));
+  v = max(v, row16_dpp<0x141>(v));
+  return max(v, row16_dpp<0x140>(v));
+}
+__device__ __forceinline__ int row16_min(int v) {
+  v = min(v, row16_dpp<0xB1>(v));
+  v = min(v, row16_dpp<0x4E>(v));
+  v = min(v, row16_dpp<0x141>(v));
+  return min(v, row16_dpp<0x140>(v));
+}
+__device__ __forceinline__ void select_topk_row16(const float* __restrict__ row, int E, int K,
+                                                  int i, int& sel_e, float& sel_v) {
+  int h[4], e[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    e[j] = i + 16 * j;
+    h[j] = e[j] < E ? order_key(row[e[j]]) : kNoKey;
+  }
+#pragma unroll
+  for (int p = 1; p < 4; ++p)                 // stable: equal keys keep the lower index first
+#pragma unroll
+    for (int j = 3; j >= p; --j) {
+      const bool sw = h[j] > h[j - 1];
+      const int a = h[j - 1], b = e[j - 1];
+      h[j - 1] = sw ? h[j] : a;
+      e[j - 1] = sw ? e[j] : b;
+      h[j] = sw ? a : h[j];
+      e[j] = sw ? b : e[j];
+    }
+  int best = kNoKey;
+  sel_e = -1;
+  for (int k = 0; k < K; ++k) {
+    const int mv = row16_max(h[0]);
+    const int win = row16_min(h[0] == mv ? e[0] : 0x7fffffff);
+    sel_e = i == k ? win : sel_e;
+    best = i == k ? mv : best;
+    const bool mine = e[0] == win && h[0] == mv;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      h[j] = mine ? h[j + 1] : h[j];
+      e[j] = mine ? e[j + 1] : e[j];
+    }
+    h[3] = mine ? kNoKey : h[3];
+  }
+  sel_v = key_value(best);
+}
+
 // The selected experts' weights (lane k < K: slot k's), as route_row's.
 template <int EPL>
 __device__ __forceinline__ float topk_weight(const int* key, int E, int K, int renorm, int lane,
@@ -186,9 +237,11 @@ __device__ __forceinline__ float topk_weight(const int* key, int E, int K, int r
 
 // ---- plan -------------------------------------------------------------------
 // One workgroup.  EPL 0: the routes are given (topk_idx, topk_w are inputs),
-// else experts per lane of the top-k selection.  A wave selects for one token
-// after another; the weights' exponentials (double, as moe_route's) are then
-// taken by one thread per slot, not by a few lanes of each token's wave.
+// else experts per lane of the selection by a wave per token.  The weights'
+// exponentials (double, as moe_route's) are taken by one thread per slot, not
+// by a few lanes of each token's wave.  Routing more tokens than there are
+// waves here is left to route_few_kernel, over many CUs, unless 16 lanes can
+// do one.
 struct DecodePlan {
   int32_t* n_entries;
   PlanEntry* entries;
@@ -201,11 +254,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
     const float* __restrict__ logits, const uint8_t* __restrict__ row_valid, int T, int E, int K,
     int renorm, int expert_begin, int El, int32_t* __restrict__ topk_idx,
     float* __restrict__ topk_w, DecodePlan plan, int32_t* __restrict__ dev_error) {
-  constexpr bool kSort = EPL > 0 && EPL <= 4;
+  constexpr int kSlots = EPL > 0 ? kMaxTokens * 32 : 1;
   __shared__ uint32_t mask[1024][2];
   __shared__ int sel_e[kMaxTokens * 32];
-  __shared__ float sel_v[kSort ? kMaxTokens * 32 : 1];
-  __shared__ double term[kSort ? kMaxTokens * 32 : 1];
+  __shared__ float sel_v[kSlots];
+  __shared__ double term[kSlots];
   __shared__ int base_of[1024];
   __shared__ int wave_sum[kPlanThreads / kWave];
   constexpr int kWaves = kPlanThreads / kWave;
@@ -214,53 +267,50 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   mask[tid][0] = 0u;
   mask[tid][1] = 0u;
   __syncthreads();
-  constexpr int kV = kSort ? EPL : 1;
-  int nv[kV];
-  if constexpr (kSort) {
-    if (wv < T) load_keys<EPL>(logits + (int64_t)wv * E, E, lane, nv);
-  }
-  for (int t = wv; t < T; t += kWaves) {
-    const bool real = !row_valid || row_valid[t];
-    const int slot = t * K + lane;
-    int e = -1;
-    if constexpr (kSort) {
-      int v[kV];
-      float sv = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kV; ++j) v[j] = nv[j];
-      if (t + kWaves < T) load_keys<EPL>(logits + (int64_t)(t + kWaves) * E, E, lane, nv);
-      if (real) {
-        select_topk<EPL>(v, K, lane, e, sv);
+  // slot k of token t goes to expert e (-1: none), its logit being v
+  auto note = [&](int t, int k, int e, float v) {
+    const int slot = t * K + k;
+    const bool here = e >= expert_begin && e < E && e - expert_begin < El;
+    // -2: no expert at all (a masked token's weight is 0)
+    sel_e[slot] = here ? e - expert_begin : e < 0 ? -2 : -1;
+    if (here) atomicOr(&mask[e - expert_begin][t >> 5], 1u << (t & 31));
+    if constexpr (EPL > 0) {
+      sel_v[slot] = v;
+      topk_idx[slot] = e;
+    }
+  };
+  if constexpr (EPL == 0) {
+    for (int i = tid; i < T * K; i += kPlanThreads) {
+      const int t = i / K;
+      const int e = !row_valid || row_valid[t] ? topk_idx[i] : -1;
+      if (e >= E) raise_error(dev_error, MOE_DEVERR_EXPERT_RANGE);
+      note(t, i - t * K, e, 0.0f);
+    }
+  } else if (EPL == 1 && K <= 16 && renorm) {
+    const int t = tid >> 4, i = tid & 15;
+    if (4 * wv < T) {                       // the whole wave or none of it
+      int e;
+      float v;
+      select_topk_row16(logits + (int64_t)min(t, T - 1) * E, E, K, i, e, v);
+      if (t < T && i < K) note(t, i, !row_valid || row_valid[t] ? e : -1, v);
+    }
+  } else {
+    for (int t = wv; t < T; t += kWaves) {
+      int key[EPL > 0 ? EPL : 1], e = -1;
+      float v = 0.0f;
+      if (!row_valid || row_valid[t]) {
+        load_keys<EPL>(logits + (int64_t)t * E, E, lane, key);
+        select_topk<EPL>(key, K, lane, e, v);
         if (!renorm) {
-          const float w = topk_weight<EPL>(v, E, K, renorm, lane, sv);
-          if (lane < K) topk_w[slot] = w;
+          const float w = topk_weight<EPL>(key, E, K, renorm, lane, v);
+          if (lane < K) topk_w[t * K + lane] = w;
         }
       }
-      if (lane < K) {
-        topk_idx[slot] = e;
-        sel_v[slot] = sv;
-      }
-    } else if constexpr (EPL > 0) {
-      float w = 0.0f;
-      if (real) route_row<EPL>(logits + (int64_t)t * E, E, K, renorm, lane, e, w);
-      if (lane < K) {
-        topk_idx[slot] = e;
-        topk_w[slot] = w;
-      }
-    } else if (lane < K && real) {
-      e = topk_idx[slot];
-      if (e >= E) raise_error(dev_error, MOE_DEVERR_EXPERT_RANGE);
-    }
-    if (lane < K) {
-      const bool here = e >= expert_begin && e < E && e - expert_begin < El;
-      const int le = here ? e - expert_begin : -1;
-      // -2: no expert at all (a masked token's weight is 0)
-      sel_e[slot] = here ? le : e < 0 ? -2 : -1;
-      if (here) atomicOr(&mask[le][t >> 5], 1u << (t & 31));
+      if (lane < K) note(t, lane, e, v);
     }
   }
   __syncthreads();
-  if constexpr (kSort) {
+  if constexpr (EPL > 0) {
     for (int i = tid; i < T * K; i += kPlanThreads)
       term[i] = weight_term(sel_v[i], sel_v[i / K * K]);
   }
@@ -293,7 +343,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   // token names the expert in several slots
   for (int i = tid; i < T * K; i += kPlanThreads) {
     const int e = sel_e[i], t = i / K;
-    if constexpr (kSort) {
+    if constexpr (EPL > 0) {
       if (renorm) {
         double den = 0.0;
         for (int j = t * K; j < (t + 1) * K; ++j) den += term[j];   // slot order
@@ -312,17 +362,36 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   }
 }
 
+// Routes alone, a wave per token over as many CUs, for a plan on given routes.
+template <int EPL>
+__global__ void __launch_bounds__(kWave) route_few_kernel(
+    const float* __restrict__ logits, const uint8_t* __restrict__ row_valid, int E, int K,
+    int renorm, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+  const int t = blockIdx.x, lane = threadIdx.x;
+  int key[EPL], e = -1;
+  float v = 0.0f, w = 0.0f;
+  if (!row_valid || row_valid[t]) {
+    load_keys<EPL>(logits + (int64_t)t * E, E, lane, key);
+    select_topk<EPL>(key, K, lane, e, v);
+    w = topk_weight<EPL>(key, E, K, renorm, lane, v);
+  }
+  if (lane < K) {
+    topk_idx[t * K + lane] = e;
+    topk_w[t * K + lane] = w;
+  }
+}
+
 // ---- the streamed product ---------------------------------------------------
-// acc[i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * B^T for NF weight
-// fragments of one column tile and one 16-column B given as NB bf16 addends
-// (buffers b[a], boff the lane's byte offset of its column's first element).
+// acc[a][i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * B_a^T for NF weight
+// fragments of one column tile and NB 16-column operands out of the buffer b
+// (boff[a]: the byte offset of the lane's column's first element).
 // GU: the first half of the fragments are gate rows, the others the matching
 // up rows, two fragments on.  D blocks are in flight per wave; the loop that
 // refills is free of branches, so that each wait covers one block only.
 template <int FMT, int NF, int NB, int D, bool GU>
-__device__ __forceinline__ void few_stream(const WStream<FMT>& ws, const buffer_t* b,
-                                           uint32_t boff, int kb0, int step, int nkb,
-                                           f32x4_t* acc) {
+__device__ __forceinline__ void few_stream(const WStream<FMT>& ws, buffer_t b,
+                                           const uint32_t* boff, int kb0, int step, int nkb,
+                                           f32x4_t (*acc)[NF]) {
   struct Buf {
     typename WStream<FMT>::Block w[NF];
     u32x4_t x[NB][4];
@@ -339,8 +408,7 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>& ws, const buffer_
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        t.x[a][p] = load_b128<false>(b[a], boff + p * 64, kb * 256);
+      for (int p = 0; p < 4; ++p) t.x[a][p] = load_b128<false>(b, boff[a] + p * 64, kb * 256);
   };
   auto use = [&](const Buf& t) {
 #pragma unroll
@@ -350,8 +418,8 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>& ws, const buffer_
         const bf16x8_t wf = t.w[f].operand(p);
 #pragma unroll
         for (int a = 0; a < NB; ++a)
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              wf, __builtin_bit_cast(bf16x8_t, t.x[a][p]), acc[f], 0, 0, 0);
+          acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              wf, __builtin_bit_cast(bf16x8_t, t.x[a][p]), acc[a][f], 0, 0, 0);
       }
   };
 #pragma unroll
@@ -375,15 +443,16 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>& ws, const buffer_
     if (i + D + d < n) use(buf[d]);
 }
 
-// The gate/up tile and its stream, by format: NF fragments a wave (half gate,
-// half up) and D blocks in flight.  bf16 blocks are large (4 KB a fragment):
-// 2 fragments, so that registers leave four waves to a SIMD; the narrower
-// formats take a whole 64-row column tile, which reads each row of x for four
-// fragments instead of two.
+// The shape of a few-row product, by format: NF fragments a wave (gate/up: half
+// gate, half up), D blocks in flight per wave, kWaves waves to a SIMD (what the
+// registers of that allow).  bf16 blocks are large (4 KB a fragment): two
+// fragments; the narrower formats take a whole 64-row column tile, which reads
+// each row of x, or of a, for four fragments.
 template <int FMT>
-struct GateShape {
-  static constexpr int NF = FMT == MOE_W_BF16 || FMT == MOE_W_FP8 ? 2 : 4;
+struct FewShape {
+  static constexpr int NF = FMT == MOE_W_BF16 ? 2 : 4;
   static constexpr int D = 2;
+  static constexpr int kWaves = FMT == MOE_W_FP8 ? 3 : 4;
 };
 
 // v as the sum of two bf16 numbers, high part first
@@ -394,25 +463,26 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) 
 
 // One workgroup's gate/up tile: 8 NF intermediate columns, nt of expert g, for
 // the cnt <= 16 rows whose x this lane's column is at byte xoff of x (columns
-// past cnt repeat the last one and are not stored).  a rows go to hi / lo +
-// column * I.
+// past cnt repeat the last one and are not stored).  a rows go to a + column *
+// 2 I, the I high parts before the I low ones.
 template <int FMT, int NW>
 __device__ __forceinline__ void few_gate_up(const WMat& W, int g, int nt, int H, int I,
                                             buffer_t x, uint32_t xoff, int cnt,
-                                            uint16_t* hi, uint16_t* lo,
-                                            f32x4_t (*red)[GateShape<FMT>::NF][kWave]) {
-  constexpr int NF = GateShape<FMT>::NF, NH = NF / 2;   // NH gate and NH up fragments
+                                            uint16_t* a,
+                                            f32x4_t (*red)[FewShape<FMT>::NF][kWave]) {
+  constexpr int NF = FewShape<FMT>::NF, NH = NF / 2;   // NH gate and NH up fragments
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = H / 128, ct = nt * NH / 2, f0 = nt * NH % 2;
   WStream<FMT> ws;
   ws.init(W, g, ct, f0, I / 32, nkb, 32 * ct, I + 32 * ct, lane);
-  f32x4_t acc[NF];
+  f32x4_t acc[1][NF];
 #pragma unroll
-  for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  few_stream<FMT, NF, 1, GateShape<FMT>::D, true>(ws, &x, xoff + 16 * (lane >> 4), w, NW, nkb, acc);
+  for (int i = 0; i < NF; ++i) acc[0][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const uint32_t off[1] = {xoff + 16 * (lane >> 4)};
+  few_stream<FMT, NF, 1, FewShape<FMT>::D, true>(ws, x, off, w, NW, nkb, acc);
 #pragma unroll
-  for (int i = 0; i < NF; ++i) red[w][i][lane] = acc[i];
+  for (int i = 0; i < NF; ++i) red[w][i][lane] = acc[0][i];
   __syncthreads();
   if (w >= NH) return;
   f32x4_t gt = red[0][w][lane], up = red[0][NH + w][lane];
@@ -427,9 +497,9 @@ __device__ __forceinline__ void few_gate_up(const WMat& W, int g, int nt, int H,
   uint32_t h[4], l[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) split_bf16(silu_f(gt[q]) * up[q], h[q], l[q]);
-  const int64_t o = (int64_t)col * I + 32 * ct + 16 * (f0 + w) + 4 * (lane >> 4);
-  *reinterpret_cast<uint2*>(hi + o) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  *reinterpret_cast<uint2*>(lo + o) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  uint16_t* o = a + (int64_t)col * 2 * I + 32 * ct + 16 * (f0 + w) + 4 * (lane >> 4);
+  *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  *reinterpret_cast<uint2*>(o + I) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
 // ---- the plan of a few routed tokens, by every wave on its own ------------------
@@ -469,29 +539,29 @@ __device__ __forceinline__ SmallPlan small_plan(int e, int n_slots, int T, int l
 // end of the grid writes the plan for the down kernel.  That saves a launch,
 // 5 us, and costs each workgroup about 1.
 template <int FMT, int NW, int EPL>
-__global__ void __launch_bounds__(NW * kWave, 4) decode_gate_up_kernel(
+__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate_up_kernel(
     const uint16_t* __restrict__ x, int T, int H, int I, WMat routed, WMat shared, int sI,
-    int shared_blocks, DecodePlan plan, uint16_t* __restrict__ a_hi, uint16_t* __restrict__ a_lo,
-    uint16_t* __restrict__ s_hi, uint16_t* __restrict__ s_lo, const float* __restrict__ logits,
+    int shared_blocks, DecodePlan plan, uint16_t* __restrict__ a, uint16_t* __restrict__ s_a,
+    const float* __restrict__ logits,
     const uint8_t* __restrict__ row_valid, int E, int K, int renorm, int expert_begin, int El,
     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
-  constexpr int kTile = 8 * GateShape<FMT>::NF;   // intermediate columns of a workgroup
-  __shared__ f32x4_t red[NW][GateShape<FMT>::NF][kWave];
+  constexpr int kTile = 8 * FewShape<FMT>::NF;   // intermediate columns of a workgroup
+  __shared__ f32x4_t red[NW][FewShape<FMT>::NF][kWave];
   __shared__ int sel[64];
   const int lane = threadIdx.x & 63, col = lane & 15;
   const buffer_t xbuf = uniform_buffer(x, (int64_t)T * H * 2);
   int b = blockIdx.x;
-  if (b < shared_blocks) {
-    const int nt = sI / kTile, v = b / nt;
-    const int t0 = v * kCols, cnt = min(kCols, T - t0);
-    few_gate_up<FMT, NW>(shared, 0, b - v * nt, H, sI, xbuf,
-                         (uint32_t)(t0 + min(col, cnt - 1)) * H * 2u, cnt, s_hi + (int64_t)t0 * sI,
-                         s_lo + (int64_t)t0 * sI, red);
-    return;
-  }
-  b -= shared_blocks;
-  const int nt = I / kTile, j = b / nt;
+  const bool sh = b < shared_blocks;
+  if (!sh) b -= shared_blocks;
+  const int Ic = sh ? sI : I;
+  const int nt = Ic / kTile, j = b / nt;
   int g, base, cnt, tok = 0;
+  if (sh) {
+    g = 0;
+    base = j * kCols;
+    cnt = min(kCols, T - base);
+    tok = base + min(col, cnt - 1);
+  } else
   if constexpr (EPL > 0) {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool writer = blockIdx.x == gridDim.x - 1;
@@ -547,76 +617,93 @@ __global__ void __launch_bounds__(NW * kWave, 4) decode_gate_up_kernel(
     cnt = plan.entries[j].cnt;
     tok = plan.row_tok[base + min(col, cnt - 1)];
   }
-  few_gate_up<FMT, NW>(routed, g, b - j * nt, H, I, xbuf, (uint32_t)tok * H * 2u, cnt,
-                       a_hi + (int64_t)base * I, a_lo + (int64_t)base * I, red);
+  few_gate_up<FMT, NW>(sh ? shared : routed, g, b - j * nt, H, Ic, xbuf,
+                          (uint32_t)tok * H * 2u, cnt, (sh ? s_a : a) + (int64_t)base * 2 * Ic,
+                          red);
 }
 
 // ---- down ---------------------------------------------------------------------
-// 16-column fragments of a down tile, by format (bf16 blocks are large)
-template <int FMT>
-constexpr int down_frags() {
-  return FMT == MOE_W_BF16 ? 2 : 4;
+// One workgroup's down tile: 16 NF output columns of the cnt <= 16 rows of a
+// (each I high parts, then I low ones), for expert g; store(first of four
+// columns, row, their sums) for every row.  The high and the low part of up to
+// 8 rows share one B operand, columns c and c + 8, and are added at the end:
+// one MFMA for both, and half the registers.  9 to 16 rows take two operands.
+template <int FMT, int NW, int NB, int D>
+__device__ __forceinline__ void few_down_rows(const WStream<FMT>& ws, buffer_t a,
+                                              const uint32_t* off, int nkb,
+                                              f32x4_t (*red)[2][FewShape<FMT>::NF][kWave]) {
+  constexpr int NF = FewShape<FMT>::NF;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  f32x4_t acc[NB][NF];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  few_stream<FMT, NF, NB, D, false>(ws, a, off, w, NW, nkb, acc);
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) red[w][i][f][lane] = acc[i][f];
 }
 
-// One workgroup's down tile: 16 NF output columns of the cnt <= 16 rows of a
-// (high and low parts, row stride I), for expert g; store(fragment's first
-// column, row, four columns' sums) for every row.
 template <int FMT, int NW, typename Store>
 __device__ __forceinline__ void few_down(const WMat& W, int g, int tile, int H, int I,
-                                         const uint16_t* hi, const uint16_t* lo, int cnt,
-                                         f32x4_t (*red)[down_frags<FMT>()][kWave], Store store) {
-  constexpr int NF = down_frags<FMT>();
+                                         const uint16_t* rows, int cnt,
+                                         f32x4_t (*red)[2][FewShape<FMT>::NF][kWave],
+                                         Store store) {
+  constexpr int NF = FewShape<FMT>::NF;
   const int lane = threadIdx.x & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WStream<FMT> ws;
   ws.init(W, g, tile * NF / 4, tile * NF % 4, H / 64, I / 128, 16 * NF * tile, 0, lane);
-  f32x4_t acc[NF];
+  // operand i: columns 0..7 the high parts of rows 8 i .., 8..15 the low ones
+  const buffer_t a = uniform_buffer(rows, (int64_t)cnt * I * 4);
+  uint32_t off[2];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int64_t bytes = (int64_t)cnt * I * 2;
-  const buffer_t b[2] = {uniform_buffer(hi, bytes), uniform_buffer(lo, bytes)};
-  const uint32_t boff = (uint32_t)(min(col, cnt - 1) * I + 8 * (lane >> 4)) * 2u;
-  few_stream<FMT, NF, 2, 2, false>(ws, b, boff, w, NW, I / 128, acc);
-#pragma unroll
-  for (int f = 0; f < NF; ++f) red[w][f][lane] = acc[f];
+  for (int i = 0; i < 2; ++i)
+    off[i] = (uint32_t)(min(8 * i + (col & 7), cnt - 1) * 2 * I + (col & 8 ? I : 0) +
+                        8 * (lane >> 4)) * 2u;
+  const int nb = cnt > 8 ? 2 : 1;
+  if (nb == 1)
+    few_down_rows<FMT, NW, 1, FewShape<FMT>::D>(ws, a, off, I / 128, red);
+  else
+    few_down_rows<FMT, NW, 2, 1>(ws, a, off, I / 128, red);
   __syncthreads();
-  for (int f = w; f < NF; f += NW) {
-    f32x4_t v = red[0][f][lane];
+  for (int u = w; u < nb * NF; u += NW) {
+    const int i = u / NF, f = u % NF;
+    f32x4_t v = red[0][i][f][lane];
 #pragma unroll
-    for (int i = 1; i < NW; ++i) v += red[i][f][lane];
-    if (col < cnt) store(16 * (tile * NF + f) + 4 * (lane >> 4), col, v);
+    for (int k = 1; k < NW; ++k) v += red[k][i][f][lane];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], 8, kWave);
+    const int row = 8 * i + col;
+    if (col < 8 && row < cnt) store(16 * (tile * NF + f) + 4 * (lane >> 4), row, v);
   }
 }
 
 // moe_decode: the rows go out in float32, unweighted; blocks as in gate/up.
 template <int FMT, int NW>
-__global__ void __launch_bounds__(NW * kWave, 2) decode_down_kernel(
+__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_down_kernel(
     int T, int H, int I, WMat routed, WMat shared, int sI, int shared_blocks, DecodePlan plan,
-    const uint16_t* __restrict__ a_hi, const uint16_t* __restrict__ a_lo,
-    const uint16_t* __restrict__ s_hi, const uint16_t* __restrict__ s_lo, float* __restrict__ rows,
+    const uint16_t* __restrict__ a, const uint16_t* __restrict__ s_a, float* __restrict__ rows,
     float* __restrict__ s_rows) {
-  __shared__ f32x4_t red[NW][down_frags<FMT>()][kWave];
-  const int nt = H / (16 * down_frags<FMT>());
+  __shared__ f32x4_t red[NW][2][FewShape<FMT>::NF][kWave];
+  const int nt = H / (16 * FewShape<FMT>::NF);
   int b = blockIdx.x;
-  if (b < shared_blocks) {
-    const int v = b / nt, t0 = v * kCols;
-    float* r = s_rows + (int64_t)t0 * H;
-    few_down<FMT, NW>(shared, 0, b - v * nt, H, sI, s_hi + (int64_t)t0 * sI,
-                      s_lo + (int64_t)t0 * sI, min(kCols, T - t0), red,
-                      [&](int c, int row, f32x4_t v4) {
-                        *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v4;
-                      });
-    return;
-  }
-  b -= shared_blocks;
+  const bool sh = b < shared_blocks;
+  if (!sh) b -= shared_blocks;
   const int j = b / nt;
-  if (j >= *plan.n_entries) return;
-  const int base = plan.entries[j].base;
-  float* r = rows + (int64_t)base * H;
-  few_down<FMT, NW>(routed, plan.entries[j].e, b - j * nt, H, I, a_hi + (int64_t)base * I,
-                    a_lo + (int64_t)base * I, plan.entries[j].cnt, red,
-                    [&](int c, int row, f32x4_t v4) {
-                      *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v4;
+  if (!sh && j >= *plan.n_entries) return;
+  const int g = sh ? 0 : plan.entries[j].e;
+  const int base = sh ? j * kCols : plan.entries[j].base;
+  const int cnt = sh ? min(kCols, T - base) : plan.entries[j].cnt;
+  const int Ic = sh ? sI : I;
+  float* r = (sh ? s_rows : rows) + (int64_t)base * H;
+  few_down<FMT, NW>(sh ? shared : routed, g, b - j * nt, H, Ic,
+                    (sh ? s_a : a) + (int64_t)base * 2 * Ic, cnt, red,
+                    [&](int c, int row, f32x4_t v) {
+                      *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v;
                     });
 }
 
@@ -680,33 +767,33 @@ template <int FMT>
 static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t stream) {
   const DecodeLayout& L = d.L;
   const DecodePlan plan = plan_of(d);
-  uint16_t* a_hi = reinterpret_cast<uint16_t*>(d.ws + L.a_hi);
-  uint16_t* a_lo = reinterpret_cast<uint16_t*>(d.ws + L.a_lo);
-  uint16_t* s_hi = reinterpret_cast<uint16_t*>(d.ws + L.s_hi);
-  uint16_t* s_lo = reinterpret_cast<uint16_t*>(d.ws + L.s_lo);
+  uint16_t* a = reinterpret_cast<uint16_t*>(d.ws + L.a);
+  uint16_t* s_a = reinterpret_cast<uint16_t*>(d.ws + L.s_a);
   float* rows = reinterpret_cast<float*>(d.ws + L.rows);
   float* s_rows = d.sI ? reinterpret_cast<float*>(d.ws + L.s_rows) : nullptr;
-  constexpr int kTile = 8 * GateShape<FMT>::NF;
+  constexpr int kTile = 8 * FewShape<FMT>::NF;
   const int runs = d.sI ? (d.T + kCols - 1) / kCols : 0;
   const int sb = runs * (d.sI / kTile);
   const unsigned gate = (unsigned)(sb + L.max_entries * (d.I / kTile) + (fused ? 1 : 0));
 #define MOE_DECODE_GATE(EPL)                                                                      \
   hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kGateWaves, EPL>), dim3(gate),                     \
                      dim3(kGateWaves * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI,   \
-                     sb, plan, a_hi, a_lo, s_hi, s_lo, d.logits, d.row_valid, d.E, d.K, d.renorm,   \
+                     sb, plan, a, s_a, d.logits, d.row_valid, d.E, d.K, d.renorm,                   \
                      d.expert_begin, d.El, d.topk_idx, d.topk_w)
   if (!fused) MOE_DECODE_GATE(0);
   else if (d.E <= 64) MOE_DECODE_GATE(1);
   else MOE_DECODE_GATE(4);
 #undef MOE_DECODE_GATE
-  const int nt = d.H / (16 * down_frags<FMT>());
+  const int nt = d.H / (16 * FewShape<FMT>::NF);
   hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves>),
                      dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
-                     stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a_hi, a_lo, s_hi,
-                     s_lo, rows, s_rows);
+                     stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a,
+                     rows, s_rows);
   hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
                      dim3(64), 0, stream, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
 }
+
+int launch_route(const float*, const uint8_t*, int, int, int, int, int32_t*, float*, hipStream_t);
 
 int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t* x, int T, int H,
                   int I, int E, int K, int expert_begin, int El, int renorm, int32_t* topk_idx,
@@ -723,19 +810,32 @@ int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t*
   const int64_t most = d.L.max_entries + (T + kCols - 1) / kCols;
   if (most * std::max(std::max(I, sI) / 16, H / 32) >= 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const bool fused = logits && T <= kFusedTokens && T * K <= 64 && E <= 256;
-  const int epl = (E + kWave - 1) / kWave;
 #define MOE_PLAN(N)                                                                             \
   hipLaunchKernelGGL(plan_kernel<N>, dim3(1), dim3(kPlanThreads), 0, stream, logits, row_valid, T, \
                      E, K, renorm, expert_begin, El, topk_idx, topk_w, plan_of(d), dev_error)
+#define MOE_ROUTE_FEW(N)                                                                       \
+  hipLaunchKernelGGL(route_few_kernel<N>, dim3((unsigned)T), dim3(kWave), 0, stream, logits,    \
+                     row_valid, E, K, renorm, topk_idx, topk_w)
   if (!fused) {
+    // one workgroup routes as it plans while it has a wave per token, or 16
+    // lanes (at 64 tokens, top-8: 64 experts 5 us; 256 experts 16 us, in two
+    // launches 8 us)
+    const bool in_plan = logits && (T <= kPlanThreads / kWave ? E <= 256 : E <= 64 && K <= 16 && renorm);
     if (!logits) MOE_PLAN(0);
-    else if (epl <= 1) MOE_PLAN(1);
-    else if (epl <= 2) MOE_PLAN(2);
-    else if (epl <= 4) MOE_PLAN(4);
-    else if (epl <= 8) MOE_PLAN(8);
-    else MOE_PLAN(16);
+    else if (in_plan && E <= 64) MOE_PLAN(1);
+    else if (in_plan) MOE_PLAN(4);
+    else {
+      if (E <= 64) MOE_ROUTE_FEW(1);
+      else if (E <= 256) MOE_ROUTE_FEW(4);
+      else {
+        const int st = launch_route(logits, row_valid, T, E, K, renorm, topk_idx, topk_w, stream);
+        if (st != MOE_OK) return st;
+      }
+      MOE_PLAN(0);
+    }
   }
 #undef MOE_PLAN
+#undef MOE_ROUTE_FEW
   switch (routed->format) {
     case MOE_W_BF16: launch_decode_ffn<MOE_W_BF16>(d, fused, stream); break;
     case MOE_W_FP8: launch_decode_ffn<MOE_W_FP8>(d, fused, stream); break;
@@ -795,30 +895,30 @@ __device__ __forceinline__ bool find_run(int j, const int32_t* __restrict__ cu_s
 }
 
 template <int FMT, int NW>
-__global__ void __launch_bounds__(NW * kWave, 4) few_gate_up_kernel(
+__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) few_gate_up_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ cu_seqlens,
     const int32_t* __restrict__ counts, int G, int H, int I, WMat W, int64_t capacity,
-    uint16_t* __restrict__ a_hi, uint16_t* __restrict__ a_lo, int32_t* __restrict__ dev_error) {
-  __shared__ f32x4_t red[NW][GateShape<FMT>::NF][kWave];
-  const int nt = I / (8 * GateShape<FMT>::NF), j = blockIdx.x / nt;
+    uint16_t* __restrict__ a, int32_t* __restrict__ dev_error) {
+  __shared__ f32x4_t red[NW][FewShape<FMT>::NF][kWave];
+  const int nt = I / (8 * FewShape<FMT>::NF), j = blockIdx.x / nt;
   RowRun r;
   long long total;
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
   const int col = threadIdx.x & 15;
   few_gate_up<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I,
                        uniform_buffer(x + (int64_t)r.row0 * H, (int64_t)r.cnt * H * 2),
-                       (uint32_t)min(col, r.cnt - 1) * H * 2u, r.cnt, a_hi + (int64_t)r.row0 * I,
-                       a_lo + (int64_t)r.row0 * I, red);
+                       (uint32_t)min(col, r.cnt - 1) * H * 2u, r.cnt,
+                       a + (int64_t)r.row0 * 2 * I, red);
 }
 
 template <int FMT, int NW>
-__global__ void __launch_bounds__(NW * kWave, 2) few_down_kernel(
-    const uint16_t* __restrict__ a_hi, const uint16_t* __restrict__ a_lo,
-    const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ counts, int G, int H,
-    int I, WMat W, const float* __restrict__ row_scale, uint16_t* __restrict__ y,
+__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) few_down_kernel(
+    const uint16_t* __restrict__ a, const int32_t* __restrict__ cu_seqlens,
+    const int32_t* __restrict__ counts, int G, int H, int I, WMat W,
+    const float* __restrict__ row_scale, uint16_t* __restrict__ y,
     int64_t capacity, int64_t max_runs, int32_t* __restrict__ dev_error) {
-  __shared__ f32x4_t red[NW][down_frags<FMT>()][kWave];
-  const int nt = H / (16 * down_frags<FMT>()), j = blockIdx.x / nt;
+  __shared__ f32x4_t red[NW][2][FewShape<FMT>::NF][kWave];
+  const int nt = H / (16 * FewShape<FMT>::NF), j = blockIdx.x / nt;
   RowRun r;
   long long total;
   if (blockIdx.x == 0 && threadIdx.x < kWave) {
@@ -828,8 +928,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) few_down_kernel(
       raise_error(dev_error, MOE_DEVERR_ROW_RANGE);
   }
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
-  few_down<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I, a_hi + (int64_t)r.row0 * I,
-                    a_lo + (int64_t)r.row0 * I, r.cnt, red, [&](int c, int i, f32x4_t v) {
+  few_down<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I, a + (int64_t)r.row0 * 2 * I, r.cnt,
+                    red, [&](int c, int i, f32x4_t v) {
                       const int64_t row = r.row0 + i;
                       const float sc = row_scale ? row_scale[row] : 1.0f;
                       *reinterpret_cast<uint2*>(y + row * H + c) =
@@ -846,40 +946,39 @@ static int64_t max_row_runs(int64_t capacity, int G) {
 template <int FMT>
 static int launch_few_fmt(const uint16_t* x, const int32_t* cu, const int32_t* counts, int G,
                           int H, int I, const WMat& w13, const WMat& w2, const float* row_scale,
-                          uint16_t* y, int64_t capacity, int flags, uint16_t* hi, uint16_t* lo,
+                          uint16_t* y, int64_t capacity, int flags, uint16_t* a,
                           int32_t* dev_error, hipStream_t stream) {
   const int64_t runs = max_row_runs(capacity, G);
-  const int64_t gu = runs * (I / (8 * GateShape<FMT>::NF)), dn = runs * (H / (16 * down_frags<FMT>()));
+  const int64_t gu = runs * (I / (8 * FewShape<FMT>::NF)), dn = runs * (H / (16 * FewShape<FMT>::NF));
   if (gu > 0x7fffffff || dn > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   if (flags & MOE_FFN_GATE_UP)
     hipLaunchKernelGGL((few_gate_up_kernel<FMT, kGateWaves>), dim3((unsigned)gu),
                        dim3(kGateWaves * kWave), 0, stream, x, cu, counts, G, H, I, w13, capacity,
-                       hi, lo, dev_error);
+                       a, dev_error);
   if (flags & MOE_FFN_DOWN)
     hipLaunchKernelGGL((few_down_kernel<FMT, kDownWaves>), dim3((unsigned)dn),
-                       dim3(kDownWaves * kWave), 0, stream, hi, lo, cu, counts, G, H, I, w2,
+                       dim3(kDownWaves * kWave), 0, stream, a, cu, counts, G, H, I, w2,
                        row_scale, y, capacity, runs, dev_error);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-// The intermediate: capacity rows of I, high and low parts.
+// The intermediate: capacity rows of I high and I low parts.
 size_t few_ffn_workspace_bytes(int64_t capacity, int I) {
-  return 2 * align256((size_t)capacity * I * 2);
+  return align256((size_t)capacity * I * 4);
 }
 
 int launch_few_ffn(const uint16_t* x, const int32_t* cu, const int32_t* counts, int G, int H,
                    int I, const moe_ffn_weights* wt, const float* row_scale, uint16_t* y,
                    int64_t capacity, int flags, void* workspace, int32_t* dev_error,
                    hipStream_t stream) {
-  uint16_t* hi = static_cast<uint16_t*>(workspace);
-  uint16_t* lo = hi + align256((size_t)capacity * I * 2) / 2;
+  uint16_t* a = static_cast<uint16_t*>(workspace);
   const WMat w13{wt->w13, wt->w13_scales, wt->w13_tensor_scale};
   const WMat w2{wt->w2, wt->w2_scales, wt->w2_tensor_scale};
   if (wt->format == MOE_W_MXFP4)
     return launch_few_fmt<MOE_W_MXFP4>(x, cu, counts, G, H, I, w13, w2, row_scale, y, capacity,
-                                       flags, hi, lo, dev_error, stream);
+                                       flags, a, dev_error, stream);
   return launch_few_fmt<MOE_W_NVFP4>(x, cu, counts, G, H, I, w13, w2, row_scale, y, capacity,
-                                     flags, hi, lo, dev_error, stream);
+                                     flags, a, dev_error, stream);
 }
 
 }  // namespace moe

@@ -12,14 +12,10 @@
 
 namespace moe {
 
-// E8M0 byte -> the float32 power of two 2^(byte - 127) (byte 0: 2^-127, a
-// subnormal)
-__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
-  return __uint_as_float(b ? b << 23 : 0x00400000u);
-}
-
 // 8 E2M1 codes (one dword, code j in bits 4j) times the power of two s, as
-// bf16: exact (2 significant bits), one conversion instruction per pair.
+// bf16: exact (2 significant bits), one conversion instruction per pair.  It
+// reads only the exponent field of s, so that an E8M0 byte shifted there is
+// its scale, 0 meaning 2^-127 (checked on the GPU for all codes and bytes).
 __device__ __forceinline__ bf16x8_t dequant8_mxfp4(uint32_t c, float s) {
   const u32x4_t w = {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
@@ -159,7 +155,7 @@ struct WStream<MOE_W_MXFP4> {
     u32x4_t v;
     uint32_t s;
     __device__ __forceinline__ bf16x8_t operand(int p) const {
-      return dequant8_mxfp4(v[p], e8m0_to_f32((s >> (8 * p)) & 0xffu));
+      return dequant8_mxfp4(v[p], __uint_as_float(((s >> (8 * p)) & 0xffu) << 23));
     }
   };
   buffer_t buf, sbuf;

@@ -266,3 +266,28 @@ def test_no_tokens():
     out, idx, w = ops.moe_decode(torch.empty(0, 4, device="cuda"),
                                  torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), 2, L.handle)
     assert out.shape == (0, 128) and idx.shape == (0, 2)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16, 17, 64])
+@pytest.mark.parametrize("E,K", [(1, 1), (16, 16), (40, 17), (60, 7), (64, 8), (64, 32), (65, 8), (128, 4),
+                                 (200, 9), (256, 8), (257, 3), (700, 20)])
+def test_routes_are_moe_routes(T, E, K, renorm):
+    """Every routing path (in gate/up, in the plan by a wave or by 16 lanes, in
+    a launch of its own) on logits with ties, +-0, infinities and NaN."""
+    rng = np.random.default_rng(T * E + K)
+    logits = rng.integers(-3, 4, (T, E)).astype(np.float32)
+    logits[rng.random((T, E)) < 0.1] = -0.0
+    logits[0, 0] = np.inf
+    logits[T - 1] = rng.standard_normal(E)
+    if T > 2:
+        logits[1] = -np.inf
+        logits[2, ::2] = np.nan
+    valid = (rng.random(T) < 0.8).astype(np.uint8)
+    handle = ops.ffn_weights(torch.zeros(E, 256, 128, dtype=torch.bfloat16, device="cuda"),
+                             torch.zeros(E, 128, 128, dtype=torch.bfloat16, device="cuda"))
+    x = dev_bf16(fu.bf16(rng.standard_normal((T, 128))))
+    _, idx, w = ops.moe_decode(dev(logits), x, K, handle, row_valid=dev(valid), renormalize=renorm)
+    ri, rw = ops.moe_route(dev(logits), K, dev(valid), renorm)
+    assert torch.equal(idx, ri)
+    np.testing.assert_array_equal(host(w).view(np.uint32), host(rw).view(np.uint32))
