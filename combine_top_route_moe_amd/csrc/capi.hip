@@ -40,7 +40,7 @@ int launch_grouped_ffn_w8a8(const uint8_t*, const float*, int64_t, const int32_t
                             hipStream_t);
 int launch_pack_weights_fp4(const uint16_t*, const uint16_t*, int, int, int, int, const float*,
                             const float*, uint8_t*, uint8_t*, uint8_t*, uint8_t*, hipStream_t);
-size_t grouped_ffn_fp4_workspace_bytes(int64_t, int, int);
+size_t grouped_ffn_fp4_workspace_bytes(int64_t, int, int, int);
 int launch_grouped_ffn_fp4(const uint16_t*, const int32_t*, const int32_t*, int, int, int,
                            const moe_ffn_weights*, const float*, uint16_t*, int64_t, int, void*,
                            int32_t*, hipStream_t);
@@ -371,9 +371,8 @@ static bool weights_ok(const moe_ffn_weights* w, int stages) {
 }
 
 size_t moe_grouped_ffn_fp4_workspace_bytes(int64_t capacity, int num_groups, int H, int I) {
-  (void)H;
-  if (capacity < 0 || num_groups < 1 || I < 1) return 0;
-  return grouped_ffn_fp4_workspace_bytes(capacity, num_groups, I);
+  if (capacity < 0 || num_groups < 1 || H < 1 || I < 1) return 0;
+  return grouped_ffn_fp4_workspace_bytes(capacity, num_groups, H, I);
 }
 
 int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int32_t* counts,
@@ -392,7 +391,7 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
   if (((flags & MOE_FFN_GATE_UP) && !x) || ((flags & MOE_FFN_DOWN) && !y))
     return MOE_ERR_INVALID_ARG;
   if ((x && !aligned16(x)) || (y && !aligned16(y))) return MOE_ERR_INVALID_ARG;
-  const size_t need = grouped_ffn_fp4_workspace_bytes(capacity, num_groups, I);
+  const size_t need = grouped_ffn_fp4_workspace_bytes(capacity, num_groups, H, I);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
   return launch_grouped_ffn_fp4(x, cu_seqlens, counts, num_groups, H, I, weights, row_scale, y,

@@ -385,26 +385,21 @@ __global__ void __launch_bounds__(kWave) route_few_kernel(
 // acc[a][i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * B_a^T for NF weight
 // fragments of one column tile and NB 16-column operands out of the buffer b
 // (boff[a]: the byte offset of the lane's column's first element).
-// GU: the first half of the fragments are gate rows, the others the matching
-// up rows, two fragments on.  D blocks are in flight per wave; the loop that
-// refills is free of branches, so that each wait covers one block only.
+// D blocks are in flight per wave; the loop that refills is free of branches,
+// so that each wait covers one block only.
 template <int FMT, int NF, int NB, int D, bool GU>
-__device__ __forceinline__ void few_stream(const WStream<FMT>& ws, buffer_t b,
+__device__ __forceinline__ void few_stream(const WStream<FMT, NF, GU>& ws, buffer_t b,
                                            const uint32_t* boff, int kb0, int step, int nkb,
                                            f32x4_t (*acc)[NF]) {
   struct Buf {
-    typename WStream<FMT>::Block w[NF];
+    typename WStream<FMT, NF, GU>::Tile w;
     u32x4_t x[NB][4];
   } buf[D];
   const int n = kb0 < nkb ? (nkb - kb0 + step - 1) / step : 0;
   if (n == 0) return;
   auto load = [&](Buf& t, int i) {
     const int kb = kb0 + i * step;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const bool up = GU && f >= NF / 2;
-      ws.load(t.w[f], kb, up ? f - NF / 2 + 2 : f, up);
-    }
+    ws.load(t.w, kb);
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
@@ -415,7 +410,7 @@ __device__ __forceinline__ void few_stream(const WStream<FMT>& ws, buffer_t b,
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const bf16x8_t wf = t.w[f].operand(p);
+        const bf16x8_t wf = t.w.operand(f, p);
 #pragma unroll
         for (int a = 0; a < NB; ++a)
           acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -474,7 +469,7 @@ __device__ __forceinline__ void few_gate_up(const WMat& W, int g, int nt, int H,
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = H / 128, ct = nt * NH / 2, f0 = nt * NH % 2;
-  WStream<FMT> ws;
+  WStream<FMT, NF, true> ws;
   ws.init(W, g, ct, f0, I / 32, nkb, 32 * ct, I + 32 * ct, lane);
   f32x4_t acc[1][NF];
 #pragma unroll
@@ -629,7 +624,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
 // 8 rows share one B operand, columns c and c + 8, and are added at the end:
 // one MFMA for both, and half the registers.  9 to 16 rows take two operands.
 template <int FMT, int NW, int NB, int D>
-__device__ __forceinline__ void few_down_rows(const WStream<FMT>& ws, buffer_t a,
+__device__ __forceinline__ void few_down_rows(const WStream<FMT, FewShape<FMT>::NF, false>& ws, buffer_t a,
                                               const uint32_t* off, int nkb,
                                               f32x4_t (*red)[2][FewShape<FMT>::NF][kWave]) {
   constexpr int NF = FewShape<FMT>::NF;
@@ -655,7 +650,7 @@ __device__ __forceinline__ void few_down(const WMat& W, int g, int tile, int H, 
   constexpr int NF = FewShape<FMT>::NF;
   const int lane = threadIdx.x & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  WStream<FMT> ws;
+  WStream<FMT, NF, false> ws;
   ws.init(W, g, tile * NF / 4, tile * NF % 4, H / 64, I / 128, 16 * NF * tile, 0, lane);
   // operand i: columns 0..7 the high parts of rows 8 i .., 8..15 the low ones
   const buffer_t a = uniform_buffer(rows, (int64_t)cnt * I * 4);

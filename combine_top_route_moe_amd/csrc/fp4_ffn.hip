@@ -98,9 +98,9 @@ __global__ void __launch_bounds__(256) pack_weights_fp4_kernel(
   }
   Q[frag * 64 + lane] = u32x4_t{code[0], code[1], code[2], code[3]};
   if constexpr (FMT == MOE_W_MXFP4) {
-    if (lane < 16) S[frag * 16 + lane] = scales;
+    if (lane < 16) S[(t * 16 + lane) * 4 + f] = scales;
   } else {
-    if (!(lane & 16)) S[frag * 32 + (lane >> 5) * 16 + (lane & 15)] = scales;
+    if (!(lane & 16)) S[((t * 2 + (lane >> 5)) * 16 + (lane & 15)) * 4 + f] = scales;
   }
 }
 
@@ -131,11 +131,10 @@ int launch_pack_weights_fp4(const uint16_t* w13, const uint16_t* w2, int G, int 
 // fit one tile, so its weights are read once and stream past the caches.
 template <bool GATE_UP, int FMT, bool NT>
 __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
-                                              const WStream<FMT>& ws, const uint16_t* a_base,
+                                              const WStream<FMT, 4, GATE_UP>& ws, const uint16_t* a_base,
                                               const uint32_t* a_voff, int64_t a_sub_stride,
                                               int a_kb_stride, int w, int lane, int nkb,
                                               int nlive, f32x4_t (*acc)[4]) {
-  using Block = typename WStream<FMT>::Block;
   // the wave fills subtiles 2 w and 2 w + 1 of the K-block, 1 KB per K-step
   auto fill = [&](int kb, int buf) {
     asm volatile("" ::: "memory");
@@ -149,31 +148,28 @@ __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
     }
     asm volatile("" ::: "memory");
   };
-  Block cur[4], nxt[4];
+  typename WStream<FMT, 4, GATE_UP>::Tile cur, nxt;
   fill(0, 0);
-#pragma unroll
-  for (int f = 0; f < 4; ++f) ws.template load<NT>(nxt[f], 0, f);
+  ws.template load<NT>(nxt, 0);
   for (int kb = 0; kb < nkb; ++kb) {
     const int buf = kb & 1;
     // everything in flight is block kb's: its DMA has landed in LDS after
     // this wait and the barrier, and its codes are in the registers
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     lds_barrier();
-#pragma unroll
-    for (int f = 0; f < 4; ++f) cur[f] = nxt[f];
+    cur = nxt;
     if (kb + 1 < nkb) {
       // the other buffer was last read for block kb - 1, which every wave
       // has finished
       fill(kb + 1, buf ^ 1);
-#pragma unroll
-      for (int f = 0; f < 4; ++f) ws.template load<NT>(nxt[f], kb + 1, f);
+      ws.template load<NT>(nxt, kb + 1);
       asm volatile("" ::: "memory");
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       bf16x8_t bfr[4];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) bfr[f] = cur[f].operand(p);
+      for (int f = 0; f < 4; ++f) bfr[f] = cur.operand(f, p);
       u32x4_t a[kTileSub];
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = As[buf][i][p][lane];
@@ -234,7 +230,7 @@ __global__ void __launch_bounds__(kTileWaves * kWave, 2) fp4_tile_kernel(
   const int ct = ct_ok ? cb * kTileWaves + w : n_ct - 1;
   const int nkb = Kdim / 128;
 
-  WStream<FMT> ws;
+  WStream<FMT, 4, GATE_UP> ws;
   ws.init(W, g, ct, 0, n_ct, nkb, 0, 0, lane);
   // gate/up reads the rows themselves (rows past the end re-read the last);
   // down the gate/up kernel's output, in fragment order per m-tile: block
@@ -317,14 +313,36 @@ int launch_few_ffn(const uint16_t*, const int32_t*, const int32_t*, int, int, in
                    const moe_ffn_weights*, const float*, uint16_t*, int64_t, int, void*, int32_t*,
                    hipStream_t);
 
-// Mean rows per group up to which the few-row kernels are used.
-constexpr int64_t kFewMeanRows = 16;
-static bool few_rows(int64_t capacity, int G) { return capacity <= kFewMeanRows * G; }
+// Few-row or tile kernels, by what the host knows.  Both read each weight once
+// while a group has few rows.  The few-row kernels split the reduction over
+// waves, so a few groups fill the GPU, but they read the weights again for
+// every 16 rows (on average every 12 or so).  The tile kernel reads them once
+// per 128 rows, but a workgroup walks the whole reduction by itself, at about
+// 0.9 us a K-block of either stage however few there are: the time in which
+// 42 KB are streamed for each column of H and I.  Where both stream at the
+// memory's rate, sharing the rows through LDS pays from 4 rows a group
+// (NVFP4, whose conversions weigh more there, 8).  Measured, both stages,
+// few / tile in us, MXFP4: H = 4096, I = 1536, 4 groups of 64 rows 42 / 66;
+// 8 groups of 32 rows 43 / 52, of 64 74 / 67; 16 groups of 16 rows 49 / 51, of
+// 24 81 / 55; H = 2048, I = 1024, 64 groups of 1 row 44 / 42, of 8 52 / 43, of
+// 32 112 / 54.  NVFP4, 32 groups (H = 4096, I = 1536) of 4 rows 79 / 91, of 16
+// 102 / 95.
+static bool few_rows(int64_t capacity, int G, int H, int I, int format) {
+  const int64_t active = std::min<int64_t>(G, capacity);
+  if (capacity < (format == MOE_W_MXFP4 ? 4 : 8) * active) return true;
+  const double bytes = 1.6 * H * I;   // an expert's weights
+  const double tile = std::max(active * bytes, 42e3 * ((double)H + I));
+  return std::max<double>(active, capacity / 12.0) * bytes < tile;
+}
 
-size_t grouped_ffn_fp4_workspace_bytes(int64_t capacity, int G, int I) {
-  if (few_rows(capacity, G)) return few_ffn_workspace_bytes(capacity, I);
+// The larger of the two forms' (the choice goes by the weights' format, the
+// size query does not).
+size_t grouped_ffn_fp4_workspace_bytes(int64_t capacity, int G, int H, int I) {
   const int64_t rows = ((capacity + kBM - 1) / kBM + G) * kBM;
-  return (((size_t)rows * I * 2) + 255) & ~(size_t)255;
+  const size_t tile = (((size_t)rows * I * 2) + 255) & ~(size_t)255;
+  if (!few_rows(capacity, G, H, I, MOE_W_NVFP4)) return tile;
+  const size_t few = few_ffn_workspace_bytes(capacity, I);
+  return few_rows(capacity, G, H, I, MOE_W_MXFP4) ? few : std::max(few, tile);
 }
 
 template <int FMT>
@@ -354,7 +372,7 @@ int launch_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu, const int32_t* 
                            int H, int I, const moe_ffn_weights* wt, const float* row_scale,
                            uint16_t* y, int64_t capacity, int flags, void* workspace,
                            int32_t* dev_error, hipStream_t stream) {
-  if (few_rows(capacity, G))
+  if (few_rows(capacity, G, H, I, wt->format))
     return launch_few_ffn(x, cu, counts, G, H, I, wt, row_scale, y, capacity, flags, workspace,
                           dev_error, stream);
   uint16_t* act = static_cast<uint16_t*>(workspace);

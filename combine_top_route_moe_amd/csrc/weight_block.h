@@ -1,7 +1,7 @@
-// One expert-weight fragment as the few-row kernels stream it: 16 weight
-// rows x one 128-wide block of the reduction dimension, in registers, for
-// every weight format, and its conversion to the four bf16 MFMA operands
-// (16 x 32 each) that the block holds.
+// Expert weights as a wave streams them: fragments of 16 weight rows x one
+// 128-wide block of the reduction dimension, in registers, for every weight
+// format, and their conversion to the four bf16 MFMA operands (16 x 32 each)
+// that a fragment's block holds.
 //
 // Lane l holds row l % 16; piece p = 0..3 covers columns 32 p + 8 (l / 16)
 // .. +8 of the block.  Column tiles (64 weight rows, four fragments) and
@@ -84,22 +84,26 @@ struct WMat {
   const float* tensor_scale;
 };
 
-// The stream of a column tile's fragments f0, f0 + 1, .. over the reduction
-// dimension: load(block, kb, f) fetches K-block kb of fragment f0 + f, and
-// Block::operand(p) converts piece p.  g: expert, ct: column tile, n_ct:
-// column tiles, nkb: Kdim / 128.  For w13 `up0` is the first weight row of
-// the tile's up half, whose fragments are 2 and 3 (FP8: the other tile scale).
-template <int FMT>
+// The stream of a column tile's fragments f0 .. f0 + NF - 1 (GU, a w13 tile
+// with NF < 4: NF / 2 gate fragments and the matching up ones, two on) over
+// the reduction dimension: load(t, kb) fetches K-block kb into a Tile in kLoads
+// vector loads, and Tile::operand(f, p) converts piece p of fragment f.  g:
+// expert, ct: column tile, n_ct: column tiles, nkb: Kdim / 128; row0, up0: the
+// tile's first weight row, and of a w13 tile's up half.
+constexpr int frag_of(bool gu, int nf, int f) { return gu && f >= nf / 2 ? f - nf / 2 + 2 : f; }
+
+template <int FMT, int NF, bool GU>
 struct WStream;
 
-template <>
-struct WStream<MOE_W_BF16> {
-  struct Block {
-    u32x4_t v[4];
-    __device__ __forceinline__ bf16x8_t operand(int p) const {
-      return __builtin_bit_cast(bf16x8_t, v[p]);
+template <int NF, bool GU>
+struct WStream<MOE_W_BF16, NF, GU> {
+  struct Tile {
+    u32x4_t v[NF][4];
+    __device__ __forceinline__ bf16x8_t operand(int f, int p) const {
+      return __builtin_bit_cast(bf16x8_t, v[f][p]);
     }
   };
+  static constexpr int kLoads = 4 * NF;
   buffer_t buf;
   uint32_t stride, off;   // bytes between K-steps; the lane's
   __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
@@ -110,20 +114,25 @@ struct WStream<MOE_W_BF16> {
     off = (uint32_t)lane * 16u;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
+  __device__ __forceinline__ void load(Tile& t, int kb) const {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-      b.v[p] = load_b128<NT>(buf, off + f * 1024, (4 * kb + p) * stride);
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        t.v[f][p] = load_b128<NT>(buf, off + frag_of(GU, NF, f) * 1024, (4 * kb + p) * stride);
   }
 };
 
-template <>
-struct WStream<MOE_W_FP8> {
-  struct Block {
-    u32x2_t v[4];
-    float s;
-    __device__ __forceinline__ bf16x8_t operand(int p) const { return dequant8_fp8(v[p], s); }
+template <int NF, bool GU>
+struct WStream<MOE_W_FP8, NF, GU> {
+  struct Tile {
+    u32x2_t v[NF][4];
+    float s[2];   // gate (or all), up
+    __device__ __forceinline__ bf16x8_t operand(int f, int p) const {
+      return dequant8_fp8(v[f][p], s[GU && f >= NF / 2]);
+    }
   };
+  static constexpr int kLoads = 4 * NF;
   buffer_t buf;
   const float* sc;
   const float* sc_up;
@@ -139,79 +148,88 @@ struct WStream<MOE_W_FP8> {
     sc_up = s + (int64_t)(up0 / 128) * nkb;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb, int f, bool up = false) const {
+  __device__ __forceinline__ void load(Tile& t, int kb) const {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-      b.v[p] = load_b64<NT>(buf, off + f * 512, (4 * kb + p) * stride);
-    b.s = up ? sc_up[kb] : sc[kb];
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        t.v[f][p] = load_b64<NT>(buf, off + frag_of(GU, NF, f) * 512, (4 * kb + p) * stride);
+    t.s[0] = sc[kb];
+    t.s[1] = GU ? sc_up[kb] : t.s[0];
   }
 };
 
-// 4-bit codes: a lane's 16 bytes are its whole 32 weights of the block
-// (dword p is piece p); its scales one dword, byte p for piece p.
-template <>
-struct WStream<MOE_W_MXFP4> {
-  struct Block {
-    u32x4_t v;
-    uint32_t s;
-    __device__ __forceinline__ bf16x8_t operand(int p) const {
-      return dequant8_mxfp4(v[p], __uint_as_float(((s >> (8 * p)) & 0xffu) << 23));
+// 4-bit codes, whole column tiles: a lane's 16 bytes per fragment are its 32
+// weights of the block (dword p is piece p), its scales of the four fragments
+// one more 16 bytes (dword f, byte p).
+template <bool GU>
+struct WStream<MOE_W_MXFP4, 4, GU> {
+  struct Tile {
+    u32x4_t v[4];
+    u32x4_t s;
+    __device__ __forceinline__ bf16x8_t operand(int f, int p) const {
+      return dequant8_mxfp4(v[f][p], __uint_as_float(((s[f] >> (8 * p)) & 0xffu) << 23));
     }
   };
+  static constexpr int kLoads = 5;
   buffer_t buf, sbuf;
   uint32_t stride;   // code bytes between K-blocks (scales: 1/16 of them)
   uint32_t off, soff;
-  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
+  __device__ __forceinline__ void init(const WMat& m, int g, int ct, int /*f0*/, int n_ct, int nkb,
                                        int /*row0*/, int /*up0*/, int lane) {
     stride = n_ct * 4096;
-    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096 + f0 * 1024;
+    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096;
     buf = uniform_buffer(static_cast<const char*>(m.w) + g * matrix + at, matrix - at);
     sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (g * matrix + at) / 16,
                           (matrix - at) / 16);
     off = (uint32_t)lane * 16u;
-    soff = (uint32_t)(lane & 15) * 4u;
+    soff = (uint32_t)(lane & 15) * 16u;
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
-    b.v = load_b128<NT>(buf, off + f * 1024, kb * stride);
-    b.s = load_b32<NT>(sbuf, soff + f * 64, kb * (stride / 16));
+  __device__ __forceinline__ void load(Tile& t, int kb) const {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) t.v[f] = load_b128<NT>(buf, off + f * 1024, kb * stride);
+    t.s = load_b128<NT>(sbuf, soff, kb * (stride / 16));
   }
 };
 
-template <>
-struct WStream<MOE_W_NVFP4> {
-  struct Block {
-    u32x4_t v;
-    uint32_t s;
+template <bool GU>
+struct WStream<MOE_W_NVFP4, 4, GU> {
+  struct Tile {
+    u32x4_t v[4];
+    u32x4_t s;
     float g;
-    __device__ __forceinline__ bf16x8_t operand(int p) const {
-      const float b = p == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)s, 0)
-                      : p == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)s, 1)
-                      : p == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)s, 2)
-                               : __builtin_amdgcn_cvt_f32_fp8((int)s, 3);
-      return dequant8_nvfp4(v[p], b * g);
+    __device__ __forceinline__ bf16x8_t operand(int f, int p) const {
+      const int q = (int)s[f];
+      const float b = p == 0   ? __builtin_amdgcn_cvt_f32_fp8(q, 0)
+                      : p == 1 ? __builtin_amdgcn_cvt_f32_fp8(q, 1)
+                      : p == 2 ? __builtin_amdgcn_cvt_f32_fp8(q, 2)
+                               : __builtin_amdgcn_cvt_f32_fp8(q, 3);
+      return dequant8_nvfp4(v[f][p], b * g);
     }
   };
+  static constexpr int kLoads = 5;
   buffer_t buf, sbuf;
   float g;
   uint32_t stride;   // code bytes between K-blocks (scales: 1/8 of them)
   uint32_t off, soff;
-  __device__ __forceinline__ void init(const WMat& m, int grp, int ct, int f0, int n_ct, int nkb,
-                                       int /*row0*/, int /*up0*/, int lane) {
+  __device__ __forceinline__ void init(const WMat& m, int grp, int ct, int /*f0*/, int n_ct,
+                                       int nkb, int /*row0*/, int /*up0*/, int lane) {
     stride = n_ct * 4096;
-    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096 + f0 * 1024;
+    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096;
     buf = uniform_buffer(static_cast<const char*>(m.w) + grp * matrix + at, matrix - at);
     sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (grp * matrix + at) / 8,
                           (matrix - at) / 8);
     off = (uint32_t)lane * 16u;
-    soff = (uint32_t)((lane >> 5) * 16 + (lane & 15)) * 4u;
+    soff = (uint32_t)((lane >> 5) * 16 + (lane & 15)) * 16u;
     g = m.tensor_scale[grp];
   }
   template <bool NT = true>
-  __device__ __forceinline__ void load(Block& b, int kb, int f, bool /*up*/ = false) const {
-    b.v = load_b128<NT>(buf, off + f * 1024, kb * stride);
-    b.s = load_b32<NT>(sbuf, soff + f * 128, kb * (stride / 8));
-    b.g = g;
+  __device__ __forceinline__ void load(Tile& t, int kb) const {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) t.v[f] = load_b128<NT>(buf, off + f * 1024, kb * stride);
+    t.s = load_b128<NT>(sbuf, soff, kb * (stride / 8));
+    t.g = g;
   }
 };
 

@@ -138,9 +138,9 @@ def unpack_fp4(q, s, mode_nv: bool, gate_up: bool):
     c = c.transpose(0, 2, 3, 5, 1, 6, 4, 7)              # g ct f r kb p q4 j
     codes = _rows(c.reshape(G, n_ct, 4, 16, K), gate_up, N)
     if mode_nv:
-        v = s.reshape(G, nkb, n_ct, 4, 2, 16, 4).transpose(0, 2, 3, 5, 1, 6, 4)   # g ct f r kb p h
+        v = s.reshape(G, nkb, n_ct, 2, 16, 4, 4).transpose(0, 2, 5, 4, 1, 6, 3)   # g ct f r kb p h
         return codes, _rows(v.reshape(G, n_ct, 4, 16, K // 16), gate_up, N)
-    v = s.reshape(G, nkb, n_ct, 4, 16, 4).transpose(0, 2, 3, 4, 1, 5)
+    v = s.reshape(G, nkb, n_ct, 16, 4, 4).transpose(0, 2, 4, 3, 1, 5)     # g ct f r kb p
     return codes, _rows(v.reshape(G, n_ct, 4, 16, K // 32), gate_up, N)
 
 

@@ -65,6 +65,10 @@ SHAPES = [
     (64, 256, 2, 2, 128, 128, 2, 0, 0),
     (64, 128, 200, 10, 128, 0, 200, 0, 5),
     (64, 256, 7, 3, 384, 128, 3, 2, 0),
+    # enough experts at work for the row tiles; a few with many tokens
+    (40, 128, 300, 8, 128, 128, 300, 0, 0),
+    (64, 640, 40, 6, 896, 256, 40, 0, 3),
+    (64, 384, 3, 2, 4096, 0, 3, 0, 0),
 ]
 
 

@@ -111,12 +111,13 @@ def _check(y_bits, x, cu, counts, v13, v2, scale, a_step, sentinel=None):
         np.testing.assert_array_equal(y_bits[~covered], sentinel[~covered])
 
 
-# (counts, H, I): few rows a group (at most 16 on average) and many
+# (counts, H, I): few rows a group or few groups, which the few-row kernels take,
+# and the tile kernel's
 FEW = [([1], 128, 128), ([1], 2048, 256), ([16], 256, 128), ([0, 3, 0, 1, 17, 0], 384, 256),
        ([33, 0, 0, 2, 0], 256, 384), ([0] * 70 + [5, 0, 1], 128, 128), ([2] * 130, 128, 128),
-       ([0, 0, 1], 1152, 640)]
-MANY = [([17], 128, 128), ([128], 256, 128), ([129], 384, 256), ([300, 0, 5, 77], 256, 384),
-        ([0, 260, 0], 640, 128), ([40, 20, 31, 64], 1152, 640), ([127, 1, 128, 130], 128, 1152)]
+       ([0, 0, 1], 1152, 640), ([17, 9], 128, 128), ([8, 129], 384, 256)]
+MANY = [([64] * 80, 128, 128), ([1, 0, 130, 65, 64, 63, 16, 17] * 6, 384, 256), ([0, 50] * 18, 640, 1152),
+        ([5000], 128, 128), ([300, 0, 5, 77, 640, 800], 256, 640), ([127, 1, 128, 130, 257, 0], 1152, 896)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -138,13 +139,13 @@ def test_ffn_matches_float64(fmt, case, scaled):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("counts", [[3, 0, 9], [70, 0, 29]])
-def test_rows_outside_the_segments_stay_and_do_not_matter(fmt, counts):
+@pytest.mark.parametrize("counts,I", [([3, 0, 9], 128), ([1000, 0, 429], 2048)])
+def test_rows_outside_the_segments_stay_and_do_not_matter(fmt, counts, I):
     """Unused rows between segments hold NaN and are neither read into other
     rows nor written; a NaN or inf in one row reaches that row only; the
     workspace is not written past its size."""
     rng = np.random.default_rng(7)
-    H, I, G = 256, 128, len(counts)
+    H, G = 256, len(counts)
     handle, v13, v2 = _weights(rng, fmt, G, H, I)
     cu, cap = _segments(counts, pad=3)
     x = fu.bf16(rng.standard_normal((cap, H)))
@@ -171,10 +172,10 @@ def test_rows_outside_the_segments_stay_and_do_not_matter(fmt, counts):
     assert (ws[need:] == 0x5A).all()
 
 
-@pytest.mark.parametrize("rows", [5, 90])
-def test_bad_segments_are_skipped_and_reported(rows):
+@pytest.mark.parametrize("rows,I", [(5, 128), (3000, 768)])
+def test_bad_segments_are_skipped_and_reported(rows, I):
     rng = np.random.default_rng(9)
-    H = I = 128
+    H = 128
     handle, v13, v2 = _weights(rng, "mxfp4", 3, H, I)
     x = fu.bf16(rng.standard_normal((rows, H)))
     half = rows // 2
@@ -193,19 +194,19 @@ def test_bad_segments_are_skipped_and_reported(rows):
     counts = np.array([rows, rows, rows], np.int32)
     ops.moe_grouped_ffn_fp4(dev_bf16(x), dev(np.zeros(4, np.int32)), dev(counts), handle, None, dev_error=err)
     torch.cuda.synchronize()
-    if rows == 90:
+    if rows >= 90:
         ops.moe_grouped_ffn_fp4(dev_bf16(x), dev(np.zeros(4, np.int32)),
                                 dev(np.full(3, 1 << 30, np.int32)), handle, None, dev_error=err)
         assert int(err.item()) == ops.MOE_DEVERR_ROW_RANGE
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("counts", [[2, 5], [60, 33]])
-def test_stages_streams_graphs_and_repeats(fmt, counts):
+@pytest.mark.parametrize("counts,I", [([2, 5], 256), ([760, 350], 1280)])
+def test_stages_streams_graphs_and_repeats(fmt, counts, I):
     """GATE_UP then DOWN equals ALL; another stream; a captured graph replayed
     between eager calls on other inputs; the same bits every time."""
     rng = np.random.default_rng(11)
-    H, I = 384, 256
+    H = 384
     handle, v13, v2 = _weights(rng, fmt, 2, H, I)
     cu, cap = _segments(counts)
     cu_d, n_d = dev(cu), dev(np.array(counts, np.int32))
