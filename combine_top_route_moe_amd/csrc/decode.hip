@@ -15,12 +15,12 @@
 //   down      a workgroup owns a tile of output columns of one entry, its waves
 //             split I; the rows go out unrounded, in float32;
 //   combine   weights and adds each token's rows in slot order, the shared
-//             expert's last, and rounds once.
-// (Down and combine in one launch were tried two ways.  A workgroup per 16
-// columns of all entries has too few workgroups to keep the memory busy: 1.6
-// TB/s at 13 tokens, 64 experts, H = 2048.  Splitting those and adding the
-// parts in the last workgroup to arrive needs a device-wide release in each:
-// writing back the L2s took 150 us at one token.)
+//             expert's last, and rounds once (small layers: within down).
+// (Down and combine in one launch were tried two ways for all sizes.  A
+// workgroup per 16 columns of all entries has too few workgroups to keep the
+// memory busy: 1.6 TB/s at 13 tokens, 64 experts, H = 2048.  Splitting those
+// and adding the parts in the last workgroup to arrive needs a device-wide
+// release in each: writing back the L2s took 150 us at one token.)
 // The products run on the matrix cores with the weights as the A operand (16
 // weight rows) and the tokens as the B operand's 16 columns, so columns are
 // independent: a token sees its own experts only, whatever values the others
@@ -50,7 +50,7 @@ struct PlanEntry {
 
 // The workspace: plan, intermediate rows (routed, then shared), float32 rows.
 struct DecodeLayout {
-  size_t entries, row_tok, row_of, a, s_a, rows, s_rows, total;
+  size_t entries, row_tok, row_of, row_w, a, s_a, rows, s_rows, total;
   int64_t max_entries;
 };
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -67,6 +67,7 @@ static DecodeLayout decode_layout(int T, int H, int I, int K, int El, int sI) {
   L.entries = put((size_t)L.max_entries * sizeof(PlanEntry));
   L.row_tok = put((size_t)rows * 4);
   L.row_of = put((size_t)rows * 4);
+  L.row_w = put((size_t)rows * 4);
   L.a = put((size_t)rows * I * 4);
   L.s_a = put((size_t)T * sI * 4);
   L.rows = put((size_t)rows * H * 4);
@@ -247,6 +248,7 @@ struct DecodePlan {
   PlanEntry* entries;
   int32_t* row_tok;   // token of a compact row
   int32_t* row_of;    // compact row of a slot, -1: no local expert
+  float* row_w;       // weight of a compact row (written by gate/up's plan only)
 };
 
 template <int EPL>
@@ -543,6 +545,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
   constexpr int kTile = 8 * FewShape<FMT>::NF;   // intermediate columns of a workgroup
   __shared__ f32x4_t red[NW][FewShape<FMT>::NF][kWave];
   __shared__ int sel[64];
+  __shared__ float sel_w[64];
   const int lane = threadIdx.x & 63, col = lane & 15;
   const buffer_t xbuf = uniform_buffer(x, (int64_t)T * H * 2);
   int b = blockIdx.x;
@@ -573,6 +576,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
         if (writer) {
           topk_idx[t * K + lane] = e;
           topk_w[t * K + lane] = wt;
+          sel_w[t * K + lane] = wt;
         }
         sel[t * K + lane] = e >= expert_begin && e - expert_begin < El ? e - expert_begin : -1;
       }
@@ -589,6 +593,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
       if (lane < T * K) plan.row_of[lane] = e >= 0 ? pos : -1;
       if (e >= 0) {
         plan.row_tok[pos] = lane / K;
+        plan.row_w[pos] = sel_w[lane];
         if (lead == lane)
           plan.entries[__popcll(p.leaders & ((1ull << lane) - 1))] =
               PlanEntry{e, p.base, (int)__popcll(p.same)};
@@ -702,11 +707,126 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_down
                     });
 }
 
+// ---- moe_decode: down + combine of a small layer ----------------------------------
+// After gate/up's own plan, where the down weights are so few that launches are
+// what counts: a workgroup of 16 waves owns 16 NF output columns of all the (at
+// most 8) tokens.  The blocks of 128 intermediate columns of all entries (the
+// shared expert's last) form one axis, which the waves split evenly; a wave
+// accumulates an entry's rows, high parts in columns 0 .. 7 and low ones in
+// 8 .. 15 as in few_down, and at its end weights them and adds them to the
+// tokens' lanes; the waves' sums are added through LDS in order and rounded.
+// It saves a launch and has few workgroups: one token, 16 experts, top-2, H =
+// 1024, I = 512, bf16, the layer takes 9.3 us instead of 10.2; 64 experts,
+// top-8, H = 2048, I = 1024 29 instead of 25.
+constexpr int64_t kSmallDown = 1 << 20;   // down weights of a call's slots, up to here
+template <int FMT>
+struct FewDownShape {
+  static constexpr int NF = FMT == MOE_W_BF16 || FMT == MOE_W_FP8 ? 2 : 4;
+};
+template <int FMT>
+__global__ void __launch_bounds__(16 * kWave) decode_down_combine_kernel(
+    int T, int H, int I, WMat routed, WMat shared, int sI, DecodePlan plan,
+    const uint16_t* __restrict__ a, const uint16_t* __restrict__ s_a, uint16_t* __restrict__ out) {
+  constexpr int NF = FewDownShape<FMT>::NF, NW = 16, D = 2;
+  __shared__ f32x4_t red[NW][NF][kWave];
+  const int lane = threadIdx.x & 63, col = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ct = blockIdx.x * NF / 4, f0 = blockIdx.x * NF % 4, n_ct = H / 64;
+  const int nb = I / 128, n = *plan.n_entries, nr = n * nb, total = nr + sI / 128;
+  const int b0 = total * w / NW, b1 = total * (w + 1) / NW;
+  f32x4_t tok[NF], acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) tok[f] = acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  struct Buf {
+    typename WStream<FMT, NF, false>::Tile w;
+    u32x4_t x[4];
+  } buf[D];
+  auto load = [&](Buf& t, int b) {
+    const bool sh = b >= nr;
+    const int j = sh ? 0 : b / nb;
+    const int kb = sh ? b - nr : b - j * nb;
+    const PlanEntry en = plan.entries[j];   // (unused past the plan: the shared expert)
+    const int cnt = sh ? T : en.cnt;
+    const int64_t base = sh ? 0 : en.base;
+    const int Ic = sh ? sI : I;
+    WStream<FMT, NF, false> ws;
+    ws.init(sh ? shared : routed, sh ? 0 : en.e, ct, f0, n_ct, Ic / 128, 64 * ct, 0, lane);
+    ws.load(t.w, kb);
+    const buffer_t r = uniform_buffer((sh ? s_a : a) + base * 2 * Ic, (int64_t)cnt * Ic * 4);
+    const uint32_t off =
+        (uint32_t)(min(col & 7, cnt - 1) * 2 * Ic + (col & 8 ? Ic : 0) + 8 * (lane >> 4)) * 2u;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) t.x[p] = load_b128<false>(r, off + p * 64, kb * 256);
+  };
+  auto use = [&](const Buf& t, int b, bool last) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            t.w.operand(f, p), __builtin_bit_cast(bf16x8_t, t.x[p]), acc[f], 0, 0, 0);
+    const bool sh = b >= nr;
+    const int j = sh ? 0 : b / nb;
+    if (!last && b + 1 != (sh ? total : (j + 1) * nb)) return;
+    // the entry (or the wave's part of it) is done: row i is column i, its low
+    // part column i + 8
+    const int cnt = sh ? T : plan.entries[j].cnt, base = sh ? 0 : plan.entries[j].base;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[f][q] += __shfl_xor(acc[f][q], 8, kWave);
+    for (int i = 0; i < cnt; ++i) {
+      const int t_ = sh ? i : plan.row_tok[base + i];
+      const float wt = sh ? 1.0f : plan.row_w[base + i];
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float v = __shfl(acc[f][q], (lane & 48) | i, kWave);
+          tok[f][q] += col == t_ ? wt * v : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  if (b1 > b0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(buf[d], min(b0 + d, b1 - 1));
+    int b = b0;
+    for (; b + 2 * D <= b1; b += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        use(buf[d], b + d, false);
+        load(buf[d], b + d + D);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (b + d < b1) {
+        use(buf[d], b + d, b + d + 1 == b1);
+        if (b + d + D < b1) load(buf[d], b + d + D);
+      }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (b + D + d < b1) use(buf[d], b + D + d, b + D + d + 1 == b1);
+  }
+#pragma unroll
+  for (int f = 0; f < NF; ++f) red[w][f][lane] = tok[f];
+  __syncthreads();
+  if (w >= NF || col >= T) return;
+  f32x4_t v = red[0][w][lane];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) v += red[i][w][lane];
+  *reinterpret_cast<uint2*>(out + (int64_t)col * H + 16 * (blockIdx.x * NF + w) + 4 * (lane >> 4)) =
+      make_uint2(f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16,
+                 f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16);
+}
+
 // ---- moe_decode: combine --------------------------------------------------------
 // out[t] = bf16( sum over the slots in order of w * row, then the shared row ):
 // one thread per 4 columns of a token, 64-thread workgroups.
 __global__ void __launch_bounds__(64) decode_combine_kernel(
-    int H, int K, const int32_t* __restrict__ row_of, const float* __restrict__ topk_w,
+    int T, int H, int K, const int32_t* __restrict__ row_of, const float* __restrict__ topk_w,
     const float* __restrict__ rows, const float* __restrict__ s_rows, uint16_t* __restrict__ out) {
   const int t = blockIdx.y, c = (blockIdx.x * 64 + threadIdx.x) * 4;
   if (c >= H) return;
@@ -720,6 +840,7 @@ __global__ void __launch_bounds__(64) decode_combine_kernel(
     for (int i = 0; i < 8; ++i) {
       const int at = t * K + min(k0 + i, K - 1);
       r[i] = k0 + i < K ? row_of[at] : -1;
+      r[i] = r[i] < T * K ? r[i] : -1;   // never past the rows, whatever the plan holds
       w[i] = topk_w[at];
     }
 #pragma unroll
@@ -755,7 +876,8 @@ struct DecodeArgs {
 static DecodePlan plan_of(const DecodeArgs& d) {
   return {reinterpret_cast<int32_t*>(d.ws), reinterpret_cast<PlanEntry*>(d.ws + d.L.entries),
           reinterpret_cast<int32_t*>(d.ws + d.L.row_tok),
-          reinterpret_cast<int32_t*>(d.ws + d.L.row_of)};
+          reinterpret_cast<int32_t*>(d.ws + d.L.row_of),
+          reinterpret_cast<float*>(d.ws + d.L.row_w)};
 }
 
 template <int FMT>
@@ -779,13 +901,19 @@ static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t strea
   else if (d.E <= 64) MOE_DECODE_GATE(1);
   else MOE_DECODE_GATE(4);
 #undef MOE_DECODE_GATE
+  if (fused && ((int64_t)d.T * d.K * d.I + d.sI) * d.H <= kSmallDown) {
+    hipLaunchKernelGGL((decode_down_combine_kernel<FMT>),
+                       dim3((unsigned)(d.H / (16 * FewDownShape<FMT>::NF))), dim3(16 * kWave), 0,
+                       stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, plan, a, s_a, d.out);
+    return;
+  }
   const int nt = d.H / (16 * FewShape<FMT>::NF);
   hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves>),
                      dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
                      stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a,
                      rows, s_rows);
   hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
-                     dim3(64), 0, stream, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
+                     dim3(64), 0, stream, d.T, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
 }
 
 int launch_route(const float*, const uint8_t*, int, int, int, int, int32_t*, float*, hipStream_t);

@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(256) pack_weights_fp4_kernel(
   const int n_ct = N / 64, nkb = Kdim / 128;
   const int f = (int)(frag & 3);
   const int64_t t = frag >> 2;
-  const int ct = (int)(t % n_ct);
-  const int kb = (int)(t / n_ct % nkb);
+  const int kb = (int)(t % nkb);
+  const int ct = (int)(t / nkb % n_ct);
   const int64_t g = t / n_ct / nkb;
   const int row0 = !gate_up ? 64 * ct + 16 * f : f < 2 ? 32 * ct + 16 * f : N / 2 + 32 * ct + 16 * (f - 2);
   const uint16_t* src = W + (g * N + row0 + (lane & 15)) * Kdim + kb * 128 + 8 * (lane >> 4);

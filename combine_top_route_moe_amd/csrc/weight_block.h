@@ -177,8 +177,8 @@ struct WStream<MOE_W_MXFP4, 4, GU> {
   uint32_t off, soff;
   __device__ __forceinline__ void init(const WMat& m, int g, int ct, int /*f0*/, int n_ct, int nkb,
                                        int /*row0*/, int /*up0*/, int lane) {
-    stride = n_ct * 4096;
-    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096;
+    stride = 4096;
+    const int64_t matrix = (int64_t)nkb * n_ct * 4096, at = (int64_t)ct * nkb * 4096;
     buf = uniform_buffer(static_cast<const char*>(m.w) + g * matrix + at, matrix - at);
     sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (g * matrix + at) / 16,
                           (matrix - at) / 16);
@@ -215,8 +215,8 @@ struct WStream<MOE_W_NVFP4, 4, GU> {
   uint32_t off, soff;
   __device__ __forceinline__ void init(const WMat& m, int grp, int ct, int /*f0*/, int n_ct,
                                        int nkb, int /*row0*/, int /*up0*/, int lane) {
-    stride = n_ct * 4096;
-    const int64_t matrix = (int64_t)nkb * stride, at = ct * 4096;
+    stride = 4096;
+    const int64_t matrix = (int64_t)nkb * n_ct * 4096, at = (int64_t)ct * nkb * 4096;
     buf = uniform_buffer(static_cast<const char*>(m.w) + grp * matrix + at, matrix - at);
     sbuf = uniform_buffer(static_cast<const char*>(m.scales) + (grp * matrix + at) / 8,
                           (matrix - at) / 8);

@@ -44,8 +44,9 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:   # the raw handle: building a Stream object takes 2.7 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def moe_device_check(device: int = 0) -> int:

@@ -382,11 +382,11 @@ int moe_grouped_ffn_w8a8(const uint8_t* xq, const float* x_scales, int64_t scale
  *   float32 (NVFP4; NULL for MXFP4).  Outputs, in 64-row column tiles ct and
  *   fragments f as in moe_pack_ffn_weights, 128-wide K-blocks kb:
  *   w13q [G, 2I, H/2], w2q [G, H, I/2] uint8: 16-byte unit
- *     (((g * (Kdim/128) + kb) * n_ct + ct) * 4 + f) * 64 + l, dword p = 0..3
+ *     (((g * n_ct + ct) * (Kdim/128) + kb) * 4 + f) * 64 + l, dword p = 0..3
  *     of which holds weight row row0(ct, f) + l % 16, columns
  *     128 kb + 32 p + 8 (l / 16) + j in bits 4j .. 4j + 3, j = 0..7;
- *   w13_scales, w2_scales uint8, per K-block and column tile
- *     ((g * (Kdim/128) + kb) * n_ct + ct): MXFP4 [16 rows][4 fragments][4]
+ *   w13_scales, w2_scales uint8, per column tile and K-block
+ *     ((g * n_ct + ct) * (Kdim/128) + kb): MXFP4 [16 rows][4 fragments][4]
  *     bytes, byte p the scale of columns 128 kb + 32 p .. +32 ([G, 2I, H/32]
  *     and [G, H, I/32] bytes in all); NVFP4 [2 halves h][16 rows][4
  *     fragments][4] bytes, byte p the scale of columns

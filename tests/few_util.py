@@ -133,14 +133,14 @@ def unpack_fp4(q, s, mode_nv: bool, gate_up: bool):
     G, N, half = q.shape
     K = 2 * half
     nkb, n_ct = K // 128, N // 64
-    u = q.reshape(G, nkb, n_ct, 4, 4, 16, 4, 4)          # g kb ct f q4 r p byte
-    c = np.stack([u & 15, u >> 4], axis=-1).reshape(G, nkb, n_ct, 4, 4, 16, 4, 8)
-    c = c.transpose(0, 2, 3, 5, 1, 6, 4, 7)              # g ct f r kb p q4 j
+    u = q.reshape(G, n_ct, nkb, 4, 4, 16, 4, 4)          # g ct kb f q4 r p byte
+    c = np.stack([u & 15, u >> 4], axis=-1).reshape(G, n_ct, nkb, 4, 4, 16, 4, 8)
+    c = c.transpose(0, 1, 3, 5, 2, 6, 4, 7)              # g ct f r kb p q4 j
     codes = _rows(c.reshape(G, n_ct, 4, 16, K), gate_up, N)
     if mode_nv:
-        v = s.reshape(G, nkb, n_ct, 2, 16, 4, 4).transpose(0, 2, 5, 4, 1, 6, 3)   # g ct f r kb p h
+        v = s.reshape(G, n_ct, nkb, 2, 16, 4, 4).transpose(0, 1, 5, 4, 2, 6, 3)   # g ct f r kb p h
         return codes, _rows(v.reshape(G, n_ct, 4, 16, K // 16), gate_up, N)
-    v = s.reshape(G, nkb, n_ct, 16, 4, 4).transpose(0, 2, 4, 3, 1, 5)     # g ct f r kb p
+    v = s.reshape(G, n_ct, nkb, 16, 4, 4).transpose(0, 1, 4, 3, 2, 5)     # g ct f r kb p
     return codes, _rows(v.reshape(G, n_ct, 4, 16, K // 32), gate_up, N)
 
 
