@@ -95,12 +95,16 @@ class MoELayer:
         self.packed = False
         self.fp8_weights = False
         self.w8a8 = False
+        self.weights = self.shared_weights = None   # decode()'s handles of the packed weights
+        self.decode_tokens = min(T, ops.MOE_DECODE_MAX_TOKENS)
+        self.decode_ws = torch.empty(max(ops.moe_decode_workspace_bytes(
+            self.decode_tokens, H, I, K, self.El, shared_I), 1), dtype=torch.uint8, device=dev)
 
     # ------------------------------------------------------------------ weights
     def set_weights(self, w13: torch.Tensor, w2: torch.Tensor,
                     shared_w13: Optional[torch.Tensor] = None,
                     shared_w2: Optional[torch.Tensor] = None, pack: bool = True,
-                    fp8=False) -> None:
+                    fp8=False, fp4: Optional[str] = None) -> None:
         """Device bf16 weights: w13 [E_l, 2I, H], w2 [E_l, H, I] (local experts);
         the shared expert's [2Is, H] and [H, Is] (run as a single group).
 
@@ -114,12 +118,36 @@ class MoELayer:
         quantized for real (``moe_quant_rows_fp8``, 1 x 128 blocks) before the
         permute, which moves their codes, and both GEMMs run on the FP8
         matrix cores (``moe_grouped_ffn_w8a8``); this replaces the dispatch
-        fake-quant.  Requires H % 256 == 0."""
+        fake-quant.  Requires H % 256 == 0.  With ``fp4`` ("mxfp4" or
+        "nvfp4") the weights become 4-bit codes with group scales
+        (``moe_pack_ffn_weights_fp4``), routed and shared experts alike, read
+        by ``moe_grouped_ffn_fp4``.  ``decode`` runs on any of these but
+        row-major weights and "w8a8"."""
         if shared_w13 is not None and shared_w13.dim() == 2:
             shared_w13, shared_w2 = shared_w13.unsqueeze(0), shared_w2.unsqueeze(0)
         if fp8 not in (False, True, "w8a8"):
             raise ValueError(f"unknown fp8 mode {fp8!r}")
+        if fp4 not in (None, "mxfp4", "nvfp4"):
+            raise ValueError(f"unknown FP4 format {fp4!r}")
+        if fp4 and (fp8 or not pack):
+            raise ValueError("fp4 weights are packed, and neither fp8")
         self.w8a8 = fp8 == "w8a8"
+        self.weights = self.shared_weights = None
+        fmt = fp4 or ("fp8" if fp8 is True else "bf16" if pack and not fp8 else None)
+        if fmt:
+            self.weights = ops.ffn_weights(w13, w2, fmt)
+            if shared_w13 is not None:
+                self.shared_weights = ops.ffn_weights(shared_w13, shared_w2, fmt)
+        if fp4:
+            self.packed, self.fp8_weights = True, False
+            self.w13 = self.w2 = self.weights
+            self.shared_w13 = self.shared_w2 = self.shared_weights
+            size = ops.moe_grouped_ffn_fp4_workspace_bytes
+            self.ffn_ws = self._workspace(self.ffn_ws, size(self.capacity, self.El, self.H, self.I))
+            if self.shared_I:
+                self.shared_ws = self._workspace(self.shared_ws,
+                                                 size(self.T, 1, self.H, self.shared_I))
+            return
         self.fp8_weights = bool(fp8)
         if self.w8a8:
             self._setup_w8a8()
@@ -133,20 +161,25 @@ class MoELayer:
             return
         if fp8:
             self.packed = True
-            q13, s13, q2, s2 = ops.moe_pack_ffn_weights_fp8(w13, w2)
-            self.w13, self.w2 = (q13, s13), (q2, s2)
+            w, sh = self.weights, self.shared_weights
+            self.w13, self.w2 = (w.w13, w.w13_scales), (w.w2, w.w2_scales)
             self.shared_w13 = self.shared_w2 = None
-            if shared_w13 is not None:
-                q13, s13, q2, s2 = ops.moe_pack_ffn_weights_fp8(shared_w13, shared_w2)
-                self.shared_w13, self.shared_w2 = (q13, s13), (q2, s2)
+            if sh is not None:
+                self.shared_w13, self.shared_w2 = (sh.w13, sh.w13_scales), (sh.w2, sh.w2_scales)
             return
         self.packed = pack
         if pack:
-            w13, w2 = ops.moe_pack_ffn_weights(w13, w2)
+            w13, w2 = self.weights.w13, self.weights.w2
             if shared_w13 is not None:
-                shared_w13, shared_w2 = ops.moe_pack_ffn_weights(shared_w13, shared_w2)
+                shared_w13, shared_w2 = self.shared_weights.w13, self.shared_weights.w2
         self.w13, self.w2 = w13, w2
         self.shared_w13, self.shared_w2 = shared_w13, shared_w2
+
+    def _workspace(self, ws: torch.Tensor, need: int) -> torch.Tensor:
+        """``ws``, or a new buffer where it is too small."""
+        if ws.numel() >= need:
+            return ws
+        return torch.empty(need, dtype=torch.uint8, device=self.device)
 
     def _setup_w8a8(self) -> None:
         """Buffers of the FP8 path: the [T, H] rows' codes and scales, the
@@ -177,6 +210,9 @@ class MoELayer:
             ops.moe_grouped_ffn_w8a8(xq, xs, cu, counts, w13[0], w13[1], w2[0], w2[1], row_scale,
                                      y, stage, ws, self.dev_error, stream=stream, scale_src=src,
                                      scale_div=self.K)
+        elif isinstance(w13, ops.FFNWeights):   # 4-bit weights
+            ops.moe_grouped_ffn_fp4(x, cu, counts, w13, row_scale, y, stage, ws, self.dev_error,
+                                    stream=stream)
         elif self.fp8_weights:
             ops.moe_grouped_ffn_fp8(x, cu, counts, w13[0], w13[1], w2[0], w2[1], row_scale, y,
                                     stage, ws, self.dev_error, stream=stream)
@@ -269,6 +305,31 @@ class MoELayer:
         for _, enqueue in self.stages(logits, hidden, row_valid, overlap_shared=True):
             enqueue()
         return self.out
+
+    def decode(self, logits: Optional[torch.Tensor], hidden: torch.Tensor,
+               row_valid: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer for a few tokens in three launches or so (``moe_decode``):
+        ``hidden`` [n, H] with n <= min(T, 64).  The routes of those n tokens are
+        left in ``topk_idx[:n]`` / ``topk_w[:n]``; with ``logits`` None they are
+        taken from there.  Returns ``out[:n]``.  Enqueue only: no sync, no
+        allocation.  The rows are not rounded before the combine, so the result
+        differs from ``forward``'s by that rounding; a layer with row
+        quantizers (dispatch or combine) has no such form."""
+        if self.weights is None:
+            raise ValueError("decode needs packed weights (set_weights with bf16, fp8=True or fp4)")
+        if self.dispatch_block or self.dispatch_fp4 or self.combine_qdq or self.combine_fp4:
+            raise ValueError("decode has no dispatch or combine quantizers")
+        if self.shared_I and self.shared_weights is None:
+            raise ValueError("the layer has a shared expert, but no weights for it")
+        n = hidden.shape[0]
+        if n > self.decode_tokens:
+            raise ValueError(f"decode takes up to {self.decode_tokens} tokens here, got {n}")
+        ops.moe_decode(logits, hidden, self.K, self.weights, row_valid=row_valid,
+                       renormalize=self.renormalize, expert_begin=self.expert_begin,
+                       num_experts=self.E, shared=self.shared_weights if self.shared_I else None,
+                       topk_idx=self.topk_idx[:n], topk_w=self.topk_w[:n], out=self.out[:n],
+                       workspace=self.decode_ws, dev_error=self.dev_error)
+        return self.out[:n]
 
     def calibrate_combine_scale(self, logits, hidden, row_valid=None) -> torch.Tensor:
         """One-time max calibration of the constant combine-row scale: run the

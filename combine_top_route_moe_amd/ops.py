@@ -43,6 +43,21 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
 
 
+def _one_device(first: torch.Tensor, stream, *others) -> None:
+    """All tensors on the device that the call runs on: the current one, and
+    the stream's."""
+    if not first.is_cuda:
+        raise ValueError("expected a device tensor")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"tensors on {dev}, the stream on {stream.device}")
+
+
 def _stream(stream=None) -> int:
     if stream is None:   # the raw handle: building a Stream object takes 2.7 us a call
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -473,6 +488,8 @@ def moe_pack_ffn_weights_fp4(w13: Optional[torch.Tensor], w2: Optional[torch.Ten
     elif w13 is None:
         raise ValueError("w13 and w2 are both absent")
 
+    _one_device(w13 if w13 is not None else w2, stream, w2, w13_tensor_scale, w2_tensor_scale)
+
     def one(w, g):
         if w is None:
             return None, None, None
@@ -526,6 +543,7 @@ def moe_grouped_ffn_fp4(x: torch.Tensor, cu_seqlens: torch.Tensor, counts: torch
         _want(y, torch.bfloat16, "y")
         if tuple(y.shape) != (capacity, H):
             raise ValueError("y does not match x")
+    _one_device(x, stream, cu_seqlens, counts, row_scale, y, workspace, dev_error, weights.w13)
     lib = load()
     if workspace is None:
         need = lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
@@ -587,6 +605,8 @@ def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, wei
         _want(out, torch.bfloat16, "out")
         if tuple(out.shape) != (T, H):
             raise ValueError("out does not match hidden")
+    _one_device(hidden, stream, logits, row_valid, topk_idx, topk_w, out, workspace, dev_error,
+                weights.w13, shared.w13 if shared is not None else None)
     lib = load()
     shared_I = shared.I if shared is not None else 0
     if workspace is None:

@@ -146,6 +146,8 @@ def test_handles_check_their_tensors():
         ops.ffn_weights(w13.float(), w2, "bf16")
     with pytest.raises(ValueError):
         ops.moe_pack_ffn_weights_fp4(w13, w2, mode=ops.MOE_FQ_BLOCK)
+    with pytest.raises(ValueError, match="device tensor"):
+        ops.moe_pack_ffn_weights_fp4(w13, w2)
 
 
 def test_fast_fake_quantizers_are_the_oracles():

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle
-from combine_top_route_moe_amd import ops
+from combine_top_route_moe_amd import MoELayer, ops
 from oracle.numerics import bf16_bits_to_f32, bf16_bits_to_f64
 from tests import few_util as fu
 from tests.gpu_util import need_gpu, dev, dev_bf16, host, host_bits
@@ -295,3 +295,120 @@ def test_routes_are_moe_routes(T, E, K, renorm):
     ri, rw = ops.moe_route(dev(logits), K, dev(valid), renorm)
     assert torch.equal(idx, ri)
     np.testing.assert_array_equal(host(w).view(np.uint32), host(rw).view(np.uint32))
+
+
+# ---- through the layer ---------------------------------------------------------
+def _layer(fmt, T, H, E, K, I, sI, seed=3):
+    rng = np.random.default_rng(seed)
+    w13, w2 = fu.make_weights(rng, E, H, I)
+    s13, s2 = fu.make_weights(rng, 1, H, sI)
+    layer = MoELayer(T, H, E, K, I, shared_I=sI)
+    kw = {} if fmt == "bf16" else {"fp8": True} if fmt == "fp8" else {"fp4": fmt}
+    layer.set_weights(dev_bf16(w13), dev_bf16(w2), dev_bf16(s13), dev_bf16(s2), **kw)
+    q = lambda m: [fu.fake_quant(x, fmt) for x in m]  # noqa: E731
+    return layer, q(w13), q(w2), (fu.fake_quant(s13[0], fmt), fu.fake_quant(s2[0], fmt)), rng
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_prompt_then_decode_steps(fmt):
+    """The layer as it is served: a prompt through the staged path (for 4-bit
+    weights the grouped FFN on them), then decode steps of changing batches
+    eagerly and from a captured graph, in one layer's buffers."""
+    T, H, E, K, I, sI = 600, 256, 8, 2, 384, 128
+    layer, v13, v2, sv, rng = _layer(fmt, T, H, E, K, I, sI)
+    logits, x = _inputs(rng, T, E, H)
+    prompt = host_bits(layer.forward(dev(logits), dev_bf16(x)))
+    idx, w = host(layer.topk_idx), host(layer.topk_w)
+    ref, bound = fu.layer(x, idx, w, E, 0, v13, v2, sv, a_step=fu.SINGLE)
+    # the staged path also rounds each routed row and the shared one to bf16
+    rows = np.zeros_like(ref)
+    for e in range(E):
+        t, k = np.nonzero(idx == e)
+        y, _ = fu.expert(bf16_bits_to_f64(x[t]), v13[e], v2[e], fu.SINGLE)
+        np.add.at(rows, t, np.abs(w[t, k].astype(np.float64)[:, None] * y))
+    rows += np.abs(fu.expert(bf16_bits_to_f64(x), *sv, fu.SINGLE)[0])
+    fu.check(prompt, ref, bound + 1.01 * fu.BF16_HALF * (rows + bound), "prompt")
+    buf_l, buf_x = torch.zeros(5, E, device="cuda"), torch.zeros(5, H, dtype=torch.bfloat16, device="cuda")
+    layer.decode(buf_l, buf_x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.decode(buf_l, buf_x)
+    for n in (1, 5, 64, 5, 9):
+        logits, x = _inputs(rng, n, E, H)
+        if n == 5:
+            buf_l.copy_(dev(logits))
+            buf_x.copy_(dev_bf16(x))
+            graph.replay()
+            out = layer.out[:5]
+        else:
+            out = layer.decode(dev(logits), dev_bf16(x))
+        torch.cuda.synchronize()
+        idx, w = host(layer.topk_idx[:n]), host(layer.topk_w[:n])
+        np.testing.assert_array_equal(idx, oracle.route(logits, None, K, True)[0])
+        ref, bound = fu.layer(x, idx, w, E, 0, v13, v2, sv)
+        fu.check(host_bits(out), ref, bound, n)
+    # the caller's routes, as another router left them
+    layer.topk_idx[:3] = dev(np.array([[1, 1], [7, 0], [-1, 4]], np.int32))
+    layer.topk_w[:3] = 0.5
+    out = layer.decode(None, dev_bf16(x[:3]))
+    ref, bound = fu.layer(x[:3], host(layer.topk_idx[:3]), host(layer.topk_w[:3]), E, 0, v13, v2, sv)
+    fu.check(host_bits(out), ref, bound, "given")
+    assert int(layer.dev_error.item()) == 0
+
+
+def test_layer_refusals():
+    w13, w2 = fu.make_weights(np.random.default_rng(0), 4, 256, 128)
+    w13, w2 = dev_bf16(w13), dev_bf16(w2)
+    l1 = torch.zeros(1, 4, device="cuda")
+    x1 = torch.zeros(1, 256, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(pack=False), dict(fp8="w8a8")):
+        layer = MoELayer(8, 256, 4, 2, 128)
+        layer.set_weights(w13, w2, **kw)
+        with pytest.raises(ValueError, match="packed weights"):
+            layer.decode(l1, x1)
+    for kw in (dict(combine_qdq=True), dict(dispatch_block=128), dict(dispatch_fp4="mxfp4")):
+        layer = MoELayer(8, 256, 4, 2, 128, **kw)
+        layer.set_weights(w13, w2)
+        with pytest.raises(ValueError, match="quantizers"):
+            layer.decode(l1, x1)
+    layer = MoELayer(8, 256, 4, 2, 128)
+    layer.set_weights(w13, w2)
+    with pytest.raises(ValueError, match="up to 8 tokens"):
+        layer.decode(torch.zeros(9, 4, device="cuda"), torch.zeros(9, 256, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="unknown FP4"):
+        layer.set_weights(w13, w2, fp4="int4")
+    with pytest.raises(ValueError, match="neither"):
+        layer.set_weights(w13, w2, fp4="mxfp4", fp8=True)
+
+
+def test_binding_refusals(monkeypatch):
+    w13, w2 = fu.make_weights(np.random.default_rng(0), 4, 256, 128)
+    h = ops.ffn_weights(dev_bf16(w13), dev_bf16(w2), "mxfp4")
+    l2, x2 = torch.zeros(2, 4, device="cuda"), torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bad = [
+        (ValueError, lambda: ops.moe_decode(l2[:1], x2, 2, h)),
+        (ValueError, lambda: ops.moe_decode(l2, x2[:, :128].contiguous(), 2, h)),
+        (TypeError, lambda: ops.moe_decode(l2.double(), x2, 2, h)),
+        (ValueError, lambda: ops.moe_decode(l2, x2.t().contiguous().t(), 2, h)),       # strides
+        (ValueError, lambda: ops.moe_decode(None, x2, 2, h)),
+        (ValueError, lambda: ops.moe_decode(l2, x2, 2, h, topk_idx=torch.zeros(2, 3, **i32))),
+        (ValueError, lambda: ops.moe_decode(l2, x2, 2, h, out=x2[:1])),
+        (ValueError, lambda: ops.moe_decode(l2, x2, 2, h, shared=h)),
+        (ValueError, lambda: ops.moe_decode(l2.cpu(), x2, 2, h)),
+        (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, expert_begin=1)),
+        (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, out=x2)),
+        (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))),
+        (ValueError, lambda: ops.moe_grouped_ffn_fp4(x2, torch.zeros(4, **i32), torch.zeros(4, **i32), h)),
+        (ValueError, lambda: ops.moe_grouped_ffn_fp4(x2, torch.zeros(5, **i32), torch.zeros(4, **i32), h,
+                                                     torch.zeros(1, device="cuda"))),
+    ]
+    for err, call in bad:
+        with pytest.raises(err):
+            call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)      # another device is current
+    with pytest.raises(ValueError, match="current device"):
+        ops.moe_decode(l2, x2, 2, h)
+    with pytest.raises(ValueError, match="current device"):
+        ops.moe_grouped_ffn_fp4(x2, torch.zeros(5, **i32), torch.zeros(4, **i32), h)
