@@ -370,6 +370,14 @@ static bool weights_ok(const moe_ffn_weights* w, int stages) {
          (!(stages & MOE_FFN_DOWN) || matrix(w->w2, w->w2_scales, w->w2_tensor_scale));
 }
 
+// What the kernels that stream weights address: an expert's matrix (w13, the
+// larger one: 2 I H weights) by 32-bit byte offsets, the rows likewise.
+static bool streamable(int H, int I, int format) {
+  if (H > (1 << 20) || I > (1 << 20)) return false;
+  const int bits = format == MOE_W_BF16 ? 16 : format == MOE_W_FP8 ? 8 : 4;
+  return 2LL * I * H * bits / 8 < 1LL << 32;
+}
+
 size_t moe_grouped_ffn_fp4_workspace_bytes(int64_t capacity, int num_groups, int H, int I) {
   if (capacity < 0 || num_groups < 1 || H < 1 || I < 1) return 0;
   return grouped_ffn_fp4_workspace_bytes(capacity, num_groups, H, I);
@@ -386,6 +394,7 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
   if (capacity > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (!weights || (weights->format != MOE_W_MXFP4 && weights->format != MOE_W_NVFP4))
     return MOE_ERR_INVALID_ARG;
+  if (!streamable(H, I, weights->format)) return MOE_ERR_UNSUPPORTED;
   if (capacity == 0) return MOE_OK;   // no rows: nothing to read or write
   if (!cu_seqlens || !counts || !weights_ok(weights, flags)) return MOE_ERR_INVALID_ARG;
   if (((flags & MOE_FFN_GATE_UP) && !x) || ((flags & MOE_FFN_DOWN) && !y))
@@ -424,6 +433,8 @@ int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hi
     return MOE_ERR_INVALID_ARG;
   if (shared && (!weights_ok(shared, MOE_FFN_ALL) || shared->format != weights->format))
     return MOE_ERR_INVALID_ARG;
+  if (!streamable(H, I, weights->format) || !streamable(H, shared_I, weights->format))
+    return MOE_ERR_UNSUPPORTED;
   if (!aligned16(hidden) || !aligned16(out) || hidden == out) return MOE_ERR_INVALID_ARG;
   const size_t need = decode_workspace_bytes(T, H, I, K, num_local_experts, shared_I);
   if (!workspace || workspace_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;

@@ -165,7 +165,7 @@ __device__ __forceinline__ void select_topk(const int* key, int K, int lane, int
 // Four tokens at once, 16 lanes each, for E <= 64 and K <= 16: lane i of a
 // token's row of lanes holds experts i, i + 16, .. and gets slot i.  Maximum
 // and lowest index come by register moves within the row, nothing passes
-// through scalar registers: 64 tokens of 64 experts, top-8, take the plan 5 us
+// through scalar registers: 64 tokens of 64 experts, top-8, take the plan 6 us
 // instead of the 11 of a wave per token.
 __device__ __forceinline__ int row16_max(int v) {
   v = max(v, row16_dpp<0xB1>(v));

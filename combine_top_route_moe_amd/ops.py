@@ -43,19 +43,40 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
 
 
-def _one_device(first: torch.Tensor, stream, *others) -> None:
-    """All tensors on the device that the call runs on: the current one, and
-    the stream's."""
-    if not first.is_cuda:
+def _one_device(stream, first: torch.Tensor, *others) -> int:
+    """The stream's raw handle, after a check that all tensors are on the device
+    that the call runs on: the current one, and the stream's."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("expected a device tensor")
-    dev = first.device
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"tensors on {dev}, the stream on {stream.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    current = torch.cuda.current_device()
+    if dev != current:
+        raise ValueError(f"tensors on {first.device}, the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device != first.device:
+        raise ValueError(f"tensors on {first.device}, the stream on {stream.device}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A tensor for a call on ``stream``, out of that stream's pool: one of the
+    current stream's could still be in use there, or be handed out again
+    there while the call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _empty(max(need, 1), torch.uint8, device, stream)
+    _want(workspace, torch.uint8, "workspace")
+    return workspace
 
 
 def _stream(stream=None) -> int:
@@ -372,7 +393,7 @@ def moe_grouped_ffn_w8a8(xq: torch.Tensor, x_scales: torch.Tensor, cu_seqlens: t
     return y
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class FFNWeights:
     """Packed expert weights in one format (``MOE_W_*``): what ``moe_decode``
     and ``moe_grouped_ffn_fp4`` take.  Built by ``ffn_weights``, or from the
@@ -418,10 +439,10 @@ class FFNWeights:
                 raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
             if t.device != self.w13.device:
                 raise ValueError(f"{name}: not on the device of w13")
-        self._c = FFNWeightsStruct(self.format, *(
+        object.__setattr__(self, "_c", FFNWeightsStruct(self.format, *(
             _ptr(getattr(self, n)) if n in want else None
             for n in ("w13", "w13_scales", "w13_tensor_scale", "w2", "w2_scales",
-                      "w2_tensor_scale")))
+                      "w2_tensor_scale"))))
 
 
 def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
@@ -436,30 +457,31 @@ def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
     I = two_i // 2
     if tuple(w2.shape) != (G, H, I) or two_i % 2:
         raise ValueError("w13 must be [G, 2I, H] and w2 [G, H, I]")
-    if fmt == "bf16":
-        p13, p2 = moe_pack_ffn_weights(w13, w2, stream=stream)
-        return FFNWeights(MOE_W_BF16, G, H, I, p13, p2)
-    if fmt == "fp8":
-        q13, s13, q2, s2 = moe_pack_ffn_weights_fp8(w13, w2, stream=stream)
-        return FFNWeights(MOE_W_FP8, G, H, I, q13, q2, s13, s2)
-    if fmt not in ("mxfp4", "nvfp4"):
+    if fmt not in ("bf16", "fp8", "mxfp4", "nvfp4"):
         raise ValueError(f"unknown weight format {fmt!r}")
-    mode = MOE_FQ_MXFP4 if fmt == "mxfp4" else MOE_FQ_NVFP4
-    q13, s13, g13, q2, s2, g2 = moe_pack_ffn_weights_fp4(w13, w2, mode, w13_tensor_scale,
-                                                         w2_tensor_scale, stream=stream)
+    _one_device(stream, w13, w2, w13_tensor_scale, w2_tensor_scale)
+    with torch.cuda.stream(stream):   # (the current one where it is None)
+        if fmt == "bf16":
+            p13, p2 = moe_pack_ffn_weights(w13, w2)
+            return FFNWeights(MOE_W_BF16, G, H, I, p13, p2)
+        if fmt == "fp8":
+            q13, s13, q2, s2 = moe_pack_ffn_weights_fp8(w13, w2)
+            return FFNWeights(MOE_W_FP8, G, H, I, q13, q2, s13, s2)
+        mode = MOE_FQ_MXFP4 if fmt == "mxfp4" else MOE_FQ_NVFP4
+        q13, s13, g13, q2, s2, g2 = moe_pack_ffn_weights_fp4(w13, w2, mode, w13_tensor_scale,
+                                                             w2_tensor_scale)
     return FFNWeights(MOE_W_MXFP4 if fmt == "mxfp4" else MOE_W_NVFP4, G, H, I, q13, q2, s13, s2,
                       g13, g2)
 
 
-def _tensor_scales(w: torch.Tensor, stream=None) -> torch.Tensor:
+def _tensor_scales(w: torch.Tensor) -> torch.Tensor:
     """The NVFP4 tensor scale amax / 2688 of every group of w [G, N, K]."""
     G = w.shape[0]
     amax = torch.zeros(G, dtype=torch.float32, device=w.device)
     scale = torch.empty(G, dtype=torch.float32, device=w.device)
     for g in range(G):
-        moe_fake_quant_rows(w[g], mode=MOE_FQ_NVFP4, block=16, amax_out=amax[g:g + 1],
-                            stream=stream)
-        moe_scale_from_amax(amax[g:g + 1], scale[g:g + 1], stream=stream, mode=MOE_FQ_NVFP4)
+        moe_fake_quant_rows(w[g], mode=MOE_FQ_NVFP4, block=16, amax_out=amax[g:g + 1])
+        moe_scale_from_amax(amax[g:g + 1], scale[g:g + 1], mode=MOE_FQ_NVFP4)
     return scale
 
 
@@ -488,7 +510,7 @@ def moe_pack_ffn_weights_fp4(w13: Optional[torch.Tensor], w2: Optional[torch.Ten
     elif w13 is None:
         raise ValueError("w13 and w2 are both absent")
 
-    _one_device(w13 if w13 is not None else w2, stream, w2, w13_tensor_scale, w2_tensor_scale)
+    _one_device(stream, w13 if w13 is not None else w2, w2, w13_tensor_scale, w2_tensor_scale)
 
     def one(w, g):
         if w is None:
@@ -496,7 +518,7 @@ def moe_pack_ffn_weights_fp4(w13: Optional[torch.Tensor], w2: Optional[torch.Ten
         if mode == MOE_FQ_MXFP4:
             g = None
         elif g is None:
-            g = _tensor_scales(w, stream)
+            g = _tensor_scales(w)
         else:
             _want(g, torch.float32, "tensor_scale")
             if tuple(g.shape) != (G,):
@@ -505,11 +527,12 @@ def moe_pack_ffn_weights_fp4(w13: Optional[torch.Tensor], w2: Optional[torch.Ten
         return (torch.empty(G, N, Kd // 2, dtype=torch.uint8, device=w.device),
                 torch.empty(G, N, Kd // group, dtype=torch.uint8, device=w.device), g)
 
-    q13, s13, g13 = one(w13, w13_tensor_scale)
-    q2, s2, g2 = one(w2, w2_tensor_scale)
-    check("moe_pack_ffn_weights_fp4", load().moe_pack_ffn_weights_fp4(
-        _ptr(w13), _ptr(w2), G, H, I, mode, _ptr(g13), _ptr(g2), _ptr(q13), _ptr(s13), _ptr(q2),
-        _ptr(s2), _stream(stream)))
+    with torch.cuda.stream(stream):   # (the current one where it is None)
+        q13, s13, g13 = one(w13, w13_tensor_scale)
+        q2, s2, g2 = one(w2, w2_tensor_scale)
+        check("moe_pack_ffn_weights_fp4", load().moe_pack_ffn_weights_fp4(
+            _ptr(w13), _ptr(w2), G, H, I, mode, _ptr(g13), _ptr(g2), _ptr(q13), _ptr(s13),
+            _ptr(q2), _ptr(s2), _stream()))
     return q13, s13, g13, q2, s2, g2
 
 
@@ -537,21 +560,24 @@ def moe_grouped_ffn_fp4(x: torch.Tensor, cu_seqlens: torch.Tensor, counts: torch
         raise ValueError("counts / cu_seqlens do not match the number of groups")
     if row_scale is not None and row_scale.numel() < capacity:
         raise ValueError("row_scale is shorter than x")
-    if y is None:
-        y = torch.empty(capacity, H, dtype=torch.bfloat16, device=x.device)
-    else:
+    if dev_error is not None:
+        _want(dev_error, torch.int32, "dev_error")
+    if y is not None:
         _want(y, torch.bfloat16, "y")
         if tuple(y.shape) != (capacity, H):
             raise ValueError("y does not match x")
-    _one_device(x, stream, cu_seqlens, counts, row_scale, y, workspace, dev_error, weights.w13)
+    raw = _one_device(stream, x, cu_seqlens, counts, row_scale, y, workspace, dev_error,
+                      weights.w13)
     lib = load()
-    if workspace is None:
-        need = lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if y is None:
+        y = _empty((capacity, H), torch.bfloat16, x.device, stream)
+    need = (lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
+            if workspace is None else 0)
+    workspace = _workspace(workspace, need, x.device, stream)
     check("moe_grouped_ffn_fp4", lib.moe_grouped_ffn_fp4(
         _ptr(x), _ptr(cu_seqlens), _ptr(counts), G, H, I, ctypes.addressof(weights._c),
         _ptr(row_scale), _ptr(y), capacity, flags, _ptr(workspace), workspace.numel(),
-        _ptr(dev_error), _stream(stream)))
+        _ptr(dev_error), raw))
     return y
 
 
@@ -585,39 +611,44 @@ def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, wei
         raise ValueError("without logits, topk_idx and topk_w are needed")
     elif num_experts is None:
         num_experts = expert_begin + weights.num_groups
-    if topk_idx is None:
-        topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
-    if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
-    _want(topk_idx, torch.int32, "topk_idx")
-    _want(topk_w, torch.float32, "topk_w")
-    if tuple(topk_idx.shape) != (T, k) or tuple(topk_w.shape) != (T, k):
-        raise ValueError("topk_idx and topk_w must be [T, k]")
+    if topk_idx is not None:
+        _want(topk_idx, torch.int32, "topk_idx")
+        if topk_idx.shape != (T, k):
+            raise ValueError("topk_idx must be [T, k]")
+    if topk_w is not None:
+        _want(topk_w, torch.float32, "topk_w")
+        if topk_w.shape != (T, k):
+            raise ValueError("topk_w must be [T, k]")
+    if dev_error is not None:
+        _want(dev_error, torch.int32, "dev_error")
     if row_valid is not None:
         _want(row_valid, torch.uint8, "row_valid")
         if row_valid.numel() != T:
             raise ValueError("row_valid must be [T]")
     if weights.H != H or (shared is not None and (shared.H != H or shared.num_groups != 1)):
         raise ValueError("weight shapes do not match hidden")
-    if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    else:
+    if out is not None:
         _want(out, torch.bfloat16, "out")
-        if tuple(out.shape) != (T, H):
+        if out.shape != (T, H):
             raise ValueError("out does not match hidden")
-    _one_device(hidden, stream, logits, row_valid, topk_idx, topk_w, out, workspace, dev_error,
-                weights.w13, shared.w13 if shared is not None else None)
+    raw = _one_device(stream, hidden, logits, row_valid, topk_idx, topk_w, out, workspace, dev_error,
+                      weights.w13, shared.w13 if shared is not None else None)
     lib = load()
     shared_I = shared.I if shared is not None else 0
-    if workspace is None:
-        need = lib.moe_decode_workspace_bytes(T, H, weights.I, k, weights.num_groups, shared_I)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if topk_idx is None:
+        topk_idx = _empty((T, k), torch.int32, dev, stream)
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, dev, stream)
+    if out is None:
+        out = _empty((T, H), torch.bfloat16, dev, stream)
+    need = (lib.moe_decode_workspace_bytes(T, H, weights.I, k, weights.num_groups, shared_I)
+            if workspace is None else 0)
+    workspace = _workspace(workspace, need, dev, stream)
     check("moe_decode", lib.moe_decode(
         _ptr(logits), _ptr(row_valid), _ptr(hidden), T, H, weights.I, num_experts, k, expert_begin,
         weights.num_groups, MOE_ROUTE_RENORM if renormalize else 0, _ptr(topk_idx), _ptr(topk_w),
         ctypes.addressof(weights._c), ctypes.addressof(shared._c) if shared is not None else None,
-        shared_I, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_error),
-        _stream(stream)))
+        shared_I, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_error), raw))
     return out, topk_idx, topk_w
 
 

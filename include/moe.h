@@ -392,7 +392,7 @@ int moe_grouped_ffn_w8a8(const uint8_t* xq, const float* x_scales, int64_t scale
  *     fragments][4] bytes, byte p the scale of columns
  *     128 kb + 32 p + 16 h .. +16 ([G, 2I, H/16], [G, H, I/16]).
  * Either matrix (its weights, codes and scales) may be NULL altogether.
- * Pointers 16-byte aligned.  Runs once at load time.
+ * Pointers 16-byte aligned; finite weights.  Runs once at load time.
  * Requires H % 128 == 0, I % 128 == 0. */
 int moe_pack_ffn_weights_fp4(const uint16_t* w13, const uint16_t* w2, int num_groups, int H,
                              int I, int mode, const float* w13_tensor_scale,
@@ -407,7 +407,8 @@ int moe_pack_ffn_weights_fp4(const uint16_t* w13, const uint16_t* w2, int num_gr
  * bits (two bf16 numbers), else it is rounded once to bf16 as in
  * moe_grouped_ffn.  A DOWN-only call needs the workspace of a GATE_UP call
  * with the same capacity, groups and segments.  Rows outside every segment
- * are neither read nor written. */
+ * are neither read nor written.  Requires H % 128 == I % 128 == 0, both
+ * <= 2^20, H * I < 2^32, num_groups <= 1024, capacity < 2^31. */
 size_t moe_grouped_ffn_fp4_workspace_bytes(int64_t capacity, int num_groups, int H, int I);
 int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int32_t* counts,
                         int num_groups, int H, int I, const moe_ffn_weights* weights,
@@ -416,24 +417,26 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
                         void* stream);
 
 /* ---- the whole layer for a few tokens --------------------------------------
- * Route, experts, weighting and combine of up to 64 tokens in three launches,
- * with no permuted rows in between: for each token t with row_valid[t] != 0,
- * over its chosen local experts e_k (slots as moe_route defines them, the
- * local range as in moe_permute),
+ * Route, experts, weighting and combine of up to 64 tokens in two to five
+ * launches, with no permuted rows in between: for each token t with
+ * row_valid[t] != 0, over its chosen local experts e_k (slots as moe_route
+ * defines them, the local range as in moe_permute),
  *   out[t] = bf16( sum_k w_k * W2[e_k] (silu(g_k) * u_k)  +  shared_t ),
  *   g_k = W13[e_k][:I] x_t,  u_k = W13[e_k][I:] x_t,
  * shared_t the shared expert's row for every token, padding ones included.
  * Products, sums and weighting are float32 with one rounding to bf16 at the
- * end (silu(g) * u keeps 16 significant bits); the sum runs over the experts
- * in ascending order.  (The staged calls round each expert's row to bf16
- * before the combine; this call does not, and has no row quantizers.)
- * Repeated calls give the same bits.
+ * end (silu(g) * u keeps 16 significant bits).  The order of the sum is fixed
+ * for given sizes and routes, so repeated calls give the same bits; a token's
+ * bits may differ with the batch it is in.  (The staged calls round each
+ * expert's row to bf16 before the combine; this call does not, and has no row
+ * quantizers.)
  *   logits [T, E] float32, row_valid [T] uint8 or NULL: topk_idx, topk_w
  *     [T, K] are written, bit for bit as moe_route does;
  *   logits NULL: topk_idx and topk_w are inputs (a router of the caller's);
  *     a negative id is a padding slot, an id >= num_experts names no expert,
  *     is skipped and raises MOE_DEVERR_EXPERT_RANGE; a token may name one
  *     expert in several slots (their weights add up); row_valid still masks.
+ *     topk_w of a slot without a local expert is not used.
  *   hidden [T, H], out [T, H] bf16 (out must not alias hidden)
  *   weights  the local experts' (G = num_local_experts); shared NULL or the
  *     shared expert's (G = 1, intermediate size shared_I, the same format;
@@ -441,8 +444,9 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
  *   workspace of moe_decode_workspace_bytes(), contents on entry ignored.
  * flags: MOE_ROUTE_RENORM.  A token without a local expert and without a
  * shared row gets +0.  T = 0 enqueues nothing.
- * Requires T <= 64, H % 128 == I % 128 == shared_I % 128 == 0,
- * K <= min(num_experts, 32), num_experts <= 1024. */
+ * Requires T <= 64, H % 128 == I % 128 == shared_I % 128 == 0, each of them
+ * <= 2^20, K <= min(num_experts, 32), num_experts <= 1024, and every expert's
+ * w13 and w2 in less than 4 GiB each. */
 size_t moe_decode_workspace_bytes(int T, int H, int I, int K, int num_local_experts,
                                   int shared_I);
 int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hidden, int T,

@@ -115,6 +115,27 @@ def test_decode_refuses_mismatched_weights(lib):
     assert _decode(lib, _weights(4)) == INVALID
 
 
+def test_matrices_past_32_bit_offsets_are_refused(lib):
+    """An expert's w13 in 4 GiB or more, or a dimension past 2^20; the largest
+    below reach the workspace check."""
+    for fmt, bits in ((ops.MOE_W_BF16, 16), (ops.MOE_W_FP8, 8), (ops.MOE_W_MXFP4, 4), (ops.MOE_W_NVFP4, 4)):
+        w, H = _weights(fmt), 1 << 15
+        I = (1 << 32) * 8 // bits // 2 // H                  # w13: 2^32 bytes
+        for h, i, status in ((H, I, UNSUPPORTED), (H, I - 128, WORKSPACE), (1 << 20, 128, WORKSPACE),
+                             ((1 << 20) + 128, 128, UNSUPPORTED), (128, (1 << 20) + 128, UNSUPPORTED)):
+            assert _decode(lib, w, H=h, I=i, ws=None) == status, (fmt, h, i)
+            if fmt in (ops.MOE_W_MXFP4, ops.MOE_W_NVFP4):
+                assert _ffn(lib, w, H=h, I=i, ws=None) == status, (fmt, h, i)
+        assert _decode(lib, w, s=w, H=H, sI=I, ws=None) == UNSUPPORTED
+
+
+def test_handles_do_not_change():
+    q = torch.zeros(2, 256, 128, dtype=torch.uint8)
+    for name in ("w13", "format", "H"):
+        with pytest.raises(AttributeError):
+            setattr(ops.FFNWeights.__new__(ops.FFNWeights), name, q)
+
+
 def test_size_queries(lib):
     need = ops.moe_decode_workspace_bytes(64, 7168, 2048, 8, 256, 2048)
     assert need >= 64 * 9 * 2048 * 4

@@ -69,6 +69,7 @@ SHAPES = [
     (40, 128, 300, 8, 128, 128, 300, 0, 0),
     (64, 640, 40, 6, 896, 256, 40, 0, 3),
     (64, 384, 3, 2, 4096, 0, 3, 0, 0),
+    (64, 128, 1024, 32, 128, 128, 1024, 0, 0),      # all the entries there can be
 ]
 
 
@@ -248,6 +249,32 @@ def test_graphs_streams_and_repeats(fmt):
     assert torch.equal(out, cases[3][3][1][0])
 
 
+@pytest.mark.parametrize("T", [2, 30])
+def test_two_calls_at_once(T):
+    """Calls on two streams at a time, each with workspace and outputs of its
+    own, allocated by the binding on the call's stream: the bits of a call
+    alone.  The side stream's packing, too."""
+    H, I, E, K = 512, 1024, 32, 4
+    rng = np.random.default_rng(T)
+    w13, w2 = (dev_bf16(m) for m in fu.make_weights(rng, E, H, I))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    handles = [ops.ffn_weights(w13, w2, "nvfp4", stream=s) for s in streams]
+    torch.cuda.synchronize()
+    for n in ("w13", "w13_scales", "w13_tensor_scale", "w2", "w2_scales", "w2_tensor_scale"):
+        assert torch.equal(getattr(handles[0], n), getattr(handles[1], n))
+    ins = [tuple(f(a) for f, a in zip((dev, dev_bf16), _inputs(rng, T, E, H))) for _ in range(2)]
+    want = [ops.moe_decode(a, b, K, handles[0])[0] for a, b in ins]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(12):
+        for i in (0, 1):
+            got[i].append(ops.moe_decode(*ins[i], K, handles[i], stream=streams[i])[0])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_expert_parallel_shares_add_up():
     """The shares of two ranks, added, are the whole layer: each share is off
     by its own bound."""
@@ -399,6 +426,8 @@ def test_binding_refusals(monkeypatch):
         (ValueError, lambda: ops.moe_decode(l2.cpu(), x2, 2, h)),
         (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, expert_begin=1)),
         (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, out=x2)),
+        (TypeError, lambda: ops.moe_decode(l2, x2, 2, h, workspace=torch.zeros(1 << 20, device="cuda"))),
+        (TypeError, lambda: ops.moe_decode(l2, x2, 2, h, dev_error=torch.zeros(1, device="cuda"))),
         (RuntimeError, lambda: ops.moe_decode(l2, x2, 2, h, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))),
         (ValueError, lambda: ops.moe_grouped_ffn_fp4(x2, torch.zeros(4, **i32), torch.zeros(4, **i32), h)),
         (ValueError, lambda: ops.moe_grouped_ffn_fp4(x2, torch.zeros(5, **i32), torch.zeros(4, **i32), h,
