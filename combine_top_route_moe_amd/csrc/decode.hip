@@ -28,6 +28,7 @@
 // bits) and multiplied in two MFMAs, so no intermediate is rounded to bf16;
 // sums are float32 throughout.
 #include <algorithm>
+#include <type_traits>
 
 #include "route_common.h"
 #include "weight_block.h"
@@ -384,73 +385,62 @@ __global__ void __launch_bounds__(kWave) route_few_kernel(
 }
 
 // ---- the streamed product ---------------------------------------------------
-// acc[a][i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * B_a^T for NF weight
-// fragments of one column tile and NB 16-column operands out of the buffer b
-// (boff[a]: the byte offset of the lane's column's first element).
-// D blocks are in flight per wave; the loop that refills is free of branches,
-// so that each wait covers one block only.
-template <int FMT, int NF, int NB, int D, bool GU>
+// acc[i] += W_i[16 rows, blocks kb0, kb0 + step, ..] * (sum over a of B_a)^T for
+// NF weight fragments of one column tile and NB 16-column operands out of the
+// buffer b (boff[a]: the byte offset of the lane's column's first element).
+// A wave has one block in flight, into registers that the block before leaves
+// free as its MFMAs go; the waves of the other workgroups on the CU cover the
+// wait.  (Two in flight, with fewer waves: MXFP4 4 to 8 % longer at 8 tokens and
+// as long at one; NVFP4 52 us for 333 rows of ragged experts instead of 49; the
+// same for bf16 and FP8.)
+template <int FMT, int NF, int NB, bool GU>
 __device__ __forceinline__ void few_stream(const WStream<FMT, NF, GU>& ws, buffer_t b,
                                            const uint32_t* boff, int kb0, int step, int nkb,
-                                           f32x4_t (*acc)[NF]) {
-  struct Buf {
-    typename WStream<FMT, NF, GU>::Tile w;
-    u32x4_t x[NB][4];
-  } buf[D];
-  const int n = kb0 < nkb ? (nkb - kb0 + step - 1) / step : 0;
-  if (n == 0) return;
-  auto load = [&](Buf& t, int i) {
-    const int kb = kb0 + i * step;
-    ws.load(t.w, kb);
+                                           f32x4_t* acc) {
+  typename WStream<FMT, NF, GU>::Tile w;
+  u32x4_t x[NB][4];
+  auto load = [&](int kb) {
+    ws.load(w, kb);
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
-      for (int p = 0; p < 4; ++p) t.x[a][p] = load_b128<false>(b, boff[a] + p * 64, kb * 256);
+      for (int p = 0; p < 4; ++p) x[a][p] = load_b128<false>(b, boff[a] + p * 64, kb * 256);
   };
-  auto use = [&](const Buf& t) {
+  auto use = [&]() {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const bf16x8_t wf = t.w.operand(f, p);
+        const bf16x8_t wf = w.operand(f, p);
 #pragma unroll
         for (int a = 0; a < NB; ++a)
-          acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              wf, __builtin_bit_cast(bf16x8_t, t.x[a][p]), acc[a][f], 0, 0, 0);
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              wf, __builtin_bit_cast(bf16x8_t, x[a][p]), acc[f], 0, 0, 0);
       }
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(buf[d], min(d, n - 1));
-  int i = 0;
-  for (; i + 2 * D <= n; i += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      use(buf[d]);
-      load(buf[d], i + d + D);
-    }
+  if (kb0 >= nkb) return;
+  load(kb0);
+  for (int kb = kb0 + step; kb < nkb; kb += step) {
+    use();
+    load(kb);
   }
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (i + d < n) {
-      use(buf[d]);
-      if (i + d + D < n) load(buf[d], i + d + D);
-    }
-#pragma unroll
-  for (int d = 0; d < D - 1; ++d)
-    if (i + D + d < n) use(buf[d]);
+  use();
 }
 
 // The shape of a few-row product, by format: NF fragments a wave (gate/up: half
-// gate, half up), D blocks in flight per wave, kWaves waves to a SIMD (what the
-// registers of that allow).  bf16 blocks are large (4 KB a fragment): two
-// fragments; the narrower formats take a whole 64-row column tile, which reads
-// each row of x, or of a, for four fragments.
-template <int FMT>
+// gate, half up), kWaves waves to a SIMD (what the registers of that allow).
+// bf16 blocks are large (4 KB a fragment): two fragments; the narrower formats
+// take a whole 64-row column tile, which reads each row of x, or of a, for
+// four fragments.  FP8 halves the fragments (NARROW) while the launch has so few workgroups
+// that all of them run at once: one token, 8 experts, H = 2048, I = 1024 19 us
+// instead of 22; with many, reading x twice as often costs more: 40 tokens, 64
+// experts, H = 7168, I = 2048 554 us instead of 459.
+template <int FMT, bool NARROW = false>
 struct FewShape {
-  static constexpr int NF = FMT == MOE_W_BF16 ? 2 : 4;
-  static constexpr int D = 2;
-  static constexpr int kWaves = FMT == MOE_W_FP8 ? 3 : 4;
+  static constexpr int NF = FMT == MOE_W_BF16 || NARROW ? 2 : 4;
+  static constexpr int kWaves = FMT == MOE_W_FP8 && !NARROW ? 4 : 5;
 };
+constexpr int64_t kNarrowWgs = 3 * 256;   // three to a CU
 
 // v as the sum of two bf16 numbers, high part first
 __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
@@ -462,24 +452,24 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) 
 // the cnt <= 16 rows whose x this lane's column is at byte xoff of x (columns
 // past cnt repeat the last one and are not stored).  a rows go to a + column *
 // 2 I, the I high parts before the I low ones.
-template <int FMT, int NW>
+template <int FMT, int NW, typename Shape>
 __device__ __forceinline__ void few_gate_up(const WMat& W, int g, int nt, int H, int I,
                                             buffer_t x, uint32_t xoff, int cnt,
                                             uint16_t* a,
-                                            f32x4_t (*red)[FewShape<FMT>::NF][kWave]) {
-  constexpr int NF = FewShape<FMT>::NF, NH = NF / 2;   // NH gate and NH up fragments
+                                            f32x4_t (*red)[Shape::NF][kWave]) {
+  constexpr int NF = Shape::NF, NH = NF / 2;   // NH gate and NH up fragments
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = H / 128, ct = nt * NH / 2, f0 = nt * NH % 2;
   WStream<FMT, NF, true> ws;
   ws.init(W, g, ct, f0, I / 32, nkb, 32 * ct, I + 32 * ct, lane);
-  f32x4_t acc[1][NF];
+  f32x4_t acc[NF];
 #pragma unroll
-  for (int i = 0; i < NF; ++i) acc[0][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const uint32_t off[1] = {xoff + 16 * (lane >> 4)};
-  few_stream<FMT, NF, 1, FewShape<FMT>::D, true>(ws, x, off, w, NW, nkb, acc);
+  few_stream<FMT, NF, 1, true>(ws, x, off, w, NW, nkb, acc);
 #pragma unroll
-  for (int i = 0; i < NF; ++i) red[w][i][lane] = acc[0][i];
+  for (int i = 0; i < NF; ++i) red[w][i][lane] = acc[i];
   __syncthreads();
   if (w >= NH) return;
   f32x4_t gt = red[0][w][lane], up = red[0][NH + w][lane];
@@ -535,15 +525,16 @@ __device__ __forceinline__ SmallPlan small_plan(int e, int n_slots, int T, int l
 // was made; every workgroup routes the (few) tokens itself, and one more at the
 // end of the grid writes the plan for the down kernel.  That saves a launch,
 // 5 us, and costs each workgroup about 1.
-template <int FMT, int NW, int EPL>
-__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate_up_kernel(
+template <int FMT, int NW, bool NARROW, int EPL>
+__global__ void __launch_bounds__(NW * kWave, (FewShape<FMT, NARROW>::kWaves)) decode_gate_up_kernel(
     const uint16_t* __restrict__ x, int T, int H, int I, WMat routed, WMat shared, int sI,
     int shared_blocks, DecodePlan plan, uint16_t* __restrict__ a, uint16_t* __restrict__ s_a,
     const float* __restrict__ logits,
     const uint8_t* __restrict__ row_valid, int E, int K, int renorm, int expert_begin, int El,
     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
-  constexpr int kTile = 8 * FewShape<FMT>::NF;   // intermediate columns of a workgroup
-  __shared__ f32x4_t red[NW][FewShape<FMT>::NF][kWave];
+  using Shape = FewShape<FMT, NARROW>;
+  constexpr int kTile = 8 * Shape::NF;   // intermediate columns of a workgroup
+  __shared__ f32x4_t red[NW][Shape::NF][kWave];
   __shared__ int sel[64];
   __shared__ float sel_w[64];
   const int lane = threadIdx.x & 63, col = lane & 15;
@@ -617,7 +608,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
     cnt = plan.entries[j].cnt;
     tok = plan.row_tok[base + min(col, cnt - 1)];
   }
-  few_gate_up<FMT, NW>(sh ? shared : routed, g, b - j * nt, H, Ic, xbuf,
+  few_gate_up<FMT, NW, Shape>(sh ? shared : routed, g, b - j * nt, H, Ic, xbuf,
                           (uint32_t)tok * H * 2u, cnt, (sh ? s_a : a) + (int64_t)base * 2 * Ic,
                           red);
 }
@@ -627,69 +618,63 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_gate
 // (each I high parts, then I low ones), for expert g; store(first of four
 // columns, row, their sums) for every row.  The high and the low part of up to
 // 8 rows share one B operand, columns c and c + 8, and are added at the end:
-// one MFMA for both, and half the registers.  9 to 16 rows take two operands.
-template <int FMT, int NW, int NB, int D>
-__device__ __forceinline__ void few_down_rows(const WStream<FMT, FewShape<FMT>::NF, false>& ws, buffer_t a,
+// one MFMA and one read of a for both.  9 to 16 rows take two operands, into
+// the same sums.
+template <int FMT, int NF, int NW, int NB>
+__device__ __forceinline__ void few_down_rows(const WStream<FMT, NF, false>& ws, buffer_t a,
                                               const uint32_t* off, int nkb,
-                                              f32x4_t (*red)[2][FewShape<FMT>::NF][kWave]) {
-  constexpr int NF = FewShape<FMT>::NF;
+                                              f32x4_t (*red)[NF][kWave]) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  f32x4_t acc[NB][NF];
+  f32x4_t acc[NF];
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  few_stream<FMT, NF, NB, false>(ws, a, off, w, NW, nkb, acc);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  few_stream<FMT, NF, NB, D, false>(ws, a, off, w, NW, nkb, acc);
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) red[w][i][f][lane] = acc[i][f];
+  for (int f = 0; f < NF; ++f) red[w][f][lane] = acc[f];
 }
 
-template <int FMT, int NW, typename Store>
+template <int FMT, int NW, typename Shape, typename Store>
 __device__ __forceinline__ void few_down(const WMat& W, int g, int tile, int H, int I,
                                          const uint16_t* rows, int cnt,
-                                         f32x4_t (*red)[2][FewShape<FMT>::NF][kWave],
-                                         Store store) {
-  constexpr int NF = FewShape<FMT>::NF;
+                                         f32x4_t (*red)[Shape::NF][kWave], Store store) {
+  constexpr int NF = Shape::NF;
   const int lane = threadIdx.x & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WStream<FMT, NF, false> ws;
   ws.init(W, g, tile * NF / 4, tile * NF % 4, H / 64, I / 128, 16 * NF * tile, 0, lane);
-  // operand i: columns 0..7 the high parts of rows 8 i .., 8..15 the low ones
   const buffer_t a = uniform_buffer(rows, (int64_t)cnt * I * 4);
+  const bool one = cnt <= 8;
   uint32_t off[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    off[i] = (uint32_t)(min(8 * i + (col & 7), cnt - 1) * 2 * I + (col & 8 ? I : 0) +
-                        8 * (lane >> 4)) * 2u;
-  const int nb = cnt > 8 ? 2 : 1;
-  if (nb == 1)
-    few_down_rows<FMT, NW, 1, FewShape<FMT>::D>(ws, a, off, I / 128, red);
+  off[0] = (uint32_t)(min(one ? col & 7 : col, cnt - 1) * 2 * I + (one && col & 8 ? I : 0) +
+                      8 * (lane >> 4)) * 2u;
+  off[1] = off[0] + 2u * I;
+  if (one)
+    few_down_rows<FMT, NF, NW, 1>(ws, a, off, I / 128, red);
   else
-    few_down_rows<FMT, NW, 2, 1>(ws, a, off, I / 128, red);
+    few_down_rows<FMT, NF, NW, 2>(ws, a, off, I / 128, red);
   __syncthreads();
-  for (int u = w; u < nb * NF; u += NW) {
-    const int i = u / NF, f = u % NF;
-    f32x4_t v = red[0][i][f][lane];
+  for (int f = w; f < NF; f += NW) {
+    f32x4_t v = red[0][f][lane];
 #pragma unroll
-    for (int k = 1; k < NW; ++k) v += red[k][i][f][lane];
+    for (int k = 1; k < NW; ++k) v += red[k][f][lane];
+    if (one) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], 8, kWave);
-    const int row = 8 * i + col;
-    if (col < 8 && row < cnt) store(16 * (tile * NF + f) + 4 * (lane >> 4), row, v);
+      for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], 8, kWave);
+    }
+    if (col < cnt && (col < 8 || !one)) store(16 * (tile * NF + f) + 4 * (lane >> 4), col, v);
   }
 }
 
 // moe_decode: the rows go out in float32, unweighted; blocks as in gate/up.
-template <int FMT, int NW>
-__global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_down_kernel(
+template <int FMT, int NW, bool NARROW>
+__global__ void __launch_bounds__(NW * kWave, (FewShape<FMT, NARROW>::kWaves)) decode_down_kernel(
     int T, int H, int I, WMat routed, WMat shared, int sI, int shared_blocks, DecodePlan plan,
     const uint16_t* __restrict__ a, const uint16_t* __restrict__ s_a, float* __restrict__ rows,
     float* __restrict__ s_rows) {
-  __shared__ f32x4_t red[NW][2][FewShape<FMT>::NF][kWave];
-  const int nt = H / (16 * FewShape<FMT>::NF);
+  using Shape = FewShape<FMT, NARROW>;
+  __shared__ f32x4_t red[NW][Shape::NF][kWave];
+  const int nt = H / (16 * Shape::NF);
   int b = blockIdx.x;
   const bool sh = b < shared_blocks;
   if (!sh) b -= shared_blocks;
@@ -700,7 +685,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_down
   const int cnt = sh ? min(kCols, T - base) : plan.entries[j].cnt;
   const int Ic = sh ? sI : I;
   float* r = (sh ? s_rows : rows) + (int64_t)base * H;
-  few_down<FMT, NW>(sh ? shared : routed, g, b - j * nt, H, Ic,
+  few_down<FMT, NW, Shape>(sh ? shared : routed, g, b - j * nt, H, Ic,
                     (sh ? s_a : a) + (int64_t)base * 2 * Ic, cnt, red,
                     [&](int c, int row, f32x4_t v) {
                       *reinterpret_cast<f32x4_t*>(r + (int64_t)row * H + c) = v;
@@ -717,7 +702,8 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) decode_down
 // tokens' lanes; the waves' sums are added through LDS in order and rounded.
 // It saves a launch and has few workgroups: one token, 16 experts, top-2, H =
 // 1024, I = 512, bf16, the layer takes 9.3 us instead of 10.2; 64 experts,
-// top-8, H = 2048, I = 1024 29 instead of 25.
+// top-8, H = 2048, I = 1024 29 instead of 25.  Like few_stream, one block in
+// flight a wave.
 constexpr int64_t kSmallDown = 1 << 20;   // down weights of a call's slots, up to here
 template <int FMT>
 struct FewDownShape {
@@ -727,7 +713,7 @@ template <int FMT>
 __global__ void __launch_bounds__(16 * kWave) decode_down_combine_kernel(
     int T, int H, int I, WMat routed, WMat shared, int sI, DecodePlan plan,
     const uint16_t* __restrict__ a, const uint16_t* __restrict__ s_a, uint16_t* __restrict__ out) {
-  constexpr int NF = FewDownShape<FMT>::NF, NW = 16, D = 2;
+  constexpr int NF = FewDownShape<FMT>::NF, NW = 16;
   __shared__ f32x4_t red[NW][NF][kWave];
   const int lane = threadIdx.x & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -737,11 +723,9 @@ __global__ void __launch_bounds__(16 * kWave) decode_down_combine_kernel(
   f32x4_t tok[NF], acc[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) tok[f] = acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  struct Buf {
-    typename WStream<FMT, NF, false>::Tile w;
-    u32x4_t x[4];
-  } buf[D];
-  auto load = [&](Buf& t, int b) {
+  typename WStream<FMT, NF, false>::Tile wt;
+  u32x4_t x[4];
+  auto load = [&](int b) {
     const bool sh = b >= nr;
     const int j = sh ? 0 : b / nb;
     const int kb = sh ? b - nr : b - j * nb;
@@ -751,23 +735,23 @@ __global__ void __launch_bounds__(16 * kWave) decode_down_combine_kernel(
     const int Ic = sh ? sI : I;
     WStream<FMT, NF, false> ws;
     ws.init(sh ? shared : routed, sh ? 0 : en.e, ct, f0, n_ct, Ic / 128, 64 * ct, 0, lane);
-    ws.load(t.w, kb);
+    ws.load(wt, kb);
     const buffer_t r = uniform_buffer((sh ? s_a : a) + base * 2 * Ic, (int64_t)cnt * Ic * 4);
     const uint32_t off =
         (uint32_t)(min(col & 7, cnt - 1) * 2 * Ic + (col & 8 ? Ic : 0) + 8 * (lane >> 4)) * 2u;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) t.x[p] = load_b128<false>(r, off + p * 64, kb * 256);
+    for (int p = 0; p < 4; ++p) x[p] = load_b128<false>(r, off + p * 64, kb * 256);
   };
-  auto use = [&](const Buf& t, int b, bool last) {
+  auto use = [&](int b) {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int f = 0; f < NF; ++f)
         acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            t.w.operand(f, p), __builtin_bit_cast(bf16x8_t, t.x[p]), acc[f], 0, 0, 0);
+            wt.operand(f, p), __builtin_bit_cast(bf16x8_t, x[p]), acc[f], 0, 0, 0);
     const bool sh = b >= nr;
     const int j = sh ? 0 : b / nb;
-    if (!last && b + 1 != (sh ? total : (j + 1) * nb)) return;
+    if (b + 1 != b1 && b + 1 != (sh ? total : (j + 1) * nb)) return;
     // the entry (or the wave's part of it) is done: row i is column i, its low
     // part column i + 8
     const int cnt = sh ? T : plan.entries[j].cnt, base = sh ? 0 : plan.entries[j].base;
@@ -777,38 +761,25 @@ __global__ void __launch_bounds__(16 * kWave) decode_down_combine_kernel(
       for (int q = 0; q < 4; ++q) acc[f][q] += __shfl_xor(acc[f][q], 8, kWave);
     for (int i = 0; i < cnt; ++i) {
       const int t_ = sh ? i : plan.row_tok[base + i];
-      const float wt = sh ? 1.0f : plan.row_w[base + i];
+      const float rw = sh ? 1.0f : plan.row_w[base + i];
 #pragma unroll
       for (int f = 0; f < NF; ++f)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float v = __shfl(acc[f][q], (lane & 48) | i, kWave);
-          tok[f][q] += col == t_ ? wt * v : 0.0f;
+          tok[f][q] += col == t_ ? rw * v : 0.0f;
         }
     }
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   };
   if (b1 > b0) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(buf[d], min(b0 + d, b1 - 1));
-    int b = b0;
-    for (; b + 2 * D <= b1; b += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        use(buf[d], b + d, false);
-        load(buf[d], b + d + D);
-      }
+    load(b0);
+    for (int b = b0; b + 1 < b1; ++b) {
+      use(b);
+      load(b + 1);
     }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (b + d < b1) {
-        use(buf[d], b + d, b + d + 1 == b1);
-        if (b + d + D < b1) load(buf[d], b + d + D);
-      }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (b + D + d < b1) use(buf[d], b + D + d, b + D + d + 1 == b1);
+    use(b1 - 1);
   }
 #pragma unroll
   for (int f = 0; f < NF; ++f) red[w][f][lane] = tok[f];
@@ -888,30 +859,41 @@ static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t strea
   uint16_t* s_a = reinterpret_cast<uint16_t*>(d.ws + L.s_a);
   float* rows = reinterpret_cast<float*>(d.ws + L.rows);
   float* s_rows = d.sI ? reinterpret_cast<float*>(d.ws + L.s_rows) : nullptr;
-  constexpr int kTile = 8 * FewShape<FMT>::NF;
   const int runs = d.sI ? (d.T + kCols - 1) / kCols : 0;
-  const int sb = runs * (d.sI / kTile);
-  const unsigned gate = (unsigned)(sb + L.max_entries * (d.I / kTile) + (fused ? 1 : 0));
-#define MOE_DECODE_GATE(EPL)                                                                      \
-  hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kGateWaves, EPL>), dim3(gate),                     \
-                     dim3(kGateWaves * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI,   \
-                     sb, plan, a, s_a, d.logits, d.row_valid, d.E, d.K, d.renorm,                   \
-                     d.expert_begin, d.El, d.topk_idx, d.topk_w)
-  if (!fused) MOE_DECODE_GATE(0);
-  else if (d.E <= 64) MOE_DECODE_GATE(1);
-  else MOE_DECODE_GATE(4);
-#undef MOE_DECODE_GATE
+  auto gate = [&](auto narrow, auto epl) {
+    constexpr bool NARROW = decltype(narrow)::value;
+    constexpr int EPL = decltype(epl)::value, kTile = 8 * FewShape<FMT, NARROW>::NF;
+    const int sb = runs * (d.sI / kTile);
+    hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kGateWaves, NARROW, EPL>),
+                       dim3((unsigned)(sb + L.max_entries * (d.I / kTile) + (EPL ? 1 : 0))),
+                       dim3(kGateWaves * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI,
+                       sb, plan, a, s_a, d.logits, d.row_valid, d.E, d.K, d.renorm, d.expert_begin,
+                       d.El, d.topk_idx, d.topk_w);
+  };
+  auto gate_routing = [&](auto narrow) {
+    if (!fused) gate(narrow, std::integral_constant<int, 0>{});
+    else if (d.E <= 64) gate(narrow, std::integral_constant<int, 1>{});
+    else gate(narrow, std::integral_constant<int, 4>{});
+  };
+  auto down = [&](auto narrow) {
+    constexpr bool NARROW = decltype(narrow)::value;
+    const int nt = d.H / (16 * FewShape<FMT, NARROW>::NF);
+    hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves, NARROW>),
+                       dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
+                       stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a, rows,
+                       s_rows);
+  };
+  constexpr std::bool_constant<FMT == MOE_W_FP8> kNarrow{};   // (false: one shape, false twice)
+  if (kNarrow && runs * (d.sI / 32) + L.max_entries * (d.I / 32) <= kNarrowWgs) gate_routing(kNarrow);
+  else gate_routing(std::false_type{});
   if (fused && ((int64_t)d.T * d.K * d.I + d.sI) * d.H <= kSmallDown) {
     hipLaunchKernelGGL((decode_down_combine_kernel<FMT>),
                        dim3((unsigned)(d.H / (16 * FewDownShape<FMT>::NF))), dim3(16 * kWave), 0,
                        stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, plan, a, s_a, d.out);
     return;
   }
-  const int nt = d.H / (16 * FewShape<FMT>::NF);
-  hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves>),
-                     dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
-                     stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a,
-                     rows, s_rows);
+  if (kNarrow && (runs + L.max_entries) * (d.H / 64) <= kNarrowWgs) down(kNarrow);
+  else down(std::false_type{});
   hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
                      dim3(64), 0, stream, d.T, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
 }
@@ -1028,7 +1010,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) few_gate_up
   long long total;
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
   const int col = threadIdx.x & 15;
-  few_gate_up<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I,
+  few_gate_up<FMT, NW, FewShape<FMT>>(W, r.g, blockIdx.x - j * nt, H, I,
                        uniform_buffer(x + (int64_t)r.row0 * H, (int64_t)r.cnt * H * 2),
                        (uint32_t)min(col, r.cnt - 1) * H * 2u, r.cnt,
                        a + (int64_t)r.row0 * 2 * I, red);
@@ -1040,7 +1022,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) few_down_ke
     const int32_t* __restrict__ counts, int G, int H, int I, WMat W,
     const float* __restrict__ row_scale, uint16_t* __restrict__ y,
     int64_t capacity, int64_t max_runs, int32_t* __restrict__ dev_error) {
-  __shared__ f32x4_t red[NW][2][FewShape<FMT>::NF][kWave];
+  __shared__ f32x4_t red[NW][FewShape<FMT>::NF][kWave];
   const int nt = H / (16 * FewShape<FMT>::NF), j = blockIdx.x / nt;
   RowRun r;
   long long total;
@@ -1051,7 +1033,7 @@ __global__ void __launch_bounds__(NW * kWave, FewShape<FMT>::kWaves) few_down_ke
       raise_error(dev_error, MOE_DEVERR_ROW_RANGE);
   }
   if (!find_run(j, cu_seqlens, counts, G, capacity, dev_error, r, total)) return;
-  few_down<FMT, NW>(W, r.g, blockIdx.x - j * nt, H, I, a + (int64_t)r.row0 * 2 * I, r.cnt,
+  few_down<FMT, NW, FewShape<FMT>>(W, r.g, blockIdx.x - j * nt, H, I, a + (int64_t)r.row0 * 2 * I, r.cnt,
                     red, [&](int c, int i, f32x4_t v) {
                       const int64_t row = r.row0 + i;
                       const float sc = row_scale ? row_scale[row] : 1.0f;
