@@ -318,31 +318,37 @@ int launch_few_ffn(const uint16_t*, const int32_t*, const int32_t*, int, int, in
 // waves, so a few groups fill the GPU, but they read the weights again for
 // every 16 rows (on average every 12 or so).  The tile kernel reads them once
 // per 128 rows, but a workgroup walks the whole reduction by itself, at about
-// 0.9 us a K-block of either stage however few there are: the time in which
-// 42 KB are streamed for each column of H and I.  Where both stream at the
-// memory's rate, sharing the rows through LDS pays from 4 rows a group
-// (NVFP4, whose conversions weigh more there, 8).  Measured, both stages,
-// few / tile in us, MXFP4: H = 4096, I = 1536, 4 groups of 64 rows 42 / 66;
-// 8 groups of 32 rows 43 / 52, of 64 74 / 67; 16 groups of 16 rows 49 / 51, of
-// 24 81 / 55; H = 2048, I = 1024, 64 groups of 1 row 44 / 42, of 8 52 / 43, of
-// 32 112 / 54.  NVFP4, 32 groups (H = 4096, I = 1536) of 4 rows 79 / 91, of 16
-// 102 / 95.
-static bool few_rows(int64_t capacity, int G, int H, int I, int format) {
+// 0.9 us a 128-wide block of either stage however few there are (the time in
+// which 42 KB are streamed for each column of H and I) and more than twice that
+// with a tile's 128; further rows are other workgroups'.  Where both stream at
+// the memory's rate, sharing the rows through LDS pays from 8 rows a group.
+// Measured, both stages, few / tile in us, MXFP4: H = 4096, I = 1536, 4 groups of
+// 32 rows 27 / 50, of 96 57 / 86; 16 groups of 16 rows 47 / 53, of 24 77 / 57; 32
+// groups of 4 rows 61 / 63, of 16 85 / 69; H = 2048, I = 768, 128 groups of 4
+// rows 70 / 73, of 8 76 / 72, of 32 170 / 93; H = 1024, I = 512, 8 groups of 200
+// rows 28 / 41; H = 512, I = 256, 64 groups of 32 rows 16 / 16, of 64 24 / 21.
+// NVFP4, H = 4096, I = 1536, 16 groups of 16 rows 51 / 58, of 24 85 / 69; 32
+// groups of 4 rows 76 / 90, of 24 162 / 104.
+constexpr double kWalkBytes = 42e3;   // a column's, see above
+static bool few_rows(int64_t capacity, int G, int H, int I) {
   const int64_t active = std::min<int64_t>(G, capacity);
-  if (capacity < (format == MOE_W_MXFP4 ? 4 : 8) * active) return true;
+  if (capacity < 8 * active) return true;
   const double bytes = 1.6 * H * I;   // an expert's weights
-  const double tile = std::max(active * bytes, 42e3 * ((double)H + I));
+  const double walk = 1.0 + std::min<double>(kBM, (double)capacity / active) / 96.0;
+  const double tile = std::max(active * bytes, kWalkBytes * ((double)H + I) * walk);
   return std::max<double>(active, capacity / 12.0) * bytes < tile;
 }
 
-// The larger of the two forms' (the choice goes by the weights' format, the
-// size query does not).
+// Both forms', the few-row one's up to the capacities it is taken for: a buffer
+// for the largest batch does for every smaller one.
 size_t grouped_ffn_fp4_workspace_bytes(int64_t capacity, int G, int H, int I) {
+  if (capacity == 0) return 0;
+  const double walk = kWalkBytes * ((double)H + I) * (1.0 + kBM / 96.0) / (1.6 * H * I);
+  const int64_t most = (int64_t)std::max(8.0 * G, 12.0 * std::max((double)G, walk)) + 1;
+  const size_t few = few_ffn_workspace_bytes(std::min(capacity, most), I);
+  if (few_rows(capacity, G, H, I)) return few;
   const int64_t rows = ((capacity + kBM - 1) / kBM + G) * kBM;
-  const size_t tile = (((size_t)rows * I * 2) + 255) & ~(size_t)255;
-  if (!few_rows(capacity, G, H, I, MOE_W_NVFP4)) return tile;
-  const size_t few = few_ffn_workspace_bytes(capacity, I);
-  return few_rows(capacity, G, H, I, MOE_W_MXFP4) ? few : std::max(few, tile);
+  return std::max(few, (((size_t)rows * I * 2) + 255) & ~(size_t)255);
 }
 
 template <int FMT>
@@ -372,7 +378,7 @@ int launch_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu, const int32_t* 
                            int H, int I, const moe_ffn_weights* wt, const float* row_scale,
                            uint16_t* y, int64_t capacity, int flags, void* workspace,
                            int32_t* dev_error, hipStream_t stream) {
-  if (few_rows(capacity, G, H, I, wt->format))
+  if (few_rows(capacity, G, H, I))
     return launch_few_ffn(x, cu, counts, G, H, I, wt, row_scale, y, capacity, flags, workspace,
                           dev_error, stream);
   uint16_t* act = static_cast<uint16_t*>(workspace);

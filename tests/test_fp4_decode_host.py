@@ -144,7 +144,11 @@ def test_size_queries(lib):
     assert _decode(lib, T=64, H=7168, I=2048, E=256, K=8, El=256, ws_bytes=need - 1) == WORKSPACE
     assert ops.moe_grouped_ffn_fp4_workspace_bytes(1000, 4, 256, 128) >= 1000 * 128 * 2
     assert ops.moe_grouped_ffn_fp4_workspace_bytes(7, 4, 256, 128) >= 7 * 128 * 4
-    assert ops.moe_grouped_ffn_fp4_workspace_bytes(0, 4, 256, 128) >= 0
+    assert ops.moe_grouped_ffn_fp4_workspace_bytes(0, 4, 256, 128) == 0
+    for G, H, I in ((1, 128, 128), (4, 4096, 1536), (64, 2048, 1024), (1000, 256, 128)):   # one buffer for all batches
+        sizes = [ops.moe_grouped_ffn_fp4_workspace_bytes(n, G, H, I)
+                 for n in range(0, 140 * min(G, 64), 7 if G < 64 else 61)]
+        assert sizes == sorted(sizes), (G, H, I)
 
 
 def test_handles_check_their_tensors():

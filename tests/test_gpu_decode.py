@@ -336,12 +336,12 @@ def _layer(fmt, T, H, E, K, I, sI, seed=3):
     return layer, q(w13), q(w2), (fu.fake_quant(s13[0], fmt), fu.fake_quant(s2[0], fmt)), rng
 
 
-@pytest.mark.parametrize("fmt", FMTS)
-def test_a_prompt_then_decode_steps(fmt):
+@pytest.mark.parametrize("fmt,T", [(f, 600) for f in FMTS] + [("mxfp4", 6000)])
+def test_a_prompt_then_decode_steps(fmt, T):
     """The layer as it is served: a prompt through the staged path (for 4-bit
     weights the grouped FFN on them), then decode steps of changing batches
     eagerly and from a captured graph, in one layer's buffers."""
-    T, H, E, K, I, sI = 600, 256, 8, 2, 384, 128
+    H, E, K, I, sI = 256, 8, 2, 384, 128
     layer, v13, v2, sv, rng = _layer(fmt, T, H, E, K, I, sI)
     logits, x = _inputs(rng, T, E, H)
     prompt = host_bits(layer.forward(dev(logits), dev_bf16(x)))

@@ -111,20 +111,23 @@ def _check(y_bits, x, cu, counts, v13, v2, scale, a_step, sentinel=None):
         np.testing.assert_array_equal(y_bits[~covered], sentinel[~covered])
 
 
-# (counts, H, I): few rows a group or few groups, which the few-row kernels take,
-# and the tile kernel's
+# (counts, H, I): few rows a group or few groups, which the few-row kernels take;
+# more of both; and as many as only the tile kernel takes
 FEW = [([1], 128, 128), ([1], 2048, 256), ([16], 256, 128), ([0, 3, 0, 1, 17, 0], 384, 256),
        ([33, 0, 0, 2, 0], 256, 384), ([0] * 70 + [5, 0, 1], 128, 128), ([2] * 130, 128, 128),
        ([0, 0, 1], 1152, 640), ([17, 9], 128, 128), ([8, 129], 384, 256)]
 MANY = [([64] * 80, 128, 128), ([1, 0, 130, 65, 64, 63, 16, 17] * 6, 384, 256), ([0, 50] * 18, 640, 1152),
         ([5000], 128, 128), ([300, 0, 5, 77, 640, 800], 256, 640), ([127, 1, 128, 130, 257, 0], 1152, 896)]
+TILE = [([40] * 150, 256, 384), ([1, 0, 130, 65, 64, 63, 16, 17] * 20, 384, 256), ([0, 50] * 60, 640, 1152),
+        ([20000], 128, 128), ([300, 0, 5, 77, 640, 800] * 6, 256, 640),
+        ([127, 1, 128, 130, 257, 0] * 8, 1152, 896)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("case", range(len(FEW) + len(MANY)))
+@pytest.mark.parametrize("case", range(len(FEW) + len(MANY) + len(TILE)))
 @pytest.mark.parametrize("scaled", [True, False])
 def test_ffn_matches_float64(fmt, case, scaled):
-    counts, H, I = (FEW + MANY)[case]
+    counts, H, I = (FEW + MANY + TILE)[case]
     rng = np.random.default_rng(100 + case)
     G = len(counts)
     handle, v13, v2 = _weights(rng, fmt, G, H, I)
@@ -139,7 +142,7 @@ def test_ffn_matches_float64(fmt, case, scaled):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("counts,I", [([3, 0, 9], 128), ([1000, 0, 429], 2048)])
+@pytest.mark.parametrize("counts,I", [([3, 0, 9], 128), ([1000, 0, 429], 2048), ([4000, 0, 429], 2048)])
 def test_rows_outside_the_segments_stay_and_do_not_matter(fmt, counts, I):
     """Unused rows between segments hold NaN and are neither read into other
     rows nor written; a NaN or inf in one row reaches that row only; the
@@ -172,7 +175,7 @@ def test_rows_outside_the_segments_stay_and_do_not_matter(fmt, counts, I):
     assert (ws[need:] == 0x5A).all()
 
 
-@pytest.mark.parametrize("rows,I", [(5, 128), (3000, 768)])
+@pytest.mark.parametrize("rows,I", [(5, 128), (3000, 768), (9000, 768)])
 def test_bad_segments_are_skipped_and_reported(rows, I):
     rng = np.random.default_rng(9)
     H = 128
@@ -201,7 +204,7 @@ def test_bad_segments_are_skipped_and_reported(rows, I):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("counts,I", [([2, 5], 256), ([760, 350], 1280)])
+@pytest.mark.parametrize("counts,I", [([2, 5], 256), ([760, 350], 1280), ([2000, 900], 1280)])
 def test_stages_streams_graphs_and_repeats(fmt, counts, I):
     """GATE_UP then DOWN equals ALL; another stream; a captured graph replayed
     between eager calls on other inputs; the same bits every time."""
