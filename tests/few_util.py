@@ -15,10 +15,11 @@ Bounds (element-wise, in magnitudes of the same products):
 from __future__ import annotations
 
 import numpy as np
+import torch
 
 import oracle
 from oracle.ffn import silu
-from oracle.numerics import bf16_bits_to_f32, bf16_bits_to_f64, e4m3fn_round, f32_to_bf16_bits
+from oracle.numerics import bf16_bits_to_f32, bf16_bits_to_f64, e4m3fn_round
 
 F32_SUM = 2.0 ** -23
 BF16_HALF = 2.0 ** -8
@@ -26,7 +27,9 @@ PAIR, SINGLE = 2.0 ** -16, 2.0 ** -8
 
 
 def bf16(a) -> np.ndarray:
-    return f32_to_bf16_bits(np.asarray(a, dtype=np.float32))
+    """bf16 bits of finite values (the host's conversion: large stacks)."""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32))
+    return t.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
 
 
 def tensor_scale(w_bits) -> np.float32:
@@ -64,13 +67,30 @@ def fake_quant(w_bits, fmt: str, g=None) -> np.ndarray:
         S = (b.astype(np.float32) * g)[..., None]
         r = x / np.where(S > 0, S, np.float32(1))
     v = np.where(S > 0, _e2m1(np.clip(r, -6, 6)) * S, np.float32(0))
-    return f32_to_bf16_bits(v.astype(np.float32)).reshape(N, K)
+    return bf16(v).reshape(N, K)
+
+
+class Stored:
+    """fake_quant of each matrix of a stack, when it is first asked for."""
+
+    def __init__(self, w_bits, fmt: str):
+        self.w, self.fmt, self.done = w_bits, fmt, {}
+
+    def __getitem__(self, e):
+        if e not in self.done:
+            self.done[e] = fake_quant(self.w[e], self.fmt)
+        return self.done[e]
 
 
 def make_weights(rng, G: int, H: int, I: int, std: float = 0.06):
     """(w13 [G, 2I, H], w2 [G, H, I]) bf16 bits."""
-    return (bf16(rng.standard_normal((G, 2 * I, H)) * std),
-            bf16(rng.standard_normal((G, H, I)) * std))
+    def normal(*shape):   # matrix by matrix: the large stacks stay in cache
+        w = np.empty(shape, np.uint16)
+        for g in range(G):
+            w[g] = bf16(rng.standard_normal(shape[1:], dtype=np.float32) * np.float32(std))
+        return w
+
+    return normal(G, 2 * I, H), normal(G, H, I)
 
 
 def expert(x, w13_bits, w2_bits, a_step: float):
@@ -152,9 +172,9 @@ def fp4_values(codes, scale_bytes, mode_nv: bool, g=None) -> np.ndarray:
     v = (E2M1[codes & 7] * np.where(codes & 8, -1.0, 1.0)).astype(np.float32)
     if not mode_nv:
         X = np.ldexp(1.0, scale_bytes.astype(np.int64) - 127).repeat(32, axis=-1)
-        return f32_to_bf16_bits((v * X).astype(np.float32))
+        return bf16(v * X)
     b = scale_bytes.astype(np.int64)
     e, m = (b >> 3) & 15, b & 7
     b = np.where(e == 0, m / 8.0 * 2.0 ** -6, (1.0 + m / 8.0) * 2.0 ** (e - 7.0)).astype(np.float32)
     S = (b * np.asarray(g, dtype=np.float32)[:, None, None]).astype(np.float32).repeat(16, axis=-1)
-    return f32_to_bf16_bits((v * S).astype(np.float32))
+    return bf16(v * S)

@@ -32,8 +32,7 @@ class Layer:
         if spoil is not None:
             spoil(w13, w2)
         self.handle = ops.ffn_weights(dev_bf16(w13), dev_bf16(w2), fmt)
-        self.v13 = [fu.fake_quant(m, fmt) for m in w13]
-        self.v2 = [fu.fake_quant(m, fmt) for m in w2]
+        self.v13, self.v2 = fu.Stored(w13, fmt), fu.Stored(w2, fmt)
         self.shared = self.shared_v = None
         if sI:
             s13, s2 = fu.make_weights(rng, 1, H, sI)

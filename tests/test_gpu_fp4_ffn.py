@@ -93,7 +93,7 @@ def _segments(counts, pad=0):
 def _weights(rng, fmt, G, H, I):
     w13, w2 = fu.make_weights(rng, G, H, I)
     handle = ops.ffn_weights(dev_bf16(w13), dev_bf16(w2), fmt)
-    return handle, [fu.fake_quant(m, fmt) for m in w13], [fu.fake_quant(m, fmt) for m in w2]
+    return handle, fu.Stored(w13, fmt), fu.Stored(w2, fmt)
 
 
 def _check(y_bits, x, cu, counts, v13, v2, scale, a_step, sentinel=None):
