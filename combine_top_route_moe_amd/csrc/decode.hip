@@ -443,10 +443,11 @@ struct FewShape {
 };
 constexpr int64_t kNarrowWgs = 3 * 256;   // three to a CU
 
-// v as the sum of two bf16 numbers, high part first
+// v as the sum of two bf16 numbers, high part first (an infinity or NaN, also
+// one that v rounds to, alone)
 __device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
   hi = f32_to_bf16(v);
-  lo = f32_to_bf16(v - bf16_to_f32(hi));
+  lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16(v - bf16_to_f32(hi));
 }
 
 // One workgroup's gate/up tile: 8 NF intermediate columns, nt of expert g, for
@@ -922,7 +923,7 @@ int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t*
     d.s2 = WMat{shared->w2, shared->w2_scales, shared->w2_tensor_scale};
   }
   const int64_t most = d.L.max_entries + (T + kCols - 1) / kCols;
-  if (most * std::max(std::max(I, sI) / 16, H / 32) >= 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (most * std::max(std::max(I, sI) / 16, H / 32) >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   const bool fused = logits && T <= kFusedTokens && T * K <= 64 && E <= 256;
 #define MOE_PLAN(N)                                                                             \
   hipLaunchKernelGGL(plan_kernel<N>, dim3(1), dim3(kPlanThreads), 0, stream, logits, row_valid, T, \
@@ -1066,7 +1067,7 @@ static int launch_few_fmt(const uint16_t* x, const int32_t* cu, const int32_t* c
                           int32_t* dev_error, hipStream_t stream) {
   const int64_t runs = max_row_runs(capacity, G);
   const int64_t gu = runs * (I / (8 * FewShape<FMT>::NF)), dn = runs * (H / (16 * FewShape<FMT>::NF));
-  if (gu > 0x7fffffff || dn > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (gu >= kMaxGrid || dn >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   if (flags & MOE_FFN_GATE_UP)
     hipLaunchKernelGGL((few_gate_up_kernel<FMT, kGateWaves>), dim3((unsigned)gu),
                        dim3(kGateWaves * kWave), 0, stream, x, cu, counts, G, H, I, w13, capacity,

@@ -116,7 +116,7 @@ int launch_pack_weights_fp4(const uint16_t* w13, const uint16_t* w2, int G, int 
                  int gate_up) -> int {
     const int64_t n_frag = (int64_t)G * (N / 16) * (Kdim / 128);
     const int64_t blocks = (n_frag + 3) / 4;
-    if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    if (blocks >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
     auto* kern = mode == MOE_FQ_MXFP4 ? pack_weights_fp4_kernel<MOE_W_MXFP4>
                                       : pack_weights_fp4_kernel<MOE_W_NVFP4>;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, stream, w, tg,
@@ -367,7 +367,7 @@ static int launch_tiles(const uint16_t* x, const int32_t* cu, const int32_t* cou
     return (m_tiles * ((n_ct + kTileWaves - 1) / kTileWaves) + unit - 1) / unit * unit;
   };
   const int64_t gu = grid(I / 32), dn = grid(H / 64);
-  if (gu > 0x7fffffff || dn > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (gu >= kMaxGrid || dn >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   if (flags & MOE_FFN_GATE_UP)
     hipLaunchKernelGGL((fp4_tile_kernel<true, FMT>), dim3((unsigned)gu), dim3(kTileWaves * kWave),
                        0, stream, x, (WMat{wt->w13, wt->w13_scales, wt->w13_tensor_scale}), cu,

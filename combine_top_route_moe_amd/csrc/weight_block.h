@@ -12,6 +12,9 @@
 
 namespace moe {
 
+// Workgroups of 256 threads that one launch can have (2^32 threads).
+constexpr int64_t kMaxGrid = 1 << 24;
+
 // 8 E2M1 codes (one dword, code j in bits 4j) times the power of two s, as
 // bf16: exact (2 significant bits), one conversion instruction per pair.  It
 // reads only the exponent field of s, so that an E8M0 byte shifted there is

@@ -446,7 +446,8 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
  * shared row gets +0.  T = 0 enqueues nothing.
  * Requires T <= 64, H % 128 == I % 128 == shared_I % 128 == 0, each of them
  * <= 2^20, K <= min(num_experts, 32), num_experts <= 1024, and every expert's
- * w13 and w2 in less than 4 GiB each. */
+ * w13 and w2 in less than 4 GiB each; sizes that need
+ * more than 2^32 threads in a launch are refused. */
 size_t moe_decode_workspace_bytes(int T, int H, int I, int K, int num_local_experts,
                                   int shared_I);
 int moe_decode(const float* logits, const uint8_t* row_valid, const uint16_t* hidden, int T,

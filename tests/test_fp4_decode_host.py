@@ -129,6 +129,13 @@ def test_matrices_past_32_bit_offsets_are_refused(lib):
         assert _decode(lib, w, s=w, H=H, sI=I, ws=None) == UNSUPPORTED
 
 
+def test_launches_past_the_grid_are_refused(lib):
+    big = dict(I=1 << 20, H=128, ws_bytes=1 << 60)
+    assert _decode(lib, T=64, E=1024, K=32, El=1024, **big) == UNSUPPORTED
+    assert _ffn(lib, cap=(1 << 31) - 1, G=1024, **big) == UNSUPPORTED
+    assert _pack(lib, G=1 << 20, H=1 << 15, I=1 << 15) == UNSUPPORTED
+
+
 def test_handles_do_not_change():
     q = torch.zeros(2, 256, 128, dtype=torch.uint8)
     for name in ("w13", "format", "H"):

@@ -196,6 +196,25 @@ def test_infinities_and_nan_stay_where_they_belong(T):
     assert np.isnan(got[(idx == 3).any(1)]).any(axis=1).all()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,E", [(1, 2), (1, 300), (12, 2), (3, 2)])
+def test_an_intermediate_past_the_range_is_an_infinity(fmt, T, E):
+    """One intermediate element overflows (float32, or its rounding to bf16):
+    the outputs are the infinities that it times w2's column gives, no NaN."""
+    H, I = 128, 128
+    w13, w2 = np.zeros((E, 2 * I, H), np.float32), np.full((E, H, I), 0.5, np.float32)
+    w13[:, 5, 0] = w13[:, I + 5, 1] = 1.0
+    w2[:, ::2, 5] = -0.5
+    h = ops.ffn_weights(dev_bf16(fu.bf16(w13)), dev_bf16(fu.bf16(w2)), fmt)
+    logits = np.zeros((T, E), np.float32)
+    # a = g u: past float32; below 2^128, but rounding past bf16 (from 2^128 (1 - 2^-9))
+    for big in ((1e30, 1e30), (2.0 ** 64 * 129 / 128, 2.0 ** 64 * 127 / 128)):
+        x = np.zeros((T, H), np.float32)
+        x[:, :2] = big
+        got = bf16_bits_to_f64(host_bits(ops.moe_decode(dev(logits), dev_bf16(fu.bf16(x)), 1, h)[0]))
+        assert np.isinf(got).all() and (got[:, ::2] < 0).all() and (got[:, 1::2] > 0).all(), big
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
 def test_graphs_streams_and_repeats(fmt):
     """Two captured batch sizes that share a workspace and the weights,
