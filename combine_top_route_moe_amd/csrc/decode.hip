@@ -38,8 +38,6 @@ namespace moe {
 constexpr int kMaxTokens = 64;    // one bit of an expert's token mask each
 constexpr int kCols = 16;         // tokens (or rows) of an entry
 constexpr int kPlanThreads = 1024;
-constexpr int kGateWaves = 4;     // waves of a gate/up workgroup
-constexpr int kDownWaves = 4;     // waves of a down workgroup
 constexpr int kFusedTokens = 8;   // up to here gate/up routes by itself (and T * K <= 64, E <= 256)
 
 // A run of at most 16 tokens of one local expert.
@@ -442,6 +440,20 @@ struct FewShape {
   static constexpr int kWaves = FMT == MOE_W_FP8 && !NARROW ? 4 : 5;
 };
 constexpr int64_t kNarrowWgs = 3 * 256;   // three to a CU
+
+// Waves of a workgroup, which split the reduction: 4, or 8 where the launch has
+// at most a workgroup for each CU and a wave of 4 would walk two blocks or more.
+// MXFP4, the grouped FFN's two stages, 4 / 8 waves in us: H = 7168, I = 2048, 1
+// row 21 / 16; H = 2048, I = 1024, 4 experts of a row 11.5 / 10.6, 8 (256
+// workgroups) 12.8 / 11.8, 16 15.6 / 16.1; H = 512, I = 256 7.8 / 8.1; one token
+// of 64 experts, top-2, H = 7168, I = 2048, 24.7 / 20.0 (FP8 29.5 / 25.1, bf16 35.4
+// / 35.5: its waves have twice the tiles and keep four).
+template <int FMT>
+static bool eight_waves(int64_t workgroups, int reduction) {
+  return FMT != MOE_W_BF16 && workgroups <= 256 && reduction >= 8 * 128;
+}
+using Four = std::integral_constant<int, 4>;
+using Eight = std::integral_constant<int, 8>;
 
 // v as the sum of two bf16 numbers, high part first (an infinity or NaN, also
 // one that v rounds to, alone)
@@ -870,40 +882,48 @@ static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t strea
   float* rows = reinterpret_cast<float*>(d.ws + L.rows);
   float* s_rows = d.sI ? reinterpret_cast<float*>(d.ws + L.s_rows) : nullptr;
   const int runs = d.sI ? (d.T + kCols - 1) / kCols : 0;
-  auto gate = [&](auto narrow, auto epl) {
+  auto gate = [&](auto narrow, auto epl, auto nw) {
     constexpr bool NARROW = decltype(narrow)::value;
-    constexpr int EPL = decltype(epl)::value, kTile = 8 * FewShape<FMT, NARROW>::NF;
+    constexpr int EPL = decltype(epl)::value, NW = decltype(nw)::value;
+    constexpr int kTile = 8 * FewShape<FMT, NARROW>::NF;
     const int sb = runs * (d.sI / kTile);
-    hipLaunchKernelGGL((decode_gate_up_kernel<FMT, kGateWaves, NARROW, EPL>),
+    hipLaunchKernelGGL((decode_gate_up_kernel<FMT, NW, NARROW, EPL>),
                        dim3((unsigned)(sb + L.max_entries * (d.I / kTile) + (EPL ? 1 : 0))),
-                       dim3(kGateWaves * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI,
-                       sb, plan, a, s_a, d.logits, d.row_valid, d.E, d.K, d.renorm, d.expert_begin,
+                       dim3(NW * kWave), 0, stream, d.x, d.T, d.H, d.I, d.r13, d.s13, d.sI, sb,
+                       plan, a, s_a, d.logits, d.row_valid, d.E, d.K, d.renorm, d.expert_begin,
                        d.El, d.topk_idx, d.topk_w);
   };
-  auto gate_routing = [&](auto narrow) {
-    if (!fused) gate(narrow, std::integral_constant<int, 0>{});
-    else if (d.E <= 64) gate(narrow, std::integral_constant<int, 1>{});
-    else gate(narrow, std::integral_constant<int, 4>{});
+  auto gate_shape = [&](auto narrow, auto nw) {
+    if (!fused) gate(narrow, std::integral_constant<int, 0>{}, nw);
+    else if (d.E <= 64) gate(narrow, std::integral_constant<int, 1>{}, nw);
+    else gate(narrow, std::integral_constant<int, 4>{}, nw);
   };
-  auto down = [&](auto narrow) {
+  auto down = [&](auto narrow, auto nw) {
     constexpr bool NARROW = decltype(narrow)::value;
+    constexpr int NW = decltype(nw)::value;
     const int nt = d.H / (16 * FewShape<FMT, NARROW>::NF);
-    hipLaunchKernelGGL((decode_down_kernel<FMT, kDownWaves, NARROW>),
-                       dim3((unsigned)((runs + L.max_entries) * nt)), dim3(kDownWaves * kWave), 0,
-                       stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a, rows,
-                       s_rows);
+    hipLaunchKernelGGL((decode_down_kernel<FMT, NW, NARROW>),
+                       dim3((unsigned)((runs + L.max_entries) * nt)), dim3(NW * kWave), 0, stream,
+                       d.T, d.H, d.I, d.r2, d.s2, d.sI, runs * nt, plan, a, s_a, rows, s_rows);
   };
+  // workgroups of the two stages at NF = 4
+  const int64_t wg_gate = runs * (d.sI / 32) + L.max_entries * (d.I / 32);
+  const int64_t wg_down = (runs + L.max_entries) * (d.H / 64);
   constexpr std::bool_constant<FMT == MOE_W_FP8> kNarrow{};   // (false: one shape, false twice)
-  if (kNarrow && runs * (d.sI / 32) + L.max_entries * (d.I / 32) <= kNarrowWgs) gate_routing(kNarrow);
-  else gate_routing(std::false_type{});
+  constexpr int kHalf = kNarrow ? 2 : 1;   // NF = 2 wherever few
+  using Most = std::conditional_t<FMT == MOE_W_BF16, Four, Eight>;
+  if (eight_waves<FMT>(kHalf * wg_gate, d.H)) gate_shape(kNarrow, Most{});
+  else if (wg_gate <= kNarrowWgs) gate_shape(kNarrow, Four{});
+  else gate_shape(std::false_type{}, Four{});
   if (fused && ((int64_t)d.T * d.K * d.I + d.sI) * d.H <= kSmallDown) {
     hipLaunchKernelGGL((decode_down_combine_kernel<FMT>),
                        dim3((unsigned)(d.H / (16 * FewDownShape<FMT>::NF))), dim3(16 * kWave), 0,
                        stream, d.T, d.H, d.I, d.r2, d.s2, d.sI, plan, a, s_a, d.out);
     return;
   }
-  if (kNarrow && (runs + L.max_entries) * (d.H / 64) <= kNarrowWgs) down(kNarrow);
-  else down(std::false_type{});
+  if (eight_waves<FMT>(kHalf * wg_down, std::max(d.I, d.sI))) down(kNarrow, Most{});
+  else if (wg_down <= kNarrowWgs) down(kNarrow, Four{});
+  else down(std::false_type{}, Four{});
   hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
                      dim3(64), 0, stream, d.T, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);
 }
@@ -1068,14 +1088,24 @@ static int launch_few_fmt(const uint16_t* x, const int32_t* cu, const int32_t* c
   const int64_t runs = max_row_runs(capacity, G);
   const int64_t gu = runs * (I / (8 * FewShape<FMT>::NF)), dn = runs * (H / (16 * FewShape<FMT>::NF));
   if (gu >= kMaxGrid || dn >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
-  if (flags & MOE_FFN_GATE_UP)
-    hipLaunchKernelGGL((few_gate_up_kernel<FMT, kGateWaves>), dim3((unsigned)gu),
-                       dim3(kGateWaves * kWave), 0, stream, x, cu, counts, G, H, I, w13, capacity,
-                       a, dev_error);
-  if (flags & MOE_FFN_DOWN)
-    hipLaunchKernelGGL((few_down_kernel<FMT, kDownWaves>), dim3((unsigned)dn),
-                       dim3(kDownWaves * kWave), 0, stream, a, cu, counts, G, H, I, w2,
-                       row_scale, y, capacity, runs, dev_error);
+  auto gate = [&](auto nw) {
+    constexpr int NW = decltype(nw)::value;
+    hipLaunchKernelGGL((few_gate_up_kernel<FMT, NW>), dim3((unsigned)gu), dim3(NW * kWave), 0,
+                       stream, x, cu, counts, G, H, I, w13, capacity, a, dev_error);
+  };
+  auto down = [&](auto nw) {
+    constexpr int NW = decltype(nw)::value;
+    hipLaunchKernelGGL((few_down_kernel<FMT, NW>), dim3((unsigned)dn), dim3(NW * kWave), 0, stream,
+                       a, cu, counts, G, H, I, w2, row_scale, y, capacity, runs, dev_error);
+  };
+  if (flags & MOE_FFN_GATE_UP) {
+    if (eight_waves<FMT>(gu, H)) gate(Eight{});
+    else gate(Four{});
+  }
+  if (flags & MOE_FFN_DOWN) {
+    if (eight_waves<FMT>(dn, I)) down(Eight{});
+    else down(Four{});
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -69,6 +69,8 @@ SHAPES = [
     (64, 640, 40, 6, 896, 256, 40, 0, 3),
     (64, 384, 3, 2, 4096, 0, 3, 0, 0),
     (64, 128, 1024, 32, 128, 128, 1024, 0, 0),      # all the entries there can be
+    (20, 1152, 4, 2, 1152, 0, 4, 0, 0),             # few tiles, long reductions
+    (2, 1152, 100, 2, 1152, 128, 100, 0, 0),
 ]
 
 

@@ -115,7 +115,7 @@ def _check(y_bits, x, cu, counts, v13, v2, scale, a_step, sentinel=None):
 # more of both; and as many as only the tile kernel takes
 FEW = [([1], 128, 128), ([1], 2048, 256), ([16], 256, 128), ([0, 3, 0, 1, 17, 0], 384, 256),
        ([33, 0, 0, 2, 0], 256, 384), ([0] * 70 + [5, 0, 1], 128, 128), ([2] * 130, 128, 128),
-       ([0, 0, 1], 1152, 640), ([17, 9], 128, 128), ([8, 129], 384, 256)]
+       ([0, 0, 1], 1152, 640), ([17, 9], 128, 128), ([8, 129], 384, 256), ([5, 20], 1152, 1152)]
 MANY = [([64] * 80, 128, 128), ([1, 0, 130, 65, 64, 63, 16, 17] * 6, 384, 256), ([0, 50] * 18, 640, 1152),
         ([5000], 128, 128), ([300, 0, 5, 77, 640, 800], 256, 640), ([127, 1, 128, 130, 257, 0], 1152, 896)]
 TILE = [([40] * 150, 256, 384), ([1, 0, 130, 65, 64, 63, 16, 17] * 20, 384, 256), ([0, 50] * 60, 640, 1152),
