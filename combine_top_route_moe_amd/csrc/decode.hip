@@ -115,7 +115,7 @@ __device__ __forceinline__ void load_keys(const float* __restrict__ row, int E, 
 }
 
 // One token's K best experts by one wave (every lane active), the same choice
-// and order as route_row: lane k < K gets slot k's expert in sel_e and its
+// and order as moe_route's: lane k < K gets slot k's expert in sel_e and its
 // logit in sel_v.  Each lane first sorts its keys, so that a round compares
 // one head per lane: the wave maximum, the lanes that hold it (one, but for
 // ties), and the winner drops its head.  Sorting pays while a lane holds few
@@ -215,7 +215,7 @@ __device__ __forceinline__ void select_topk_row16(const float* __restrict__ row,
   sel_v = key_value(best);
 }
 
-// The selected experts' weights (lane k < K: slot k's), as route_row's.
+// The selected experts' weights (lane k < K: slot k's), as moe_route's.
 template <int EPL>
 __device__ __forceinline__ float topk_weight(const int* key, int E, int K, int renorm, int lane,
                                              float sel_v) {

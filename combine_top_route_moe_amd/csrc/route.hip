@@ -14,6 +14,29 @@
 
 namespace moe {
 
+// Wave-wide max (float) and min (int), the result in every lane: within each
+// 16-lane row by two quad permutations and the half-row and row mirrors
+// (register moves, no LDS), then the four rows' results by readlane.
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, __int_as_float(row16_dpp<0xB1>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(row16_dpp<0x4E>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(row16_dpp<0x141>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(row16_dpp<0x140>(__float_as_int(v))));
+  const int b = __float_as_int(v);
+  return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 0)),
+                     __int_as_float(__builtin_amdgcn_readlane(b, 16))),
+               fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)),
+                     __int_as_float(__builtin_amdgcn_readlane(b, 48))));
+}
+__device__ __forceinline__ int wave_min_i32(int v) {
+  v = min(v, row16_dpp<0xB1>(v));
+  v = min(v, row16_dpp<0x4E>(v));
+  v = min(v, row16_dpp<0x141>(v));
+  v = min(v, row16_dpp<0x140>(v));
+  return min(min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
 // EPL: experts per lane (E <= 64 * EPL).
 template <int EPL>
 __global__ void __launch_bounds__(256) route_kernel(const float* __restrict__ logits,
@@ -34,12 +57,72 @@ __global__ void __launch_bounds__(256) route_kernel(const float* __restrict__ lo
     return;
   }
 
-  int sel_e;
-  float sel_w;
-  route_row<EPL>(logits + (int64_t)t * E, E, K, renorm, lane, sel_e, sel_w);
+  const float* row = logits + (int64_t)t * E;
+  float v[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    int e = lane + j * kWave;
+    v[j] = e < E ? rank_value(row[e]) : 0.0f;
+  }
+  uint32_t taken = 0;  // bit j: expert lane + 64 j already chosen (or absent)
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    if (lane + j * kWave >= E) taken |= 1u << j;
+
+  float sel_v = 0.0f;  // lane k keeps slot k's logit (k < 64)
+  int sel_e = -1;
+  float lmax = 0.0f;
+  for (int k = 0; k < K; ++k) {
+    // lane-local best among untaken: higher value, then lower index
+    bool has = false;
+    float bv = 0.0f;
+    int be = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (taken & (1u << j)) continue;
+      int e = lane + j * kWave;
+      if (!has || v[j] > bv || (v[j] == bv && e < be)) {
+        has = true;
+        bv = v[j];
+        be = e;
+      }
+    }
+    // wave argmax: the largest value, then the lowest index holding it (a
+    // lane with no candidate offers -inf and no index, so a real expert
+    // always wins); no LDS traffic — K rounds of shuffle butterflies through
+    // LDS permutes took a 16k-token, 128-expert batch 35 us
+    if (!has) {
+      bv = -__builtin_inff();
+      be = 0x7fffffff;
+    }
+    const float mv = wave_max_f32(bv);
+    be = wave_min_i32(has && bv == mv ? be : 0x7fffffff);   // +0 and -0 tie, as in the order
+    bv = mv;
+    // every lane now holds the winner (bv, be)
+    if ((be & 63) == lane) taken |= 1u << (be >> 6);
+    if (k == 0) lmax = bv;
+    if (lane == k) {
+      sel_v = bv;
+      sel_e = be;
+    }
+  }
+
+  // weights: exp(l_k - l_max) / sum, in double
+  double num = 0.0;
+  if (lane < K) num = weight_term(sel_v, lmax);
+  double den = 0.0;
+  if (renorm) {
+    den = sum_lanes_below(num, K);   // the K slot terms, slot order
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + j * kWave < E) den += weight_term(v[j], lmax);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) den += __shfl_xor(den, off, kWave);
+  }
   if (lane < K) {
     out_idx[lane] = sel_e;
-    out_w[lane] = sel_w;
+    out_w[lane] = (float)(num / den);
   }
 }
 

@@ -74,10 +74,6 @@ template <bool NT>
 __device__ __forceinline__ u32x2_t load_b64(buffer_t r, uint32_t lane_off, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, NT ? 2 : 0);
 }
-template <bool NT>
-__device__ __forceinline__ uint32_t load_b32(buffer_t r, uint32_t lane_off, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, NT ? 2 : 0);
-}
 
 // One weight matrix stack [G, N, Kdim] in a packed format, as the kernels
 // take it (device pointers; scales and tensor_scale as the format needs).
@@ -89,10 +85,10 @@ struct WMat {
 
 // The stream of a column tile's fragments f0 .. f0 + NF - 1 (GU, a w13 tile
 // with NF < 4: NF / 2 gate fragments and the matching up ones, two on) over
-// the reduction dimension: load(t, kb) fetches K-block kb into a Tile in kLoads
-// vector loads, and Tile::operand(f, p) converts piece p of fragment f.  g:
-// expert, ct: column tile, n_ct: column tiles, nkb: Kdim / 128; row0, up0: the
-// tile's first weight row, and of a w13 tile's up half.
+// the reduction dimension: load(t, kb) fetches K-block kb into a Tile, and
+// Tile::operand(f, p) converts piece p of fragment f.  g: expert, ct: column
+// tile, n_ct: column tiles, nkb: Kdim / 128; row0, up0: the tile's first weight
+// row, and of a w13 tile's up half.
 constexpr int frag_of(bool gu, int nf, int f) { return gu && f >= nf / 2 ? f - nf / 2 + 2 : f; }
 
 template <int FMT, int NF, bool GU>
@@ -106,7 +102,6 @@ struct WStream<MOE_W_BF16, NF, GU> {
       return __builtin_bit_cast(bf16x8_t, v[f][p]);
     }
   };
-  static constexpr int kLoads = 4 * NF;
   buffer_t buf;
   uint32_t stride, off;   // bytes between K-steps; the lane's
   __device__ __forceinline__ void init(const WMat& m, int g, int ct, int f0, int n_ct, int nkb,
@@ -135,7 +130,6 @@ struct WStream<MOE_W_FP8, NF, GU> {
       return dequant8_fp8(v[f][p], s[GU && f >= NF / 2]);
     }
   };
-  static constexpr int kLoads = 4 * NF;
   buffer_t buf;
   const float* sc;
   const float* sc_up;
@@ -174,7 +168,6 @@ struct WStream<MOE_W_MXFP4, 4, GU> {
       return dequant8_mxfp4(v[f][p], __uint_as_float(((s[f] >> (8 * p)) & 0xffu) << 23));
     }
   };
-  static constexpr int kLoads = 5;
   buffer_t buf, sbuf;
   uint32_t stride;   // code bytes between K-blocks (scales: 1/16 of them)
   uint32_t off, soff;
@@ -211,7 +204,6 @@ struct WStream<MOE_W_NVFP4, 4, GU> {
       return dequant8_nvfp4(v[f][p], b * g);
     }
   };
-  static constexpr int kLoads = 5;
   buffer_t buf, sbuf;
   float g;
   uint32_t stride;   // code bytes between K-blocks (scales: 1/8 of them)
