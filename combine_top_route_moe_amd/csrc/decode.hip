@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kWave) route_few_kernel(
 // A wave has one block in flight, into registers that the block before leaves
 // free as its MFMAs go; the waves of the other workgroups on the CU cover the
 // wait.  (Two in flight, with fewer waves: MXFP4 4 to 8 % longer at 8 tokens and
-// as long at one; NVFP4 52 us for 333 rows of ragged experts instead of 49; the
-// same for bf16 and FP8.)
+// as long at one; NVFP4 52 us for 333 rows of ragged experts instead of 49; bf16
+// and FP8 within 2 %.)
 template <int FMT, int NF, int NB, bool GU>
 __device__ __forceinline__ void few_stream(const WStream<FMT, NF, GU>& ws, buffer_t b,
                                            const uint32_t* boff, int kb0, int step, int nkb,
@@ -427,19 +427,27 @@ __device__ __forceinline__ void few_stream(const WStream<FMT, NF, GU>& ws, buffe
 }
 
 // The shape of a few-row product, by format: NF fragments a wave (gate/up: half
-// gate, half up), kWaves waves to a SIMD (what the registers of that allow).
-// bf16 blocks are large (4 KB a fragment): two fragments; the narrower formats
-// take a whole 64-row column tile, which reads each row of x, or of a, for
-// four fragments.  FP8 halves the fragments (NARROW) while the launch has so few workgroups
-// that all of them run at once: one token, 8 experts, H = 2048, I = 1024 19 us
-// instead of 22; with many, reading x twice as often costs more: 40 tokens, 64
-// experts, H = 7168, I = 2048 554 us instead of 459.
+// gate, half up), kWaves waves to a SIMD (what the registers of that allow).  A
+// whole 64-row column tile reads each row of x, or of a, for four fragments;
+// bf16 (4 KB a fragment and block) and FP8 can take two (NARROW), the 4-bit
+// formats' blocks are whole tiles.
 template <int FMT, bool NARROW = false>
 struct FewShape {
-  static constexpr int NF = FMT == MOE_W_BF16 || NARROW ? 2 : 4;
-  static constexpr int kWaves = FMT == MOE_W_FP8 && !NARROW ? 4 : 5;
+  static constexpr int NF = NARROW ? 2 : 4;
+  static constexpr int kWaves = FMT >= MOE_W_MXFP4 || NARROW ? 5 : 4;
 };
-constexpr int64_t kNarrowWgs = 3 * 256;   // three to a CU
+// FP8 is narrow while the launch has so few workgroups that all run at once,
+// three to a CU: one token, 8 of 64 experts, H = 2048, I = 1024 19 us instead of
+// 22; with more, reading x twice as often costs more: 40 tokens, H = 7168, I =
+// 2048 554 us instead of 459.  bf16 goes by the rows that share an expert and
+// their length, wide / narrow: 64 experts, top-8, H = 7168, I = 2048 and a shared
+// one, 64 tokens 886 / 1010 us, 32 840 / 889, 8 581 / 605 (and one, by another
+// run, 134 / 130); 8 experts, top-2, H = 4096, I = 8192, 64 tokens 375 / 434; 64
+// experts, top-8, H = 2048, I = 1024, 64 tokens 149 / 152, 32 145 / 136.
+template <int FMT>
+static bool narrow_tiles(int64_t workgroups, int64_t slots, int E, int reduction) {
+  return FMT == MOE_W_FP8 ? workgroups <= 3 * 256 : slots * reduction < 12288LL * E;
+}
 
 // Waves of a workgroup, which split the reduction: 4, or 8 where the launch has
 // at most a workgroup for each CU and a wave of 4 would walk two blocks or more.
@@ -909,11 +917,12 @@ static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t strea
   // workgroups of the two stages at NF = 4
   const int64_t wg_gate = runs * (d.sI / 32) + L.max_entries * (d.I / 32);
   const int64_t wg_down = (runs + L.max_entries) * (d.H / 64);
-  constexpr std::bool_constant<FMT == MOE_W_FP8> kNarrow{};   // (false: one shape, false twice)
+  constexpr std::bool_constant<FMT == MOE_W_BF16 || FMT == MOE_W_FP8> kNarrow{};   // (false: one shape)
   constexpr int kHalf = kNarrow ? 2 : 1;   // NF = 2 wherever few
+  const int64_t slots = (int64_t)d.T * d.K;
   using Most = std::conditional_t<FMT == MOE_W_BF16, Four, Eight>;
   if (eight_waves<FMT>(kHalf * wg_gate, d.H)) gate_shape(kNarrow, Most{});
-  else if (wg_gate <= kNarrowWgs) gate_shape(kNarrow, Four{});
+  else if (narrow_tiles<FMT>(wg_gate, slots, d.E, d.H)) gate_shape(kNarrow, Four{});
   else gate_shape(std::false_type{}, Four{});
   if (fused && ((int64_t)d.T * d.K * d.I + d.sI) * d.H <= kSmallDown) {
     hipLaunchKernelGGL((decode_down_combine_kernel<FMT>),
@@ -922,7 +931,7 @@ static void launch_decode_ffn(const DecodeArgs& d, bool fused, hipStream_t strea
     return;
   }
   if (eight_waves<FMT>(kHalf * wg_down, std::max(d.I, d.sI))) down(kNarrow, Most{});
-  else if (wg_down <= kNarrowWgs) down(kNarrow, Four{});
+  else if (narrow_tiles<FMT>(wg_down, slots, d.E, d.I)) down(kNarrow, Four{});
   else down(std::false_type{}, Four{});
   hipLaunchKernelGGL(decode_combine_kernel, dim3((unsigned)((d.H + 255) / 256), (unsigned)d.T),
                      dim3(64), 0, stream, d.T, d.H, d.K, plan.row_of, d.topk_w, rows, s_rows, d.out);

@@ -71,6 +71,8 @@ SHAPES = [
     (64, 128, 1024, 32, 128, 128, 1024, 0, 0),      # all the entries there can be
     (20, 1152, 4, 2, 1152, 0, 4, 0, 0),             # few tiles, long reductions
     (2, 1152, 100, 2, 1152, 128, 100, 0, 0),
+    (8, 1536, 2, 2, 256, 128, 2, 0, 0),             # a few experts for all, or long rows
+    (8, 19200, 100, 8, 128, 0, 2, 50, 1),
 ]
 
 
