@@ -62,6 +62,25 @@ def _one_device(stream, first: torch.Tensor, *others) -> int:
     return stream.cuda_stream
 
 
+def _pointers(device: int, *args) -> list:
+    """The device pointers of (tensor or None, dtype, name) after the checks of
+    ``_want`` and ``_ptr`` and of the device, in one pass: a call of a few
+    tokens takes the GPU less time than those calls took the host."""
+    out = []
+    for t, dtype, name in args:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
+
+
 def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
     """A tensor for a call on ``stream``, out of that stream's pool: one of the
     current stream's could still be in use there, or be handed out again
@@ -70,13 +89,6 @@ def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _workspace(workspace: Optional[torch.Tensor], need: int, device, stream) -> torch.Tensor:
-    if workspace is None:
-        return _empty(max(need, 1), torch.uint8, device, stream)
-    _want(workspace, torch.uint8, "workspace")
-    return workspace
 
 
 def _stream(stream=None) -> int:
@@ -547,11 +559,6 @@ def moe_grouped_ffn_fp4(x: torch.Tensor, cu_seqlens: torch.Tensor, counts: torch
                         dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The grouped FFN with 4-bit weights (``ffn_weights(..., "mxfp4")`` or
     "nvfp4")."""
-    _want(x, torch.bfloat16, "x")
-    _want(cu_seqlens, torch.int32, "cu_seqlens")
-    _want(counts, torch.int32, "counts")
-    if row_scale is not None:
-        _want(row_scale, torch.float32, "row_scale")
     capacity, H = x.shape
     G, I = weights.num_groups, weights.I
     if H != weights.H:
@@ -560,24 +567,23 @@ def moe_grouped_ffn_fp4(x: torch.Tensor, cu_seqlens: torch.Tensor, counts: torch
         raise ValueError("counts / cu_seqlens do not match the number of groups")
     if row_scale is not None and row_scale.numel() < capacity:
         raise ValueError("row_scale is shorter than x")
-    if dev_error is not None:
-        _want(dev_error, torch.int32, "dev_error")
-    if y is not None:
-        _want(y, torch.bfloat16, "y")
-        if tuple(y.shape) != (capacity, H):
-            raise ValueError("y does not match x")
-    raw = _one_device(stream, x, cu_seqlens, counts, row_scale, y, workspace, dev_error,
-                      weights.w13)
+    if y is not None and y.shape != (capacity, H):
+        raise ValueError("y does not match x")
+    raw = _one_device(stream, x, weights.w13)
     lib = load()
     if y is None:
         y = _empty((capacity, H), torch.bfloat16, x.device, stream)
-    need = (lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
-            if workspace is None else 0)
-    workspace = _workspace(workspace, need, x.device, stream)
+    if workspace is None:
+        need = lib.moe_grouped_ffn_fp4_workspace_bytes(capacity, G, H, I)
+        workspace = _empty(max(need, 1), torch.uint8, x.device, stream)
+    px, pcu, pn, ps, py, pws, perr = _pointers(
+        x.get_device(), (x, torch.bfloat16, "x"), (cu_seqlens, torch.int32, "cu_seqlens"),
+        (counts, torch.int32, "counts"), (row_scale, torch.float32, "row_scale"),
+        (y, torch.bfloat16, "y"), (workspace, torch.uint8, "workspace"),
+        (dev_error, torch.int32, "dev_error"))
     check("moe_grouped_ffn_fp4", lib.moe_grouped_ffn_fp4(
-        _ptr(x), _ptr(cu_seqlens), _ptr(counts), G, H, I, ctypes.addressof(weights._c),
-        _ptr(row_scale), _ptr(y), capacity, flags, _ptr(workspace), workspace.numel(),
-        _ptr(dev_error), raw))
+        px, pcu, pn, G, H, I, ctypes.addressof(weights._c), ps, py, capacity, flags, pws,
+        workspace.numel(), perr, raw))
     return y
 
 
@@ -600,10 +606,7 @@ def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, wei
     starting at ``expert_begin``; ``shared``: the shared expert's (one group,
     the same format)."""
     T, H = hidden.shape
-    dev = hidden.device
-    _want(hidden, torch.bfloat16, "hidden")
     if logits is not None:
-        _want(logits, torch.float32, "logits")
         if logits.shape[0] != T or num_experts not in (None, logits.shape[1]):
             raise ValueError("logits must be [T, num_experts]")
         num_experts = logits.shape[1]
@@ -611,44 +614,38 @@ def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, wei
         raise ValueError("without logits, topk_idx and topk_w are needed")
     elif num_experts is None:
         num_experts = expert_begin + weights.num_groups
-    if topk_idx is not None:
-        _want(topk_idx, torch.int32, "topk_idx")
-        if topk_idx.shape != (T, k):
-            raise ValueError("topk_idx must be [T, k]")
-    if topk_w is not None:
-        _want(topk_w, torch.float32, "topk_w")
-        if topk_w.shape != (T, k):
-            raise ValueError("topk_w must be [T, k]")
-    if dev_error is not None:
-        _want(dev_error, torch.int32, "dev_error")
-    if row_valid is not None:
-        _want(row_valid, torch.uint8, "row_valid")
-        if row_valid.numel() != T:
-            raise ValueError("row_valid must be [T]")
+    if ((topk_idx is not None and topk_idx.shape != (T, k)) or
+            (topk_w is not None and topk_w.shape != (T, k))):
+        raise ValueError("topk_idx and topk_w must be [T, k]")
+    if row_valid is not None and row_valid.numel() != T:
+        raise ValueError("row_valid must be [T]")
     if weights.H != H or (shared is not None and (shared.H != H or shared.num_groups != 1)):
         raise ValueError("weight shapes do not match hidden")
-    if out is not None:
-        _want(out, torch.bfloat16, "out")
-        if out.shape != (T, H):
-            raise ValueError("out does not match hidden")
-    raw = _one_device(stream, hidden, logits, row_valid, topk_idx, topk_w, out, workspace, dev_error,
-                      weights.w13, shared.w13 if shared is not None else None)
+    if out is not None and out.shape != (T, H):
+        raise ValueError("out does not match hidden")
+    raw = _one_device(stream, hidden, weights.w13, None if shared is None else shared.w13)
     lib = load()
-    shared_I = shared.I if shared is not None else 0
+    shared_I = 0 if shared is None else shared.I
     if topk_idx is None:
-        topk_idx = _empty((T, k), torch.int32, dev, stream)
+        topk_idx = _empty((T, k), torch.int32, hidden.device, stream)
     if topk_w is None:
-        topk_w = _empty((T, k), torch.float32, dev, stream)
+        topk_w = _empty((T, k), torch.float32, hidden.device, stream)
     if out is None:
-        out = _empty((T, H), torch.bfloat16, dev, stream)
-    need = (lib.moe_decode_workspace_bytes(T, H, weights.I, k, weights.num_groups, shared_I)
-            if workspace is None else 0)
-    workspace = _workspace(workspace, need, dev, stream)
+        out = _empty((T, H), torch.bfloat16, hidden.device, stream)
+    if workspace is None:
+        need = lib.moe_decode_workspace_bytes(T, H, weights.I, k, weights.num_groups, shared_I)
+        workspace = _empty(max(need, 1), torch.uint8, hidden.device, stream)
+    pl, pv, px, pi, pw, po, pws, perr = _pointers(
+        hidden.get_device(), (logits, torch.float32, "logits"),
+        (row_valid, torch.uint8, "row_valid"), (hidden, torch.bfloat16, "hidden"),
+        (topk_idx, torch.int32, "topk_idx"), (topk_w, torch.float32, "topk_w"),
+        (out, torch.bfloat16, "out"), (workspace, torch.uint8, "workspace"),
+        (dev_error, torch.int32, "dev_error"))
     check("moe_decode", lib.moe_decode(
-        _ptr(logits), _ptr(row_valid), _ptr(hidden), T, H, weights.I, num_experts, k, expert_begin,
-        weights.num_groups, MOE_ROUTE_RENORM if renormalize else 0, _ptr(topk_idx), _ptr(topk_w),
-        ctypes.addressof(weights._c), ctypes.addressof(shared._c) if shared is not None else None,
-        shared_I, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_error), raw))
+        pl, pv, px, T, H, weights.I, num_experts, k, expert_begin, weights.num_groups,
+        MOE_ROUTE_RENORM if renormalize else 0, pi, pw, ctypes.addressof(weights._c),
+        None if shared is None else ctypes.addressof(shared._c), shared_I, po, pws,
+        workspace.numel(), perr, raw))
     return out, topk_idx, topk_w
 
 
