@@ -144,18 +144,6 @@ def _quantize(w, fmt):
     return {"w": _nibbles(q.reshape(N, Kd)), "s": b, "g": g}
 
 
-def _fp8_packed(q, gate_up):
-    """Row-major E4M3 codes [G, N, Kd] in the framework's packed order: per
-    32-wide K-step and 64-row column tile four fragments of 64 lanes x 8 codes."""
-    G, N, Kd = q.shape
-    u = q.view(torch.uint8)
-    if gate_up:                                                     # a tile: 32 gate rows, 32 up rows
-        u = u.reshape(G, 2, N // 64, 2, 16, Kd // 32, 4, 8).permute(0, 5, 2, 1, 3, 6, 4, 7)
-    else:
-        u = u.reshape(G, N // 64, 4, 16, Kd // 32, 4, 8).permute(0, 4, 1, 2, 5, 3, 6)
-    return u.contiguous().reshape(G, N, Kd)
-
-
 def _expert_weights(gen, fmt, G, H, I):
     """G experts' (w13, w2) drawn at a checkpoint's scale, as stacked checkpoint
     tensors; the framework's packed form of the same weights beside them."""
@@ -169,20 +157,16 @@ def _expert_weights(gen, fmt, G, H, I):
             plain = {k: torch.empty((G,) + tuple(v.shape), dtype=v.dtype, device=DEV) for k, v in parts.items()}
             if own:
                 w13, w2 = plain.get("13w"), plain.get("2w")
-                if fmt in ("mxfp4", "nvfp4"):
+                if fmt != "bf16":
                     w13 = torch.empty(G, 2 * I, H, dtype=torch.bfloat16, device=DEV)
                     w2 = torch.empty(G, H, I, dtype=torch.bfloat16, device=DEV)
         for k, v in parts.items():
             plain[k][g] = v
-        if own and fmt in ("mxfp4", "nvfp4"):
+        if own and fmt != "bf16":
             w13[g], w2[g] = a, b
     handle = None
     if own:
         from combine_top_route_moe_amd import ops
-        if fmt == "fp8":                                            # the same codes and scales
-            handle = ops.FFNWeights(ops.MOE_W_FP8, G, H, I, _fp8_packed(plain["13w"], True),
-                                    _fp8_packed(plain["2w"], False), plain["13s"], plain["2s"])
-            return plain, handle
         handle = ops.ffn_weights(w13, w2, fmt, w13_tensor_scale=plain.get("13g"), w2_tensor_scale=plain.get("2g"))
     return plain, handle
 
