@@ -51,6 +51,7 @@ SIGNATURES = {
                                       _c_size, _vp, _vp]),
     "moe_pack_ffn_weights_fp4": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp,
                                           _vp, _vp, _vp, _vp]),
+    "moe_pack_ffn_codes": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
     "moe_grouped_ffn_fp4_workspace_bytes": (_c_size, [_c_i64, _c_int, _c_int, _c_int]),
     "moe_grouped_ffn_fp4": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_i64,
                                      _c_int, _vp, _c_size, _vp, _vp]),

@@ -40,6 +40,8 @@ int launch_grouped_ffn_w8a8(const uint8_t*, const float*, int64_t, const int32_t
                             hipStream_t);
 int launch_pack_weights_fp4(const uint16_t*, const uint16_t*, int, int, int, int, const float*,
                             const float*, uint8_t*, uint8_t*, uint8_t*, uint8_t*, hipStream_t);
+int launch_pack_codes(const moe_ffn_weights*, int, int, int, uint8_t*, uint8_t*, uint8_t*, uint8_t*,
+                      hipStream_t);
 size_t grouped_ffn_fp4_workspace_bytes(int64_t, int, int, int);
 int launch_grouped_ffn_fp4(const uint16_t*, const int32_t*, const int32_t*, int, int, int,
                            const moe_ffn_weights*, const float*, uint16_t*, int64_t, int, void*,
@@ -368,6 +370,25 @@ static bool weights_ok(const moe_ffn_weights* w, int stages) {
   };
   return (!(stages & MOE_FFN_GATE_UP) || matrix(w->w13, w->w13_scales, w->w13_tensor_scale)) &&
          (!(stages & MOE_FFN_DOWN) || matrix(w->w2, w->w2_scales, w->w2_tensor_scale));
+}
+
+int moe_pack_ffn_codes(const moe_ffn_weights* rows, int num_groups, int H, int I, uint8_t* w13q,
+                       uint8_t* w13_scales, uint8_t* w2q, uint8_t* w2_scales, void* stream) {
+  if (!rows || num_groups < 1 || H < 1 || I < 1) return MOE_ERR_INVALID_ARG;
+  const bool fp4 = rows->format == MOE_W_MXFP4 || rows->format == MOE_W_NVFP4;
+  if (!fp4 && rows->format != MOE_W_FP8) return MOE_ERR_INVALID_ARG;
+  if (H % 128 || I % 128 || H > (1 << 20) || I > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  // all of a matrix's pointers or none; FP8 scales are not moved
+  auto matrix = [&](const void* w, const void* s, const void* q, const void* sq) {
+    if (!w) return !q && (!fp4 || (!s && !sq));
+    if (!q || !aligned16(w) || !aligned16(q)) return false;
+    return !fp4 || (s && sq && aligned16(s) && aligned16(sq));
+  };
+  if (!matrix(rows->w13, rows->w13_scales, w13q, w13_scales) ||
+      !matrix(rows->w2, rows->w2_scales, w2q, w2_scales))
+    return MOE_ERR_INVALID_ARG;
+  return launch_pack_codes(rows, num_groups, H, I, w13q, w13_scales, w2q, w2_scales,
+                           as_stream(stream));
 }
 
 // What the kernels that stream weights address: an expert's matrix (w13, the

@@ -122,7 +122,8 @@ class MoELayer:
         "nvfp4") the weights become 4-bit codes with group scales
         (``moe_pack_ffn_weights_fp4``), routed and shared experts alike, read
         by ``moe_grouped_ffn_fp4``.  ``decode`` runs on any of these but
-        row-major weights and "w8a8"."""
+        row-major weights and "w8a8".  Weights that are codes already:
+        ``set_packed_weights``."""
         if shared_w13 is not None and shared_w13.dim() == 2:
             shared_w13, shared_w2 = shared_w13.unsqueeze(0), shared_w2.unsqueeze(0)
         if fp8 not in (False, True, "w8a8"):
@@ -131,23 +132,13 @@ class MoELayer:
             raise ValueError(f"unknown FP4 format {fp4!r}")
         if fp4 and (fp8 or not pack):
             raise ValueError("fp4 weights are packed, and neither fp8")
-        self.w8a8 = fp8 == "w8a8"
-        self.weights = self.shared_weights = None
         fmt = fp4 or ("fp8" if fp8 is True else "bf16" if pack and not fp8 else None)
         if fmt:
-            self.weights = ops.ffn_weights(w13, w2, fmt)
-            if shared_w13 is not None:
-                self.shared_weights = ops.ffn_weights(shared_w13, shared_w2, fmt)
-        if fp4:
-            self.packed, self.fp8_weights = True, False
-            self.w13 = self.w2 = self.weights
-            self.shared_w13 = self.shared_w2 = self.shared_weights
-            size = ops.moe_grouped_ffn_fp4_workspace_bytes
-            self.ffn_ws = self._workspace(self.ffn_ws, size(self.capacity, self.El, self.H, self.I))
-            if self.shared_I:
-                self.shared_ws = self._workspace(self.shared_ws,
-                                                 size(self.T, 1, self.H, self.shared_I))
+            self._take(ops.ffn_weights(w13, w2, fmt), None if shared_w13 is None else
+                       ops.ffn_weights(shared_w13, shared_w2, fmt))
             return
+        self.w8a8 = fp8 == "w8a8"
+        self.weights = self.shared_weights = None
         self.fp8_weights = bool(fp8)
         if self.w8a8:
             self._setup_w8a8()
@@ -159,21 +150,47 @@ class MoELayer:
                 self.shared_w13, self.shared_w2 = (q13, s13), (q2, s2)
             self.packed = True
             return
-        if fp8:
-            self.packed = True
-            w, sh = self.weights, self.shared_weights
-            self.w13, self.w2 = (w.w13, w.w13_scales), (w.w2, w.w2_scales)
-            self.shared_w13 = self.shared_w2 = None
-            if sh is not None:
-                self.shared_w13, self.shared_w2 = (sh.w13, sh.w13_scales), (sh.w2, sh.w2_scales)
-            return
-        self.packed = pack
-        if pack:
-            w13, w2 = self.weights.w13, self.weights.w2
-            if shared_w13 is not None:
-                shared_w13, shared_w2 = self.shared_weights.w13, self.shared_weights.w2
+        self.packed = False
         self.w13, self.w2 = w13, w2
         self.shared_w13, self.shared_w2 = shared_w13, shared_w2
+
+    def set_packed_weights(self, weights: ops.FFNWeights,
+                           shared: Optional[ops.FFNWeights] = None) -> None:
+        """Weights that are packed already, the local experts' and the shared
+        expert's (one group, the same format): a checkpoint's codes as they are
+        (``ops.ffn_weights_from_codes``), or one handle for several layers'
+        buffers."""
+        if (weights.num_groups, weights.H, weights.I) != (self.El, self.H, self.I):
+            raise ValueError(f"expected the weights of {self.El} experts, H = {self.H}, I = {self.I}")
+        if shared is not None:
+            if (shared.num_groups, shared.H, shared.I) != (1, self.H, self.shared_I):
+                raise ValueError(f"expected the shared expert's weights, H = {self.H}, "
+                                 f"I = {self.shared_I}")
+            if shared.format != weights.format:
+                raise ValueError("the shared expert's weights are of another format")
+        self._take(weights, shared)
+
+    def _take(self, weights: ops.FFNWeights, shared: Optional[ops.FFNWeights]) -> None:
+        self.weights, self.shared_weights = weights, shared
+        self.packed, self.w8a8 = True, False
+        self.fp8_weights = weights.format == ops.MOE_W_FP8
+        if weights.format in (ops.MOE_W_MXFP4, ops.MOE_W_NVFP4):
+            self.w13 = self.w2 = weights
+            self.shared_w13 = self.shared_w2 = shared
+            size = ops.moe_grouped_ffn_fp4_workspace_bytes
+            self.ffn_ws = self._workspace(self.ffn_ws, size(self.capacity, self.El, self.H, self.I))
+            if self.shared_I:
+                self.shared_ws = self._workspace(self.shared_ws,
+                                                 size(self.T, 1, self.H, self.shared_I))
+            return
+
+        def matrices(w):   # as the staged path takes them: FP8 codes with their scales
+            if w is None:
+                return None, None
+            return ((w.w13, w.w13_scales), (w.w2, w.w2_scales)) if self.fp8_weights else (w.w13, w.w2)
+
+        self.w13, self.w2 = matrices(weights)
+        self.shared_w13, self.shared_w2 = matrices(shared)
 
     def _workspace(self, ws: torch.Tensor, need: int) -> torch.Tensor:
         """``ws``, or a new buffer where it is too small."""

@@ -408,8 +408,9 @@ def moe_grouped_ffn_w8a8(xq: torch.Tensor, x_scales: torch.Tensor, cu_seqlens: t
 @dataclass(frozen=True, eq=False)
 class FFNWeights:
     """Packed expert weights in one format (``MOE_W_*``): what ``moe_decode``
-    and ``moe_grouped_ffn_fp4`` take.  Built by ``ffn_weights``, or from the
-    outputs of the pack functions."""
+    and ``moe_grouped_ffn_fp4`` take.  Built by ``ffn_weights`` from bf16
+    weights, by ``ffn_weights_from_codes`` from a checkpoint's codes, or from
+    the outputs of the pack functions."""
 
     format: int
     num_groups: int
@@ -484,6 +485,61 @@ def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
                                                              w2_tensor_scale)
     return FFNWeights(MOE_W_MXFP4 if fmt == "mxfp4" else MOE_W_NVFP4, G, H, I, q13, q2, s13, s2,
                       g13, g2)
+
+
+def ffn_weights_from_codes(fmt: str, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
+                           w2_scales: torch.Tensor,
+                           w13_tensor_scale: Optional[torch.Tensor] = None,
+                           w2_tensor_scale: Optional[torch.Tensor] = None,
+                           stream=None) -> FFNWeights:
+    """Row-major codes and scales that exist already (a checkpoint) in the
+    packed order, unchanged (``moe_pack_ffn_codes``).  ``fmt``: "fp8" (codes
+    [G, 2I, H] / [G, H, I], scales float32 [G, 2I/128, H/128] / [G, H/128,
+    I/128]), "mxfp4" or "nvfp4" (two codes a byte, [G, 2I, H/2] / [G, H, I/2],
+    scales one byte each, [.., H/32] / [.., I/32] or [.., H/16] / [.., I/16];
+    NVFP4's tensor scales [G] float32).  One-byte tensors may be uint8 or of
+    their 8-bit float type."""
+    formats = {"fp8": MOE_W_FP8, "mxfp4": MOE_W_MXFP4, "nvfp4": MOE_W_NVFP4}
+    if fmt not in formats:
+        raise ValueError(f"unknown code format {fmt!r}")
+    fp8 = fmt == "fp8"
+    group = 128 if fp8 else 32 if fmt == "mxfp4" else 16
+    if w13.dim() != 3 or w2.dim() != 3 or w13.shape[1] % 2:
+        raise ValueError("w13 and w2 must be [G, 2I, ..] and [G, H, ..]")
+    G, I, H = w13.shape[0], w13.shape[1] // 2, w2.shape[1]
+    half = 1 if fp8 else 2
+    f32, codes8 = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
+    scale8 = {"mxfp4": (torch.uint8, torch.float8_e8m0fnu), "nvfp4": codes8}.get(fmt)
+
+    def want(t, shape, dtypes, name):
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: expected {dtypes[0]}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        return t.view(torch.uint8) if dtypes is not f32 else t
+
+    n = (lambda rows: rows // 128) if fp8 else (lambda rows: rows)   # rows of scales
+    codes = codes8 if fp8 else (torch.uint8,)
+    scales = f32 if fp8 else scale8
+    w13 = want(w13, (G, 2 * I, H // half), codes, "w13")
+    w2 = want(w2, (G, H, I // half), codes, "w2")
+    s13 = want(w13_scales, (G, n(2 * I), H // group), scales, "w13_scales")
+    s2 = want(w2_scales, (G, n(H), I // group), scales, "w2_scales")
+    g13 = g2 = None
+    if fmt == "nvfp4":
+        if w13_tensor_scale is None or w2_tensor_scale is None:
+            raise ValueError("NVFP4 codes need their tensor scales")
+        g13 = want(w13_tensor_scale, (G,), f32, "w13_tensor_scale")
+        g2 = want(w2_tensor_scale, (G,), f32, "w2_tensor_scale")
+    _one_device(stream, w13, w2, s13, s2, g13, g2)
+    with torch.cuda.stream(stream):   # (the current one where it is None)
+        rows = FFNWeightsStruct(formats[fmt], _ptr(w13), None if fp8 else _ptr(s13), None, _ptr(w2),
+                                None if fp8 else _ptr(s2), None)
+        q13, q2 = torch.empty_like(w13), torch.empty_like(w2)
+        p13, p2 = (s13.clone(), s2.clone()) if fp8 else (torch.empty_like(s13), torch.empty_like(s2))
+        check("moe_pack_ffn_codes", load().moe_pack_ffn_codes(
+            ctypes.addressof(rows), G, H, I, _ptr(q13), _ptr(p13), _ptr(q2), _ptr(p2), _stream()))
+    return FFNWeights(formats[fmt], G, H, I, q13, q2, p13, p2, g13, g2)
 
 
 def _tensor_scales(w: torch.Tensor) -> torch.Tensor:

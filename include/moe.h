@@ -399,6 +399,26 @@ int moe_pack_ffn_weights_fp4(const uint16_t* w13, const uint16_t* w2, int num_gr
                              const float* w2_tensor_scale, uint8_t* w13q, uint8_t* w13_scales,
                              uint8_t* w2q, uint8_t* w2_scales, void* stream);
 
+/* Expert weights that are codes and scales already (a checkpoint in one of the
+ * formats), moved byte by byte into the packed order: the products then read
+ * exactly the values that are stored, which quantizing the dequantized weights
+ * again does not promise.  rows: format MOE_W_FP8, MOE_W_MXFP4 or MOE_W_NVFP4
+ * and device pointers to row-major matrices,
+ *   FP8    w13 [G, 2I, H], w2 [G, H, I] E4M3 codes, one byte each; the tile
+ *     scales ([G, 2I/128, H/128] and [G, H/128, I/128] float32, any values)
+ *     have the same order packed: they are not read or written here, and
+ *     w13_scales, w2_scales out are ignored;
+ *   MXFP4, NVFP4  w13 [G, 2I, H/2], w2 [G, H, I/2] E2M1 codes, two a byte, the
+ *     even column in the low half; scales one byte each, [G, 2I, H/32] and
+ *     [G, H, I/32] E8M0 (below 255), or [G, 2I, H/16] and [G, H, I/16] E4M3.
+ * Tensor scales stay as they are and are not read.  Outputs: as
+ * moe_pack_ffn_weights_fp8 (flags 0) and moe_pack_ffn_weights_fp4 write them;
+ * they must not alias the inputs.  Either matrix (its codes and scales, in and
+ * out) may be NULL altogether.  Pointers 16-byte aligned.  Runs once at load
+ * time.  Requires H % 128 == 0, I % 128 == 0, both <= 2^20. */
+int moe_pack_ffn_codes(const moe_ffn_weights* rows, int num_groups, int H, int I, uint8_t* w13q,
+                       uint8_t* w13_scales, uint8_t* w2q, uint8_t* w2_scales, void* stream);
+
 /* moe_grouped_ffn with 4-bit weights (format MOE_W_MXFP4 or MOE_W_NVFP4): the
  * same operation, segments, stage flags and errors, where every weight the
  * products read is the value its code stands for; bf16 rows.  From a single
