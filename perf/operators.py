@@ -167,6 +167,8 @@ def _expert_weights(gen, fmt, G, H, I):
     handle = None
     if own:
         from combine_top_route_moe_amd import ops
+        if fmt == "fp8":                                            # the checkpoint's codes, as they are
+            return plain, ops.ffn_weights_from_codes(fmt, plain["13w"], plain["13s"], plain["2w"], plain["2s"])
         handle = ops.ffn_weights(w13, w2, fmt, w13_tensor_scale=plain.get("13g"), w2_tensor_scale=plain.get("2g"))
     return plain, handle
 
