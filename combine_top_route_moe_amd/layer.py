@@ -151,6 +151,7 @@ class MoELayer:
             self.packed = True
             return
         self.packed = False
+        self._setup_rows()
         self.w13, self.w2 = w13, w2
         self.shared_w13, self.shared_w2 = shared_w13, shared_w2
 
@@ -174,6 +175,7 @@ class MoELayer:
         self.weights, self.shared_weights = weights, shared
         self.packed, self.w8a8 = True, False
         self.fp8_weights = weights.format == ops.MOE_W_FP8
+        self._setup_rows()
         if weights.format in (ops.MOE_W_MXFP4, ops.MOE_W_NVFP4):
             self.w13 = self.w2 = weights
             self.shared_w13 = self.shared_w2 = shared
@@ -197,6 +199,17 @@ class MoELayer:
         if ws.numel() >= need:
             return ws
         return torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _setup_rows(self) -> None:
+        """Buffers for bf16 rows, as the constructor allocates them: after the
+        FP8 path they are sized for its codes, half a row's bytes."""
+        if self.perm.x_perm.shape[1] == self.H:
+            return
+        self.perm = ops.alloc_permuted(self.T, self.K, self.H, self.El, self.capacity, self.device)
+        size = ops.moe_grouped_ffn_workspace_bytes
+        self.ffn_ws = self._workspace(self.ffn_ws, size(self.capacity, self.El, self.H, self.I))
+        if self.shared_I:
+            self.shared_ws = self._workspace(self.shared_ws, size(self.T, 1, self.H, self.shared_I))
 
     def _setup_w8a8(self) -> None:
         """Buffers of the FP8 path: the [T, H] rows' codes and scales, the

@@ -203,3 +203,22 @@ def test_refusals():
     c13, b13, c2, b2 = (t.view(2, 256, -1) for t in codes)
     with pytest.raises(ValueError, match="tensor scales"):
         ops.ffn_weights_from_codes("nvfp4", c13, b13, c2, b2)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(fp8=True), dict(fp4="nvfp4")], ids=["bf16", "fp8", "nvfp4"])
+def test_weights_after_the_fp8_path(kw):
+    """A layer that held "w8a8" weights gives the bits of a new one."""
+    T, H, E, K, I, sI = 70, 512, 8, 2, 128, 128
+    rng = np.random.default_rng(8)
+    w = [dev_bf16(m) for m in (*fu.make_weights(rng, E, H, I), *fu.make_weights(rng, 1, H, sI))]
+    logits, x = dev(rng.standard_normal((T, E)).astype(np.float32)), dev_bf16(fu.bf16(rng.standard_normal((T, H))))
+    outs = []
+    for first in (False, True):
+        layer = MoELayer(T, H, E, K, I, shared_I=sI)
+        if first:
+            layer.set_weights(*w, fp8="w8a8")
+            layer.forward(logits, x)
+        layer.set_weights(*w, **kw)
+        outs.append(layer.forward(logits, x).clone())
+        assert int(layer.dev_error.item()) == 0
+    assert torch.equal(outs[0], outs[1])

@@ -1,0 +1,47 @@
+"""MoELayer's buffers as its weights change kind.  No GPU needed: the buffers
+are host tensors, and the packing calls are stood in for."""
+
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from combine_top_route_moe_amd import MoELayer, ops
+
+T, H, E, K, I, SI = 40, 256, 4, 2, 128, 256
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    def packed(w13, w2, fmt="bf16", **kw):
+        G, two_i, Hd = w13.shape
+        f = {"bf16": ops.MOE_W_BF16, "fp8": ops.MOE_W_FP8, "mxfp4": ops.MOE_W_MXFP4, "nvfp4": ops.MOE_W_NVFP4}[fmt]
+        return SimpleNamespace(format=f, num_groups=G, H=Hd, I=two_i // 2, w13=w13, w2=w2, w13_scales=w13,
+                               w2_scales=w2)
+
+    monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: None)
+    monkeypatch.setattr(ops, "ffn_weights", packed)
+    monkeypatch.setattr(ops, "moe_pack_ffn_weights_fp8", lambda a, b, k128=False: (a, a, b, b))
+    return MoELayer(T, H, E, K, I, device="cpu", shared_I=SI)
+
+
+def _weights():
+    bf = dict(dtype=torch.bfloat16)
+    return (torch.zeros(E, 2 * I, H, **bf), torch.zeros(E, H, I, **bf), torch.zeros(2 * SI, H, **bf),
+            torch.zeros(H, SI, **bf))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(pack=False), dict(fp8=True), dict(fp4="mxfp4"), dict(fp4="nvfp4")],
+                         ids=lambda kw: "-".join(f"{k}={v}" for k, v in kw.items()) or "bf16")
+def test_rows_are_whole_again_after_the_fp8_path(layer, kw):
+    """"w8a8" moves the rows' codes, half the bytes of bf16 rows: with any
+    other weights after it the permute must find buffers for whole rows, and
+    the FFN its workspace."""
+    layer.set_weights(*_weights(), fp8="w8a8")
+    assert layer.perm.x_perm.shape == (layer.capacity, H // 2)
+    layer.set_weights(*_weights(), **kw)
+    assert not layer.w8a8
+    assert layer.perm.x_perm.shape == (layer.capacity, H)
+    size = ops.moe_grouped_ffn_fp4_workspace_bytes if "fp4" in kw else ops.moe_grouped_ffn_workspace_bytes
+    assert layer.ffn_ws.numel() >= size(layer.capacity, E, H, I)
+    assert layer.shared_ws.numel() >= size(T, 1, H, SI)
