@@ -345,13 +345,19 @@ static bool few_rows(int64_t capacity, int G, int H, int I) {
 }
 
 // Both forms', the few-row one's up to the capacities it is taken for: a buffer
-// for the largest batch does for every smaller one.
+// for the largest batch does for every smaller one.  As a tile's walk grows with
+// its rows, the rule can give tiles from 8 rows a group on, the few-row kernels
+// again from about 10 and tiles from about 12 (where the weights take 1.08 to 1.13
+// times the shortest walk: 26 groups, H = 4096, I = 1536; at 268 to 312 rows, few /
+// tile in us, MXFP4 59 to 62 / 54, NVFP4 64 to 66 / 74); the sizes in between
+// hold the tiles of the smaller ones, too.
 size_t grouped_ffn_fp4_workspace_bytes(int64_t capacity, int G, int H, int I) {
   if (capacity == 0) return 0;
   const double walk = kWalkBytes * ((double)H + I) * (1.0 + kBM / 96.0) / (1.6 * H * I);
   const int64_t most = (int64_t)std::max(8.0 * G, 12.0 * std::max((double)G, walk)) + 1;
   const size_t few = few_ffn_workspace_bytes(std::min(capacity, most), I);
-  if (few_rows(capacity, G, H, I)) return few;
+  const int64_t eight = std::min<int64_t>(capacity, 8LL * G);   // where tiles are first taken
+  if (few_rows(capacity, G, H, I) && few_rows(eight, G, H, I)) return few;
   const int64_t rows = ((capacity + kBM - 1) / kBM + G) * kBM;
   return std::max(few, (((size_t)rows * I * 2) + 255) & ~(size_t)255);
 }
