@@ -194,6 +194,17 @@ __device__ __forceinline__ void fp4_tile_body(u32x4_t (*As)[kTileSub][4][kWave],
   }
 }
 
+// Row tiles of all groups, as decode_tile counts them (every lane active).
+__device__ __forceinline__ long long total_row_tiles(const int32_t* __restrict__ counts, int G,
+                                                     int64_t capacity) {
+  long long n = 0;
+  for (int e = threadIdx.x & 63; e < G; e += kWave)
+    n += (min((int64_t)max(counts[e], 0), capacity) + kBM - 1) / kBM;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+  return n;
+}
+
 template <bool GATE_UP, int FMT>
 __global__ void __launch_bounds__(kTileWaves * kWave, 2) fp4_tile_kernel(
     const uint16_t* __restrict__ A, WMat W, const int32_t* __restrict__ cu_seqlens,
@@ -209,8 +220,13 @@ __global__ void __launch_bounds__(kTileWaves * kWave, 2) fp4_tile_kernel(
   int64_t mt_before;
   if (!decode_tile(pid, counts, G, n_cb, capacity, g, mt, cb, &mt_before)) return;
   // the intermediate's m-tile must lie in the workspace (ceil(capacity/128)
-  // + G m-tiles): overlapping segments could place it past the end
-  if (mt_before + mt >= (capacity + kBM - 1) / kBM + G) {
+  // + G m-tiles): overlapping segments could place it past the end, or past the
+  // grid, whose last workgroup has no tile of disjoint segments
+  const int64_t most = (capacity + kBM - 1) / kBM + G;
+  if (pid == (int)gridDim.x - 1 && total_row_tiles(counts, G, capacity) > most &&
+      (threadIdx.x & 63) == 0)
+    raise_error(dev_error, MOE_DEVERR_ROW_RANGE);
+  if (mt_before + mt >= most) {
     if ((threadIdx.x & 63) == 0) raise_error(dev_error, MOE_DEVERR_ROW_RANGE);
     return;
   }
