@@ -11,9 +11,10 @@ Order of the stages (titles of the pages they come from):
   shared expert   Mega-MoE page: a fused shared expert's slot, added last
   combine (+QDQ)  Mega-MoE page, PR summary and "How it works"
 
-Every buffer is allocated once in the constructor (torch is the allocator);
-``forward`` only enqueues kernels on the current stream, never synchronizes
-and never allocates, so it can be timed back to back or captured in a graph.
+Every buffer of ``forward`` is allocated once, in the constructor or with the
+weights (torch is the allocator); ``forward`` only enqueues kernels on the
+current stream, never synchronizes and never allocates, so it can be timed
+back to back or captured in a graph.
 """
 
 from __future__ import annotations
@@ -97,8 +98,7 @@ class MoELayer:
         self.w8a8 = False
         self.weights = self.shared_weights = None   # decode()'s handles of the packed weights
         self.decode_tokens = min(T, ops.MOE_DECODE_MAX_TOKENS)
-        self.decode_ws = torch.empty(max(ops.moe_decode_workspace_bytes(
-            self.decode_tokens, H, I, K, self.El, shared_I), 1), dtype=torch.uint8, device=dev)
+        self.decode_ws = None                       # of decode()'s first call
 
     # ------------------------------------------------------------------ weights
     def set_weights(self, w13: torch.Tensor, w2: torch.Tensor,
@@ -341,8 +341,9 @@ class MoELayer:
         """The layer for a few tokens in three launches or so (``moe_decode``):
         ``hidden`` [n, H] with n <= min(T, 64).  The routes of those n tokens are
         left in ``topk_idx[:n]`` / ``topk_w[:n]``; with ``logits`` None they are
-        taken from there.  Returns ``out[:n]``.  Enqueue only: no sync, no
-        allocation.  The rows are not rounded before the combine, so the result
+        taken from there.  Returns ``out[:n]``.  Enqueue only: no sync, and
+        no allocation after the first call's of the workspace (for the largest
+        batch).  The rows are not rounded before the combine, so the result
         differs from ``forward``'s by that rounding; a layer with row
         quantizers (dispatch or combine) has no such form."""
         if self.weights is None:
@@ -354,6 +355,10 @@ class MoELayer:
         n = hidden.shape[0]
         if n > self.decode_tokens:
             raise ValueError(f"decode takes up to {self.decode_tokens} tokens here, got {n}")
+        if self.decode_ws is None:
+            need = ops.moe_decode_workspace_bytes(self.decode_tokens, self.H, self.I, self.K, self.El,
+                                                  self.shared_I)
+            self.decode_ws = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
         ops.moe_decode(logits, hidden, self.K, self.weights, row_valid=row_valid,
                        renormalize=self.renormalize, expert_begin=self.expert_begin,
                        num_experts=self.E, shared=self.shared_weights if self.shared_I else None,

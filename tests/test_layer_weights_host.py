@@ -45,3 +45,19 @@ def test_rows_are_whole_again_after_the_fp8_path(layer, kw):
     size = ops.moe_grouped_ffn_fp4_workspace_bytes if "fp4" in kw else ops.moe_grouped_ffn_workspace_bytes
     assert layer.ffn_ws.numel() >= size(layer.capacity, E, H, I)
     assert layer.shared_ws.numel() >= size(T, 1, H, SI)
+
+
+def test_decodes_workspace_is_of_its_first_call(layer, monkeypatch):
+    """A layer that only runs prompts, or cannot decode, holds no workspace for
+    decode(); one that does allocates it once, for its largest batch."""
+    used = []
+    monkeypatch.setattr(ops, "moe_decode", lambda *a, workspace, **kw: used.append(workspace))
+    size = ops.moe_decode_workspace_bytes(T, H, I, K, E, SI)
+    held = lambda: [n for n, t in vars(layer).items()  # noqa: E731
+                    if torch.is_tensor(t) and t.dtype == torch.uint8 and n.startswith("decode")]
+    assert not held()
+    layer.set_weights(*_weights())
+    assert not held()
+    for n in (1, T, 7):
+        layer.decode(torch.zeros(n, E), torch.zeros(n, H, dtype=torch.bfloat16))
+    assert used[0] is used[1] is used[2] and used[0].numel() >= size
