@@ -134,8 +134,10 @@ class MoELayer:
             raise ValueError("fp4 weights are packed, and neither fp8")
         fmt = fp4 or ("fp8" if fp8 is True else "bf16" if pack and not fp8 else None)
         if fmt:
-            self._take(ops.ffn_weights(w13, w2, fmt), None if shared_w13 is None else
-                       ops.ffn_weights(shared_w13, shared_w2, fmt))
+            # bf16 and FP8 weights may lie on another device than the current one
+            one = ops.ffn_weights if fp4 else ops._packed
+            self._take(one(w13, w2, fmt),
+                       None if shared_w13 is None else one(shared_w13, shared_w2, fmt))
             return
         self.w8a8 = fp8 == "w8a8"
         self.weights = self.shared_weights = None

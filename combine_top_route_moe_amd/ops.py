@@ -458,33 +458,44 @@ class FFNWeights:
                       "w2_tensor_scale"))))
 
 
-def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
-                w13_tensor_scale: Optional[torch.Tensor] = None,
-                w2_tensor_scale: Optional[torch.Tensor] = None, stream=None) -> FFNWeights:
-    """Pack bf16 w13 [G,2I,H] / w2 [G,H,I] once into ``fmt``: "bf16", "fp8",
-    "mxfp4" or "nvfp4" (its tensor scales [G] from the weights' amax where
-    they are not given)."""
+def _group_sizes(w13: torch.Tensor, w2: torch.Tensor):
+    """(G, H, I) of bf16 w13 [G,2I,H] / w2 [G,H,I]."""
     _want(w13, torch.bfloat16, "w13")
     _want(w2, torch.bfloat16, "w2")
     G, two_i, H = w13.shape
     I = two_i // 2
     if tuple(w2.shape) != (G, H, I) or two_i % 2:
         raise ValueError("w13 must be [G, 2I, H] and w2 [G, H, I]")
+    return G, H, I
+
+
+def _packed(w13: torch.Tensor, w2: torch.Tensor, fmt: str, *tensor_scales) -> FFNWeights:
+    """``ffn_weights`` on the current device's stream; bf16 and FP8 weights may
+    lie on another device, as for their pack calls."""
+    G, H, I = _group_sizes(w13, w2)
+    if fmt == "bf16":
+        return FFNWeights(MOE_W_BF16, G, H, I, *moe_pack_ffn_weights(w13, w2))
+    if fmt == "fp8":
+        q13, s13, q2, s2 = moe_pack_ffn_weights_fp8(w13, w2)
+        return FFNWeights(MOE_W_FP8, G, H, I, q13, q2, s13, s2)
+    mode = MOE_FQ_MXFP4 if fmt == "mxfp4" else MOE_FQ_NVFP4
+    q13, s13, g13, q2, s2, g2 = moe_pack_ffn_weights_fp4(w13, w2, mode, *tensor_scales)
+    return FFNWeights(MOE_W_MXFP4 if fmt == "mxfp4" else MOE_W_NVFP4, G, H, I, q13, q2, s13, s2,
+                      g13, g2)
+
+
+def ffn_weights(w13: torch.Tensor, w2: torch.Tensor, fmt: str = "bf16",
+                w13_tensor_scale: Optional[torch.Tensor] = None,
+                w2_tensor_scale: Optional[torch.Tensor] = None, stream=None) -> FFNWeights:
+    """Pack bf16 w13 [G,2I,H] / w2 [G,H,I] once into ``fmt``: "bf16", "fp8",
+    "mxfp4" or "nvfp4" (its tensor scales [G] from the weights' amax where
+    they are not given)."""
+    _group_sizes(w13, w2)
     if fmt not in ("bf16", "fp8", "mxfp4", "nvfp4"):
         raise ValueError(f"unknown weight format {fmt!r}")
     _one_device(stream, w13, w2, w13_tensor_scale, w2_tensor_scale)
     with torch.cuda.stream(stream):   # (the current one where it is None)
-        if fmt == "bf16":
-            p13, p2 = moe_pack_ffn_weights(w13, w2)
-            return FFNWeights(MOE_W_BF16, G, H, I, p13, p2)
-        if fmt == "fp8":
-            q13, s13, q2, s2 = moe_pack_ffn_weights_fp8(w13, w2)
-            return FFNWeights(MOE_W_FP8, G, H, I, q13, q2, s13, s2)
-        mode = MOE_FQ_MXFP4 if fmt == "mxfp4" else MOE_FQ_NVFP4
-        q13, s13, g13, q2, s2, g2 = moe_pack_ffn_weights_fp4(w13, w2, mode, w13_tensor_scale,
-                                                             w2_tensor_scale)
-    return FFNWeights(MOE_W_MXFP4 if fmt == "mxfp4" else MOE_W_NVFP4, G, H, I, q13, q2, s13, s2,
-                      g13, g2)
+        return _packed(w13, w2, fmt, w13_tensor_scale, w2_tensor_scale)
 
 
 def ffn_weights_from_codes(fmt: str, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,

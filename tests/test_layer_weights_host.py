@@ -1,6 +1,7 @@
 """MoELayer's buffers as its weights change kind.  No GPU needed: the buffers
 are host tensors, and the packing calls are stood in for."""
 
+from contextlib import nullcontext
 from types import SimpleNamespace
 
 import pytest
@@ -13,15 +14,15 @@ T, H, E, K, I, SI = 40, 256, 4, 2, 128, 256
 
 @pytest.fixture
 def layer(monkeypatch):
-    def packed(w13, w2, fmt="bf16", **kw):
-        G, two_i, Hd = w13.shape
-        f = {"bf16": ops.MOE_W_BF16, "fp8": ops.MOE_W_FP8, "mxfp4": ops.MOE_W_MXFP4, "nvfp4": ops.MOE_W_NVFP4}[fmt]
-        return SimpleNamespace(format=f, num_groups=G, H=Hd, I=two_i // 2, w13=w13, w2=w2, w13_scales=w13,
-                               w2_scales=w2)
-
+    fields = ("format", "num_groups", "H", "I", "w13", "w2", "w13_scales", "w2_scales", "w13_tensor_scale",
+              "w2_tensor_scale")
+    monkeypatch.setattr(ops, "FFNWeights", lambda *a: SimpleNamespace(**dict(zip(fields, a))))
+    monkeypatch.setattr(ops, "_one_device", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
     monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: None)
-    monkeypatch.setattr(ops, "ffn_weights", packed)
+    monkeypatch.setattr(ops, "moe_pack_ffn_weights", lambda a, b: (a, b))
     monkeypatch.setattr(ops, "moe_pack_ffn_weights_fp8", lambda a, b, k128=False: (a, a, b, b))
+    monkeypatch.setattr(ops, "moe_pack_ffn_weights_fp4", lambda a, b, *rest: (a, a, None, b, b, None))
     return MoELayer(T, H, E, K, I, device="cpu", shared_I=SI)
 
 
@@ -61,3 +62,17 @@ def test_decodes_workspace_is_of_its_first_call(layer, monkeypatch):
     for n in (1, T, 7):
         layer.decode(torch.zeros(n, E), torch.zeros(n, H, dtype=torch.bfloat16))
     assert used[0] is used[1] is used[2] and used[0].numel() >= size
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(fp8=True), dict(fp8="w8a8"), dict(pack=False)],
+                         ids=["bf16", "fp8", "w8a8", "rows"])
+def test_weights_on_another_device_are_taken(layer, monkeypatch, kw):
+    """These kinds of weights are packed on the current device's stream wherever
+    they lie; only calls that were never made so refuse it."""
+    def refuse(*a):
+        raise ValueError("another device is current")
+
+    monkeypatch.setattr(ops, "_one_device", refuse)
+    layer.set_weights(*_weights(), **kw)
+    with pytest.raises(ValueError, match="another device"):
+        layer.set_weights(*_weights(), fp4="mxfp4")
