@@ -674,7 +674,8 @@ def moe_decode(logits: Optional[torch.Tensor], hidden: torch.Tensor, k: int, wei
     the same format)."""
     T, H = hidden.shape
     if logits is not None:
-        if logits.shape[0] != T or num_experts not in (None, logits.shape[1]):
+        if (logits.dim() != 2 or logits.shape[0] != T or
+                num_experts not in (None, logits.shape[1])):
             raise ValueError("logits must be [T, num_experts]")
         num_experts = logits.shape[1]
     elif topk_idx is None or topk_w is None:
