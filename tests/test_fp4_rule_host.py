@@ -36,3 +36,16 @@ def test_sizes_hold_tiles_from_the_first_capacity_that_takes_them(G, H, I):
     assert n >= min(8 * G, top)
     for m in range(n, top):
         assert ops.moe_grouped_ffn_fp4_workspace_bytes(m, G, H, I) >= _tile(m, G, I)
+
+
+def test_the_numerics_cases_reach_both_forms():
+    """Which kernels the cases of test_gpu_fp4_ffn.py run, so that neither form
+    can drop out of them unnoticed."""
+    from tests.test_gpu_fp4_ffn import FEW, MANY, TILE
+
+    for form, cases in (("few", FEW + MANY), ("tile", TILE)):
+        for counts, H, I in cases:
+            n, G = sum(counts), len(counts)
+            size = ops.moe_grouped_ffn_fp4_workspace_bytes(n, G, H, I)
+            assert (size == _few(n, I)) == (form == "few"), (counts[:8], H, I)
+            assert form == "few" or size >= _tile(n, G, I)
