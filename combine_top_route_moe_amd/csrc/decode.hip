@@ -551,7 +551,7 @@ __device__ __forceinline__ SmallPlan small_plan(int e, int n_slots, int T, int l
 // 7168, I = 2048) 83 us in bf16, 6.4 TB/s, 29 in MXFP4, where a plain read of as
 // many bytes takes 24; 13 tokens of 64 experts in FP8 (H = 2048, I = 1024) 42,
 // a plain read 33.  NVFP4 by its conversion: 24 tokens of 128 experts, top-8 (H =
-// 4096, I = 1536) 135 us, 5.2 TB/s.
+// 4096, I = 1536) 136 us, 5.2 TB/s, the vector units busy 87 % of the time.
 template <int FMT, int NW, bool NARROW, int EPL>
 __global__ void __launch_bounds__(NW * kWave, (FewShape<FMT, NARROW>::kWaves)) decode_gate_up_kernel(
     const uint16_t* __restrict__ x, int T, int H, int I, WMat routed, WMat shared, int sI,
@@ -994,8 +994,9 @@ int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t*
 // order; a run's place follows from a scan of the counts by every wave (its
 // answer the same in every lane).  A segment that leaves [0, capacity) has no
 // runs and raises ROW_RANGE.  333 ragged rows of 64 experts (H = 2048, I = 1024),
-// NVFP4, take 28 + 18 us, bound by the conversion; one row of one expert, MXFP4,
-// 7 + 5, the launches.  Returns false past the last run; `total` is the
+// NVFP4, take 28 + 19 us, bound by the conversion (the vector units busy 83 and
+// 71 % of the time), 59 runs of 51 experts reading 135 MB past the L2 for gate/up's 120; one
+// row of one expert, MXFP4, 6 + 5, the launches.  Returns false past the last run; `total` is the
 // number of runs then.
 struct RowRun {
   int g, row0, cnt;

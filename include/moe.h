@@ -463,7 +463,8 @@ int moe_grouped_ffn_fp4(const uint16_t* x, const int32_t* cu_seqlens, const int3
  *     shared_I must be 0 without it).
  *   workspace of moe_decode_workspace_bytes(), contents on entry ignored.
  * flags: MOE_ROUTE_RENORM.  A token without a local expert and without a
- * shared row gets +0.  T = 0 enqueues nothing.
+ * shared row gets +0.  T = 0 enqueues nothing.  Weights are finite: an
+ * infinite one gives NaN where a's low part is zero or of the other sign.
  * Requires T <= 64, H % 128 == I % 128 == shared_I % 128 == 0, each of them
  * <= 2^20, K <= min(num_experts, 32), num_experts <= 1024, and every expert's
  * w13 and w2 in less than 4 GiB each; sizes that need
