@@ -995,9 +995,9 @@ int launch_decode(const float* logits, const uint8_t* row_valid, const uint16_t*
 // answer the same in every lane).  A segment that leaves [0, capacity) has no
 // runs and raises ROW_RANGE.  333 ragged rows of 64 experts (H = 2048, I = 1024),
 // NVFP4, take 28 + 19 us, bound by the conversion (the vector units busy 83 and
-// 71 % of the time), 59 runs of 51 experts reading 135 MB past the L2 for gate/up's 120; one
-// row of one expert, MXFP4, 6 + 5, the launches.  Returns false past the last run; `total` is the
-// number of runs then.
+// 71 % of the time), 59 runs of 51 experts reading 135 MB past the L2 for
+// gate/up's 120; one row of one expert, MXFP4, 6 + 5, the launches.  Returns
+// false past the last run; `total` is the number of runs then.
 struct RowRun {
   int g, row0, cnt;
 };
