@@ -171,6 +171,9 @@ class MoELayer:
                                  f"I = {self.shared_I}")
             if shared.format != weights.format:
                 raise ValueError("the shared expert's weights are of another format")
+        for w in (weights, shared):
+            if w is not None and w.w13.device != self.out.device:
+                raise ValueError(f"the layer is on {self.out.device}, weights on {w.w13.device}")
         self._take(weights, shared)
 
     def _take(self, weights: ops.FFNWeights, shared: Optional[ops.FFNWeights]) -> None:

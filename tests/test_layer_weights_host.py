@@ -76,3 +76,10 @@ def test_weights_on_another_device_are_taken(layer, monkeypatch, kw):
     layer.set_weights(*_weights(), **kw)
     with pytest.raises(ValueError, match="another device"):
         layer.set_weights(*_weights(), fp4="mxfp4")
+
+
+def test_packed_weights_lie_where_the_layer_does(layer):
+    bf = dict(dtype=torch.bfloat16, device="meta")
+    w = ops._packed(torch.zeros(E, 2 * I, H, **bf), torch.zeros(E, H, I, **bf), "bf16")
+    with pytest.raises(ValueError, match="weights on meta"):
+        layer.set_packed_weights(w)
