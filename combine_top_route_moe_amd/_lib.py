@@ -12,6 +12,7 @@ import os
 from ._build import LIB
 
 _c_int, _c_i64, _c_size, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+_c_float = ctypes.c_float
 
 
 
@@ -65,6 +66,21 @@ SIGNATURES = {
                              _vp]),
     "moe_combine_check": (_c_int, [_vp, _c_i64, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp,
                                    _vp]),
+    "moe_rmsnorm": (_c_int, [_vp, _vp, _vp, _c_i64, _c_int, _c_float, _c_int, _vp, _vp, _vp, _vp,
+                             _c_i64, _vp, _vp]),
+    "moe_rmsnorm_backward_workspace_bytes": (_c_size, [_c_i64, _c_int]),
+    "moe_rmsnorm_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int, _vp, _vp, _vp,
+                                      _vp, _c_size, _vp]),
+    "moe_linear_fp8_packed_bytes": (_c_size, [_c_int, _c_int]),
+    "moe_pack_linear_fp8": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_linear_fp8_workspace_bytes": (_c_size, [_c_i64, _c_int, _c_int]),
+    "moe_linear_fp8": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp, _vp, _c_int, _vp,
+                                _vp, _c_size, _vp]),
+    "moe_balance_loss_workspace_bytes": (_c_size, [_c_int, _c_int]),
+    "moe_balance_loss": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp,
+                                  _c_size, _vp, _vp]),
+    "moe_route_backward": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
+                                    _vp, _vp, _vp, _vp, _vp]),
     "moe_copy_bytes": (_c_int, [_vp, _vp, _c_size, _vp]),
     "moe_read_bytes": (_c_int, [_vp, _c_size, _vp, _vp]),
 }

@@ -50,6 +50,22 @@ size_t decode_workspace_bytes(int, int, int, int, int, int);
 int launch_decode(const float*, const uint8_t*, const uint16_t*, int, int, int, int, int, int, int,
                   int, int32_t*, float*, const moe_ffn_weights*, const moe_ffn_weights*, int,
                   uint16_t*, void*, int32_t*, hipStream_t);
+int launch_rmsnorm(const uint16_t*, const uint16_t*, const void*, int, int64_t, int, float,
+                   uint16_t*, uint16_t*, uint8_t*, float*, int64_t, float*, hipStream_t);
+size_t rmsnorm_backward_workspace_bytes(int64_t, int);
+int launch_rmsnorm_backward(const uint16_t*, const uint16_t*, const float*, const void*, int,
+                            int64_t, int, const uint16_t*, uint16_t*, float*, void*, hipStream_t);
+int launch_pack_linear_fp8(const uint16_t*, const uint8_t*, const float*, int, int, int, uint8_t*,
+                           float*, hipStream_t);
+size_t linear_fp8_workspace_bytes(int64_t, int, int);
+int launch_linear_fp8(const uint8_t*, const float*, int64_t, int64_t, int, int, const uint8_t*,
+                      const float*, void*, int, void*, hipStream_t);
+size_t balance_loss_workspace_bytes(int, int);
+int launch_balance_loss(const float*, const uint8_t*, const int32_t*, int, int, int, float*,
+                        int32_t*, float*, int32_t*, void*, int32_t*, hipStream_t);
+int launch_route_backward(const float*, const uint8_t*, const int32_t*, const float*, const float*,
+                          int, int, int, int, const float*, const int32_t*, const int32_t*, float*,
+                          int32_t*, hipStream_t);
 
 // Each workgroup copies runs of 4 x 256 vectors: the four loads of a thread
 // are in flight together, and both sides stream past the caches
@@ -511,6 +527,126 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
     return MOE_ERR_INVALID_ARG;
   return launch_combine_check(rows, num_rows, row_of, shared, T, K, H, kernel_out, state,
                               dev_error, as_stream(stream));
+}
+
+static bool norm_size_ok(int64_t T, int H) {
+  return H % 128 == 0 && H <= 32768 && T <= (H <= 2048 ? 1 << 26 : H <= 8192 ? 1 << 24 : 1 << 22);
+}
+
+int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,
+                float eps, int flags, uint16_t* h, uint16_t* y, uint8_t* codes, float* scales,
+                int64_t scale_stride, float* rstd, void* stream) {
+  if (T < 0 || H < 1 || (flags & ~MOE_NORM_WEIGHT_F32)) return MOE_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !(eps <= 3.402823466e38f)) return MOE_ERR_INVALID_ARG;
+  if (!norm_size_ok(T, H)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!codes != !scales || (codes && scale_stride < T)) return MOE_ERR_INVALID_ARG;
+  if (!x || !weight || (!h && !y && !codes && !rstd)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) ||
+      !aligned16(y) || !aligned16(codes))
+    return MOE_ERR_INVALID_ARG;
+  if (y && (y == residual || y == h)) return MOE_ERR_INVALID_ARG;
+  return launch_rmsnorm(x, residual, weight, flags & MOE_NORM_WEIGHT_F32, T, H, eps, h, y, codes,
+                        scales, scale_stride, rstd, as_stream(stream));
+}
+
+size_t moe_rmsnorm_backward_workspace_bytes(int64_t T, int H) {
+  if (T < 0 || H < 1 || !norm_size_ok(T, H)) return 0;
+  return rmsnorm_backward_workspace_bytes(T, H);
+}
+
+int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,
+                         const void* weight, int64_t T, int H, int flags,
+                         const uint16_t* d_residual, uint16_t* dx, float* d_weight,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || H < 1 || (flags & ~MOE_NORM_WEIGHT_F32)) return MOE_ERR_INVALID_ARG;
+  if (!norm_size_ok(T, H)) return MOE_ERR_UNSUPPORTED;
+  if (!d_weight || !aligned16(d_weight)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !h || !rstd || !weight || !dx || dx == h)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(d_residual) ||
+      !aligned16(dx))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = rmsnorm_backward_workspace_bytes(T, H);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return launch_rmsnorm_backward(dy, h, rstd, weight, flags & MOE_NORM_WEIGHT_F32, T, H, d_residual,
+                                 dx, d_weight, workspace, as_stream(stream));
+}
+
+static constexpr int kLinearMost = 1 << 20;   // N and K
+
+size_t moe_linear_fp8_packed_bytes(int N, int K) {
+  if (N < 1 || K < 1 || K % 128 || N > kLinearMost || K > kLinearMost) return 0;
+  return (size_t)((N + 15) / 16) * 16 * K;
+}
+
+int moe_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float* scales, int N, int K,
+                        int flags, uint8_t* packed, float* packed_scales, void* stream) {
+  if (N < 1 || K < 1 || (flags & ~MOE_LINEAR_TRANSPOSE)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 || N > kLinearMost || K > kLinearMost) return MOE_ERR_UNSUPPORTED;
+  if ((flags & MOE_LINEAR_TRANSPOSE) && N % 128) return MOE_ERR_UNSUPPORTED;
+  if (!w == !codes || !codes != !scales || !packed || !packed_scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(packed)) return MOE_ERR_INVALID_ARG;
+  if (packed == codes || packed_scales == scales) return MOE_ERR_INVALID_ARG;
+  return launch_pack_linear_fp8(w, codes, scales, N, K, flags & MOE_LINEAR_TRANSPOSE, packed,
+                                packed_scales, as_stream(stream));
+}
+
+size_t moe_linear_fp8_workspace_bytes(int64_t M, int N, int K) {
+  if (M < 1 || M > 0x7fffffffLL || N < 1 || K < 1 || K % 128 || N > kLinearMost || K > kLinearMost)
+    return 0;
+  return linear_fp8_workspace_bytes(M, N, K);
+}
+
+int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride, int64_t M, int N,
+                   int K, const uint8_t* packed, const float* packed_scales, int flags, void* y,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 1 || K < 1 || scale_stride < M || (flags & ~MOE_LINEAR_OUT_F32))
+    return MOE_ERR_INVALID_ARG;
+  if (K % 128 || N > kLinearMost || K > kLinearMost || M > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !x_scales || !packed || !packed_scales || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  const size_t need = linear_fp8_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return launch_linear_fp8(x, x_scales, scale_stride, M, N, K, packed, packed_scales, y,
+                           flags & MOE_LINEAR_OUT_F32, workspace, as_stream(stream));
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E) {
+  if (T < 0 || E < 1 || E > 1024) return 0;
+  return balance_loss_workspace_bytes(T, E);
+}
+
+int moe_balance_loss(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx, int T,
+                     int E, int K, float* loss, int32_t* counts, float* probs, int32_t* num_tokens,
+                     void* workspace, size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (T < 0 || E < 1 || K < 1 || K > E) return MOE_ERR_INVALID_ARG;
+  if (K > 32 || E > 1024) return MOE_ERR_UNSUPPORTED;
+  if (!loss || !counts || !probs || !num_tokens) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+  const size_t need = balance_loss_workspace_bytes(T, E);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return launch_balance_loss(logits, row_valid, topk_idx, T, E, K, loss, counts, probs, num_tokens,
+                             workspace, dev_error, as_stream(stream));
+}
+
+int moe_route_backward(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx,
+                       const float* topk_w, const float* d_topk_w, int T, int E, int K, int flags,
+                       const float* d_loss, const int32_t* counts, const int32_t* num_tokens,
+                       float* d_logits, int32_t* dev_error, void* stream) {
+  if (T < 0 || E < 1 || K < 1 || K > E || (flags & ~MOE_ROUTE_RENORM)) return MOE_ERR_INVALID_ARG;
+  if (K > 32 || E > 1024) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!d_logits || (!d_topk_w && !d_loss)) return MOE_ERR_INVALID_ARG;
+  if (d_topk_w && (!topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
+  if (d_loss && (!counts || !num_tokens)) return MOE_ERR_INVALID_ARG;
+  if (!logits && (d_loss || !(flags & MOE_ROUTE_RENORM))) return MOE_ERR_INVALID_ARG;
+  return launch_route_backward(logits, row_valid, topk_idx, topk_w, d_topk_w, T, E, K,
+                               flags & MOE_ROUTE_RENORM, d_loss, counts, num_tokens, d_logits,
+                               dev_error, as_stream(stream));
 }
 
 int moe_copy_bytes(const void* src, void* dst, size_t bytes, void* stream) {

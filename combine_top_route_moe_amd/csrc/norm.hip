@@ -1,0 +1,329 @@
+// Root-mean-square norm of the residual stream with the residual's addition
+// in front and FP8 codes behind, and its gradient.
+//
+// Forward, per row of H channels (float32 between the two roundings):
+//   h = bf16(x + residual)                       (x itself without a residual)
+//   r = 1 / sqrt(sum(h^2) / H + eps),  v = (h r) w
+//   y = bf16(v);  per 128 channels s = amax |v| / 448, code = e4m3(v / s)
+// h is rounded before it is normed because that rounded value is what the
+// stream keeps: the gradient, which starts from the stored h, is then exactly
+// the forward's.  The codes come from v and not from y: one rounding less.
+//
+// Gradient, with hat = h r and g = dy w:
+//   dh = r (g - hat sum(g hat) / H) (+ the stream's own gradient),
+//   dw = sum over the rows of dy hat.
+//
+// Both are bound by memory: every tensor is read or written once, a row stays
+// in registers between the reduction and its use.  One row belongs to kWaves
+// waves (1, 4 or 16 by H, four 16-byte vectors a thread at most), so that the
+// loads of a whole row are in flight at once and no loop runs over it.
+#include "reduce.h"
+
+namespace moe {
+
+constexpr int kNormVecs = 4;            // 16-byte vectors (8 channels) per thread
+
+// A row's sum over its kWaves waves; `buf` is theirs, used by one call at a time.
+template <int kWaves>
+__device__ __forceinline__ float row_sum(float v, float* buf, int wave) {
+  v = wave_sum_f32(v);
+  if (kWaves == 1) return v;
+  if ((threadIdx.x & 63) == 0) buf[wave] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) s += buf[i];
+  return s;
+}
+
+template <bool kF32>
+__device__ __forceinline__ void load_gain(const void* w, int vec, float* out) {
+  if (kF32) {
+    const float4* p = static_cast<const float4*>(w) + 2 * vec;
+    const float4 a = p[0], b = p[1];
+    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+    out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
+  } else {
+    unpack8(static_cast<const uint4*>(w)[vec], out);
+  }
+}
+
+__device__ __forceinline__ uint4 to_bf16x8(const float* v) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * j], v[2 * j + 1]}, b2));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A workgroup of 4 waves (16 for the longest rows) holds 4 / kWaves rows.
+// x, residual and h may be one buffer: a thread stores what it has read.
+template <int kWaves, bool kWF32>
+__global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
+    const uint16_t* x, const uint16_t* residual, const void* __restrict__ weight, int64_t T, int H,
+    float eps, uint16_t* h_out, uint16_t* y, uint8_t* __restrict__ codes,
+    float* __restrict__ scales, int64_t sstride, float* __restrict__ rstd) {
+  constexpr int kRows = kWaves == 1 ? 4 : 1;
+  constexpr int kThreads = kWaves * kWave;
+  __shared__ float part[kWaves];
+  const int wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
+  if (t >= T) return;
+  const int tid = kWaves == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int nvec = H / 8;
+  const uint4* xr = reinterpret_cast<const uint4*>(x) + t * nvec;
+  uint4 hv[kNormVecs];
+#pragma unroll
+  for (int i = 0; i < kNormVecs; ++i) {
+    const int c = tid + i * kThreads;
+    hv[i] = c < nvec ? xr[c] : make_uint4(0, 0, 0, 0);
+  }
+  if (residual) {
+    const uint4* rr = reinterpret_cast<const uint4*>(residual) + t * nvec;
+    uint4 rv[kNormVecs];
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int c = tid + i * kThreads;
+      rv[i] = c < nvec ? rr[c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      float a[8], b[8];
+      unpack8(hv[i], a);
+      unpack8(rv[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+      hv[i] = to_bf16x8(a);
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNormVecs; ++i) {
+    float f[8];
+    unpack8(hv[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
+  }
+  sum = row_sum<kWaves>(sum, part, wave);
+  const float r = 1.0f / sqrtf(sum / (float)H + eps);
+  if (rstd && tid == 0) rstd[t] = r;
+#pragma unroll
+  for (int i = 0; i < kNormVecs; ++i) {
+    const int c = tid + i * kThreads;
+    if (c >= nvec) break;               // (all 16 lanes of a block together: nvec % 16 == 0)
+    if (h_out) reinterpret_cast<uint4*>(h_out)[t * nvec + c] = hv[i];
+    float v[8], w[8];
+    unpack8(hv[i], v);
+    load_gain<kWF32>(weight, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
+    if (y) reinterpret_cast<uint4*>(y)[t * nvec + c] = to_bf16x8(v);
+    if (codes) {
+      // |v| compared as integers: the order of the magnitudes, a NaN above all,
+      // so that a block with a NaN gets a NaN scale instead of losing it
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+      m = row16_max_u32(m);
+      const float s = __uint_as_float(m) / 448.0f;
+      uint2 q = make_uint2(0, 0);
+      if (!(s <= 0.0f)) {
+        // the quotient by the reciprocal: one more rounding (2^-24) before that to
+        // 3 bits; scales whose reciprocal leaves the range divide
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = __builtin_amdgcn_fmed3f(rcp_scale_ok(s) ? v[j] * inv : v[j] / s, -448.0f, 448.0f);
+        q = e4m3x8(v);
+        if (s != s) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+      }
+      reinterpret_cast<uint2*>(codes)[t * nvec + c] = q;
+      if ((c & 15) == 0) scales[(int64_t)(c / 16) * sstride + t] = s;
+    }
+  }
+}
+
+// One workgroup walks the rows blockIdx.x, blockIdx.x + gridDim.x, .. (in
+// groups of kRows) and keeps its share of dw in registers; `partial`
+// [gridDim.x, H] takes the shares, which norm_dw_kernel adds up in order.
+template <int kWaves, bool kWF32>
+__global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_kernel(
+    const uint16_t* dy, const uint16_t* __restrict__ h, const float* __restrict__ rstd,
+    const void* __restrict__ weight, int64_t T, int H, const uint16_t* d_residual, uint16_t* dx,
+    float* __restrict__ partial) {
+  constexpr int kRows = kWaves == 1 ? 4 : 1;
+  constexpr int kThreads = kWaves * kWave;
+  __shared__ float part[2][kWaves];
+  __shared__ float4 join[kWaves == 1 ? 3 : 1][kWaves == 1 ? 2 * kWave : 1];
+  const int wave = threadIdx.x >> 6;
+  const int tid = kWaves == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int nvec = H / 8;
+  float dw[kNormVecs][8];
+#pragma unroll
+  for (int i = 0; i < kNormVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  int flip = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < T; t0 += (int64_t)gridDim.x * kRows) {
+    const int64_t t = t0 + (kWaves == 1 ? wave : 0);
+    if (kWaves == 1 && t >= T) break;
+    const float r = rstd[t];
+    const uint4* dyr = reinterpret_cast<const uint4*>(dy) + t * nvec;
+    const uint4* hr = reinterpret_cast<const uint4*>(h) + t * nvec;
+    const uint4* dr = reinterpret_cast<const uint4*>(d_residual) + t * nvec;
+    uint4 a[kNormVecs], b[kNormVecs], d[kNormVecs];
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int c = tid + i * kThreads;
+      const bool in = c < nvec;
+      a[i] = in ? dyr[c] : make_uint4(0, 0, 0, 0);
+      b[i] = in ? hr[c] : make_uint4(0, 0, 0, 0);
+      d[i] = in && d_residual ? dr[c] : make_uint4(0, 0, 0, 0);
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int c = tid + i * kThreads;
+      if (c >= nvec) break;
+      float g[8], f[8], w[8];
+      unpack8(a[i], g);
+      unpack8(b[i], f);
+      load_gain<kWF32>(weight, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hat = f[j] * r;
+        dw[i][j] = __builtin_fmaf(g[j], hat, dw[i][j]);
+        dot = __builtin_fmaf(g[j] * w[j], hat, dot);
+      }
+    }
+    dot = row_sum<kWaves>(dot, part[flip], wave) / (float)H;
+    flip ^= 1;                          // the next row's sums go to the other buffer: one barrier a row
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int c = tid + i * kThreads;
+      if (c >= nvec) break;
+      float g[8], f[8], w[8], e[8];
+      unpack8(a[i], g);
+      unpack8(b[i], f);
+      unpack8(d[i], e);
+      load_gain<kWF32>(weight, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = r * __builtin_fmaf(-dot, f[j] * r, g[j] * w[j]);
+        g[j] = d_residual ? v + e[j] : v;
+      }
+      reinterpret_cast<uint4*>(dx)[t * nvec + c] = to_bf16x8(g);
+    }
+  }
+  float* out = partial + (int64_t)blockIdx.x * H;
+#pragma unroll
+  for (int i = 0; i < kNormVecs; ++i) {
+    const int c = tid + i * kThreads;
+    float4 lo = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+    float4 hi = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    if (kWaves == 1) {                  // the four rows' waves meet in LDS, in order
+      if (wave > 0) join[wave - 1][tid] = lo, join[wave - 1][kWave + tid] = hi;
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int v = 0; v < 3; ++v) {
+          const float4 p = join[v][tid], q = join[v][kWave + tid];
+          lo.x += p.x, lo.y += p.y, lo.z += p.z, lo.w += p.w;
+          hi.x += q.x, hi.y += q.y, hi.z += q.z, hi.w += q.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (c < nvec && (kWaves != 1 || wave == 0)) {
+      reinterpret_cast<float4*>(out)[2 * c] = lo;
+      reinterpret_cast<float4*>(out)[2 * c + 1] = hi;
+    }
+  }
+}
+
+// dw[c] = sum over the n shares, four channels a thread, 32 threads along the
+// shares (each every 32nd, ascending), their sums added in order.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ partial, int n, int H,
+                                                      float* __restrict__ dw) {
+  __shared__ float4 sums[32][8];
+  const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int c = blockIdx.x * 8 + col;   // of H / 4
+  float4 s = make_float4(0, 0, 0, 0);
+  const float4* p = reinterpret_cast<const float4*>(partial) + c;
+#pragma unroll 4
+  for (int i = slice; i < n; i += 32) {
+    const float4 v = p[(int64_t)i * (H / 4)];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  sums[slice][col] = s;
+  __syncthreads();
+  if (slice) return;
+#pragma unroll
+  for (int i = 1; i < 32; ++i) {
+    const float4 v = sums[i][col];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  reinterpret_cast<float4*>(dw)[c] = s;
+}
+
+static int norm_waves(int H) { return H <= 2048 ? 1 : H <= 8192 ? 4 : 16; }
+
+int launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int wf32,
+                   int64_t T, int H, float eps, uint16_t* h, uint16_t* y, uint8_t* codes,
+                   float* scales, int64_t sstride, float* rstd, hipStream_t stream) {
+  const int waves = norm_waves(H);
+  const int64_t blocks = waves == 1 ? (T + 3) / 4 : T;
+  if (blocks * (waves == 16 ? 1024 : 256) > 0xffffffffLL) return MOE_ERR_UNSUPPORTED;
+#define MOE_NORM(W, F)                                                                          \
+  hipLaunchKernelGGL((rmsnorm_kernel<W, F>), dim3((unsigned)blocks), dim3(W == 16 ? 1024 : 256), 0, \
+                     stream, x, residual, weight, T, H, eps, h, y, codes, scales, sstride, rstd)
+  if (waves == 1) {
+    if (wf32) MOE_NORM(1, true); else MOE_NORM(1, false);
+  } else if (waves == 4) {
+    if (wf32) MOE_NORM(4, true); else MOE_NORM(4, false);
+  } else {
+    if (wf32) MOE_NORM(16, true); else MOE_NORM(16, false);
+  }
+#undef MOE_NORM
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// Workgroups of the gradient: each leaves H floats of dw behind, so no more
+// than fill the GPU.
+static int64_t norm_shares(int64_t T, int H) {
+  const int waves = norm_waves(H);
+  const int64_t rows = waves == 1 ? (T + 3) / 4 : T;
+  const int64_t most = waves == 16 ? 256 : 1024;
+  return rows < most ? rows : most;
+}
+
+size_t rmsnorm_backward_workspace_bytes(int64_t T, int H) {
+  return (size_t)norm_shares(T, H) * H * sizeof(float);
+}
+
+int launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,
+                            const void* weight, int wf32, int64_t T, int H,
+                            const uint16_t* d_residual, uint16_t* dx, float* dw, void* workspace,
+                            hipStream_t stream) {
+  const int waves = norm_waves(H);
+  const int blocks = (int)norm_shares(T, H);
+  float* partial = static_cast<float*>(workspace);
+#define MOE_NORM(W, F)                                                                            \
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<W, F>), dim3(blocks), dim3(W == 16 ? 1024 : 256), 0, \
+                     stream, dy, h, rstd, weight, T, H, d_residual, dx, partial)
+  if (blocks == 0) {
+  } else if (waves == 1) {
+    if (wf32) MOE_NORM(1, true); else MOE_NORM(1, false);
+  } else if (waves == 4) {
+    if (wf32) MOE_NORM(4, true); else MOE_NORM(4, false);
+  } else {
+    if (wf32) MOE_NORM(16, true); else MOE_NORM(16, false);
+  }
+#undef MOE_NORM
+  hipLaunchKernelGGL(norm_dw_kernel, dim3(H / 32), dim3(256), 0, stream, partial, blocks, H, dw);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // namespace moe

@@ -26,6 +26,8 @@ MOE_ERR_SCRATCH = -6
 MOE_FP8_LAYOUT_K128 = 1
 MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4, MOE_W_NVFP4 = 0, 1, 2, 3
 MOE_DECODE_MAX_TOKENS = 64
+MOE_NORM_WEIGHT_F32 = 1
+MOE_LINEAR_TRANSPOSE, MOE_LINEAR_OUT_F32 = 1, 2
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -775,6 +777,322 @@ def moe_combine_check(rows: torch.Tensor, row_of: torch.Tensor, T: int, K: int,
     check("moe_combine_check", load().moe_combine_check(
         _ptr(rows), num_rows, _ptr(row_of), _ptr(shared), T, K, H, _ptr(kernel_out), _ptr(state),
         _ptr(dev_error), _stream(stream)))
+
+
+def _output(want, shape, dtype: torch.dtype, device, stream, name: str):
+    """An output that the caller asks for by True, declines by False or None, or
+    passes as a buffer of that shape."""
+    if want is None or want is False:
+        return None
+    if want is True:
+        return _empty(shape, dtype, device, stream)
+    if tuple(want.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(want.shape)}")
+    return want
+
+
+def _gain(weight: torch.Tensor, H: int):
+    """(flags, dtype) of a norm's weight [H]."""
+    if tuple(weight.shape) != (H,):
+        raise ValueError(f"weight: expected shape ({H},), got {tuple(weight.shape)}")
+    if weight.dtype == torch.float32:
+        return MOE_NORM_WEIGHT_F32, torch.float32
+    return 0, torch.bfloat16
+
+
+@dataclass
+class Normed:
+    """What ``moe_rmsnorm`` writes (None where it was not asked for)."""
+
+    h: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                residual: Optional[torch.Tensor] = None, h=None, y=True, codes=False, scales=None,
+                rstd=False, stream=None) -> Normed:
+    """Add ``residual`` to the rows x [T, H] (``h``, by default a new tensor
+    where there is a residual and not written where there is none), norm them:
+    ``y`` in bf16, ``codes`` E4M3 uint8 [T, H] with ``scales`` [H/128, stride]
+    as ``moe_quant_rows_fp8`` writes them, ``rstd`` [T].  Each output is True, False or a
+    buffer (``h`` may be x or residual, ``y`` may be x)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("residual does not match x")
+    flags, wtype = _gain(weight, H)
+    raw = _one_device(stream, x, weight, residual)
+    dev = x.device
+    h = _output(residual is not None if h is None else h, (T, H), torch.bfloat16, dev, stream, "h")
+    y = _output(y, (T, H), torch.bfloat16, dev, stream, "y")
+    codes = _output(codes, (T, H), torch.uint8, dev, stream, "codes")
+    rstd = _output(rstd, (T,), torch.float32, dev, stream, "rstd")
+    if codes is None:
+        if scales is not None:
+            raise ValueError("scales without codes")
+    elif scales is None:
+        scales = _empty((H // 128, max(T, 1)), torch.float32, dev, stream)
+    elif scales.dim() != 2 or scales.shape[0] != H // 128 or scales.shape[1] < T:
+        raise ValueError("scales must be [H/128, >= T]")
+    px, pw, pr, ph, py, pc, ps, pi = _pointers(
+        x.get_device(), (x, torch.bfloat16, "x"), (weight, wtype, "weight"),
+        (residual, torch.bfloat16, "residual"), (h, torch.bfloat16, "h"), (y, torch.bfloat16, "y"),
+        (codes, torch.uint8, "codes"), (scales, torch.float32, "scales"),
+        (rstd, torch.float32, "rstd"))
+    check("moe_rmsnorm", load().moe_rmsnorm(
+        px, pr, pw, T, H, eps, flags, ph, py, pc, ps, 0 if scales is None else scales.shape[1], pi,
+        raw))
+    return Normed(h, y, codes, scales, rstd)
+
+
+def moe_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
+    return load().moe_rmsnorm_backward_workspace_bytes(T, H)
+
+
+def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
+                         weight: torch.Tensor, d_residual: Optional[torch.Tensor] = None,
+                         dx: Optional[torch.Tensor] = None,
+                         d_weight: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """``(dx, d_weight)``: the gradient of x (and of the residual alike) and of
+    the weight, from the ``h`` (x itself where there was no residual) and
+    ``rstd`` of ``moe_rmsnorm``; ``d_residual`` is the stream's own gradient
+    with respect to h.  ``dx`` may be dy's or d_residual's buffer."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, H]")
+    T, H = dy.shape
+    if h.shape != dy.shape or (d_residual is not None and d_residual.shape != dy.shape):
+        raise ValueError("h or d_residual does not match dy")
+    if tuple(rstd.shape) != (T,):
+        raise ValueError("rstd must be [T]")
+    flags, wtype = _gain(weight, H)
+    raw = _one_device(stream, dy, h, weight)
+    lib = load()
+    dx = _output(True if dx is None else dx, (T, H), torch.bfloat16, dy.device, stream, "dx")
+    d_weight = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy.device, stream,
+                       "d_weight")
+    if workspace is None:
+        need = lib.moe_rmsnorm_backward_workspace_bytes(T, H)
+        workspace = _empty(max(need, 1), torch.uint8, dy.device, stream)
+    pdy, ph, pi, pw, pd, px, pdw, pws = _pointers(
+        dy.get_device(), (dy, torch.bfloat16, "dy"), (h, torch.bfloat16, "h"),
+        (rstd, torch.float32, "rstd"), (weight, wtype, "weight"),
+        (d_residual, torch.bfloat16, "d_residual"), (dx, torch.bfloat16, "dx"),
+        (d_weight, torch.float32, "d_weight"), (workspace, torch.uint8, "workspace"))
+    check("moe_rmsnorm_backward", lib.moe_rmsnorm_backward(
+        pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, workspace.numel(), raw))
+    return dx, d_weight
+
+
+@dataclass(frozen=True, eq=False)
+class LinearWeights:
+    """Packed weights of ``moe_linear_fp8``: those of a matrix [N, K].  Built by
+    ``linear_weights`` or ``linear_weights_from_codes``."""
+
+    N: int
+    K: int
+    packed: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        _want(self.packed, torch.uint8, "packed")
+        _want(self.scales, torch.float32, "scales")
+        if self.packed.numel() != moe_linear_fp8_packed_bytes(self.N, self.K):
+            raise ValueError("packed: not the size of a matrix [N, K] in the packed order")
+        if tuple(self.scales.shape) != (-(-self.N // 128), self.K // 128):
+            raise ValueError("scales must be [ceil(N/128), K/128]")
+        if self.scales.device != self.packed.device:
+            raise ValueError("scales: not on the device of packed")
+        _ptr(self.packed), _ptr(self.scales)
+
+
+def moe_linear_fp8_packed_bytes(N: int, K: int) -> int:
+    return load().moe_linear_fp8_packed_bytes(N, K)
+
+
+def moe_pack_linear_fp8(w: Optional[torch.Tensor], codes: Optional[torch.Tensor] = None,
+                        scales: Optional[torch.Tensor] = None, transpose: bool = False,
+                        stream=None) -> LinearWeights:
+    """Lay out W [N, K] for ``moe_linear_fp8``: bf16 ``w``, quantized per
+    128 x 128 tile, or ``codes`` uint8 with ``scales`` [ceil(N/128), K/128]."""
+    src = codes if w is None else w
+    if src is None or (w is not None and (codes is not None or scales is not None)):
+        raise ValueError("either w, or codes and scales")
+    if src.dim() != 2:
+        raise ValueError("weights must be [N, K]")
+    N, K = src.shape
+    if w is None and (scales is None or tuple(scales.shape) != (-(-N // 128), K // 128)):
+        raise ValueError("scales must be [ceil(N/128), K/128]")
+    if transpose and N % 128:
+        raise ValueError("transposed weights need N % 128 == 0")
+    raw = _one_device(stream, src, scales)
+    rows, cols = (K, N) if transpose else (N, K)
+    packed = _empty(max(moe_linear_fp8_packed_bytes(rows, cols), 1), torch.uint8, src.device, stream)
+    packed_scales = _empty((-(-rows // 128), cols // 128), torch.float32, src.device, stream)
+    pw, pc, ps = _pointers(src.get_device(), (w, torch.bfloat16, "w"), (codes, torch.uint8, "codes"),
+                           (scales, torch.float32, "scales"))
+    check("moe_pack_linear_fp8", load().moe_pack_linear_fp8(
+        pw, pc, ps, N, K, MOE_LINEAR_TRANSPOSE if transpose else 0, _ptr(packed),
+        _ptr(packed_scales), raw))
+    return LinearWeights(rows, cols, packed, packed_scales)
+
+
+def linear_weights(w: torch.Tensor, transpose: bool = False, stream=None) -> LinearWeights:
+    """Quantize and pack bf16 W [N, K] once; with ``transpose`` W^T (the weights
+    of the gradient with respect to the rows, N % 128 == 0)."""
+    return moe_pack_linear_fp8(w, transpose=transpose, stream=stream)
+
+
+def linear_weights_from_codes(codes: torch.Tensor, scales: torch.Tensor, transpose: bool = False,
+                              stream=None) -> LinearWeights:
+    """A checkpoint's E4M3 codes [N, K] (uint8 or float8_e4m3fn) and tile scales
+    [ceil(N/128), K/128] float32 in the packed order, unchanged."""
+    if codes.dtype == torch.float8_e4m3fn:
+        codes = codes.view(torch.uint8)
+    return moe_pack_linear_fp8(None, codes, scales, transpose, stream)
+
+
+def moe_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return load().moe_linear_fp8_workspace_bytes(M, N, K)
+
+
+def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeights,
+                   y: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x W^T on E4M3 codes x [M, K] (uint8 or float8_e4m3fn) and
+    their scales [K/128, >= M], as ``moe_quant_rows_fp8`` and ``moe_rmsnorm``
+    write them.  ``y`` is bf16 or float32 (``out_dtype``, by default bf16)."""
+    if x.dtype == torch.float8_e4m3fn:
+        x = x.view(torch.uint8)
+    if x.dim() != 2 or x.shape[1] != weights.K:
+        raise ValueError(f"x must be [M, {weights.K}]")
+    M, N, K = x.shape[0], weights.N, weights.K
+    if x_scales.dim() != 2 or x_scales.shape[0] != K // 128 or x_scales.shape[1] < M:
+        raise ValueError("x_scales must be [K/128, >= M]")
+    if y is None:
+        out_dtype = out_dtype or torch.bfloat16
+    elif out_dtype not in (None, y.dtype):
+        raise TypeError(f"y: expected {out_dtype}, got {y.dtype}")
+    else:
+        out_dtype = y.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"y is bfloat16 or float32, not {out_dtype}")
+    raw = _one_device(stream, x, x_scales, weights.packed)
+    lib = load()
+    y = _output(True if y is None else y, (M, N), out_dtype, x.device, stream, "y")
+    if workspace is None:
+        need = lib.moe_linear_fp8_workspace_bytes(M, N, K)
+        workspace = _empty(max(need, 1), torch.uint8, x.device, stream)
+    px, ps, py, pws = _pointers(
+        x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"),
+        (y, out_dtype, "y"), (workspace, torch.uint8, "workspace"))
+    check("moe_linear_fp8", lib.moe_linear_fp8(
+        px, ps, x_scales.shape[1], M, N, K, weights.packed.data_ptr(), weights.scales.data_ptr(),
+        MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, workspace.numel(), raw))
+    return y
+
+
+@dataclass
+class RouterLosses:
+    """``loss`` [2]: balance and z; ``counts`` [E], ``probs`` [E], ``num_tokens`` [1]."""
+
+    loss: torch.Tensor
+    counts: torch.Tensor
+    probs: torch.Tensor
+    num_tokens: torch.Tensor
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
+    return load().moe_balance_loss_workspace_bytes(T, E)
+
+
+def _router_shapes(logits_shape, topk_idx, row_valid, *slots):
+    T, E = logits_shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, K]")
+    for t in slots:
+        if t is not None and t.shape != topk_idx.shape:
+            raise ValueError("topk_idx, topk_w and d_topk_w must have one shape")
+    if row_valid is not None and tuple(row_valid.shape) != (T,):
+        raise ValueError("row_valid must be [T]")
+    return T, E, topk_idx.shape[1]
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
+                     row_valid: Optional[torch.Tensor] = None,
+                     out: Optional[RouterLosses] = None, workspace: Optional[torch.Tensor] = None,
+                     dev_error: Optional[torch.Tensor] = None, stream=None) -> RouterLosses:
+    """The balance and z losses of a batch's routing, with the experts' counts
+    and mean probabilities; ``row_valid`` as ``moe_route`` got it."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E, K = _router_shapes(logits.shape, topk_idx, row_valid)
+    raw = _one_device(stream, logits, topk_idx, row_valid)
+    lib, dev = load(), logits.device
+    want = (True,) * 4 if out is None else (out.loss, out.counts, out.probs, out.num_tokens)
+    f32, i32 = torch.float32, torch.int32
+    out = RouterLosses(_output(want[0], (2,), f32, dev, stream, "loss"),
+                       _output(want[1], (E,), i32, dev, stream, "counts"),
+                       _output(want[2], (E,), f32, dev, stream, "probs"),
+                       _output(want[3], (1,), i32, dev, stream, "num_tokens"))
+    if workspace is None:
+        workspace = _empty(max(lib.moe_balance_loss_workspace_bytes(T, E), 1), torch.uint8, dev, stream)
+    pl, pv, pi, po, pc, pp, pn, pws, perr = _pointers(
+        logits.get_device(), (logits, f32, "logits"), (row_valid, torch.uint8, "row_valid"),
+        (topk_idx, i32, "topk_idx"), (out.loss, f32, "loss"), (out.counts, i32, "counts"),
+        (out.probs, f32, "probs"), (out.num_tokens, i32, "num_tokens"),
+        (workspace, torch.uint8, "workspace"), (dev_error, i32, "dev_error"))
+    check("moe_balance_loss", lib.moe_balance_loss(pl, pv, pi, T, E, K, po, pc, pp, pn, pws,
+                                                   workspace.numel(), perr, raw))
+    return out
+
+
+def moe_route_backward(logits: Optional[torch.Tensor], topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                       d_topk_w: Optional[torch.Tensor],
+                       row_valid: Optional[torch.Tensor] = None, renormalize: bool = True,
+                       d_loss: Optional[torch.Tensor] = None,
+                       counts: Optional[torch.Tensor] = None,
+                       num_tokens: Optional[torch.Tensor] = None,
+                       d_logits: Optional[torch.Tensor] = None,
+                       num_experts: Optional[int] = None,
+                       dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient with respect to the logits [T, E] of ``moe_route``'s weights
+    (``d_topk_w``, or None) and of ``moe_balance_loss``'s losses (``d_loss`` [2]
+    with its ``counts`` and ``num_tokens``, or None).  ``logits`` may be None
+    where neither needs a softmax over all experts (no d_loss, renormalized
+    weights); ``num_experts`` is E then."""
+    if logits is not None:
+        if logits.dim() != 2 or num_experts not in (None, logits.shape[1]):
+            raise ValueError("logits must be [T, num_experts]")
+        shape = logits.shape
+    elif d_logits is not None:
+        shape = d_logits.shape
+    elif num_experts is not None:
+        shape = (topk_idx.shape[0], num_experts)
+    else:
+        raise ValueError("without logits, num_experts is needed")
+    T, E, K = _router_shapes(shape, topk_idx, row_valid, topk_w, d_topk_w)
+    if d_loss is not None:
+        if counts is None or num_tokens is None:
+            raise ValueError("d_loss needs counts and num_tokens")
+        if d_loss.numel() != 2 or counts.numel() != E or num_tokens.numel() != 1:
+            raise ValueError("d_loss must be [2], counts [E] and num_tokens [1]")
+    raw = _one_device(stream, topk_idx, logits, topk_w)
+    d_logits = _output(True if d_logits is None else d_logits, (T, E), torch.float32, topk_idx.device,
+                       stream, "d_logits")
+    f32, i32 = torch.float32, torch.int32
+    pl, pv, pi, pw, pd, po, pc, pn, pg, perr = _pointers(
+        topk_idx.get_device(), (logits, f32, "logits"), (row_valid, torch.uint8, "row_valid"),
+        (topk_idx, i32, "topk_idx"), (topk_w, f32, "topk_w"), (d_topk_w, f32, "d_topk_w"),
+        (d_loss, f32, "d_loss"), (counts, i32, "counts"), (num_tokens, i32, "num_tokens"),
+        (d_logits, f32, "d_logits"), (dev_error, i32, "dev_error"))
+    check("moe_route_backward", load().moe_route_backward(
+        pl, pv, pi, pw, pd, T, E, K, MOE_ROUTE_RENORM if renormalize else 0, po, pc, pn, pg, perr, raw))
+    return d_logits
 
 
 def moe_read_bytes(src: torch.Tensor, sink: torch.Tensor, stream=None) -> None:

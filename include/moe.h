@@ -86,6 +86,10 @@ enum { MOE_W_BF16 = 0,                /* expert-weight formats: bf16, packed  */
        MOE_W_MXFP4 = 2,               /* E2M1 codes, E8M0 scales of 32        */
        MOE_W_NVFP4 = 3 };             /* E2M1 codes, E4M3 scales of 16        */
 
+enum { MOE_NORM_WEIGHT_F32 = 1 };     /* moe_rmsnorm: a float32 gain, not bf16 */
+enum { MOE_LINEAR_TRANSPOSE = 1,      /* moe_pack_linear_fp8: pack W^T        */
+       MOE_LINEAR_OUT_F32 = 2 };      /* moe_linear_fp8: y in float32         */
+
 /* The packed weights of G experts (device pointers) in one of the formats
  * above; the struct itself is host memory, read during the call only.
  *   MOE_W_BF16   w13, w2 from moe_pack_ffn_weights; no scales
@@ -573,6 +577,125 @@ int moe_combine(const uint16_t* rows, int64_t num_rows, const int32_t* row_of,
 int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row_of,
                       const uint16_t* shared, int T, int K, int H, const uint16_t* kernel_out,
                       int32_t* state, int32_t* dev_error, void* stream);
+
+/* ---- norm of the residual stream, with codes ------------------------------
+ * In front of the layer, per row t of H channels (float32 between roundings):
+ *   h = bf16(x + residual), x itself without a residual
+ *   r = 1 / sqrt(sum(h^2) / H + eps),   v = (h r) weight
+ *   y = bf16(v)                                                  (the router's rows)
+ *   s = fl32(amax |v| / 448) per 128 channels, codes = e4m3(v / s)  (the experts')
+ * h is rounded before it is normed: it is what the stream keeps and what the
+ * gradient starts from.  The codes are those of v, not of the rounded y; the
+ * quotient is taken through float32, to nearest even, saturating at 448.
+ *   x [T, H] bf16;  residual [T, H] bf16 or NULL;  weight [H] bf16, or float32
+ *   with MOE_NORM_WEIGHT_F32;  outputs, each may be NULL but not all: h [T, H]
+ *   bf16;  y [T, H] bf16;  codes [T, H] uint8 with scales [H/128, scale_stride]
+ *   float32 (K-block-major, as moe_quant_rows_fp8 writes them; scale_stride >=
+ *   T; columns past T are left as they are);  rstd [T] float32, r.
+ * h may be x's or residual's buffer and y may be x's.  An all-zero block gets
+ * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) must be within
+ * float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd, scales: 4).
+ * Requires H % 128 == 0, H <= 32768, eps > 0 and finite; sizes that need more
+ * than 2^32 threads are refused (T <= 2^26 at H <= 2048, 2^24 to 8192, else 2^22). */
+int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,
+                float eps, int flags, uint16_t* h, uint16_t* y, uint8_t* codes, float* scales,
+                int64_t scale_stride, float* rstd, void* stream);
+
+/* The gradient of moe_rmsnorm's y (its rounding, and that of codes, counting as
+ * the identity), from the h and rstd that it wrote: with hat = h r, g = dy weight,
+ *   dx = bf16( r (g - hat sum(g hat) / H) + d_residual )
+ *   d_weight = sum_t dy hat                       (float32, a fixed order)
+ * dx is the gradient of x and of the residual alike; d_residual [T, H] bf16 (NULL:
+ * none) that of the h that went on down the stream.
+ *   dy, h [T, H] bf16;  rstd [T] float32;  weight as above;  dx [T, H] bf16,
+ *   which may be dy's or d_residual's buffer;  d_weight [H] float32 (written, not
+ *   added to).  T = 0 writes zeros to d_weight.  Requires as moe_rmsnorm. */
+size_t moe_rmsnorm_backward_workspace_bytes(int64_t T, int H);
+int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,
+                         const void* weight, int64_t T, int H, int flags,
+                         const uint16_t* d_residual, uint16_t* dx, float* d_weight,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the dense product on FP8 codes ----------------------------------------
+ * y = x W^T for rows and weights in 8 bits, the formats of the FP8 path above:
+ *   y[m, n] = sum_b sx[b, m] sw[n / 128, b] sum_{k in block b} qx[m, k] qw[n, k]
+ * over the 128-wide blocks b of K, every block's products summed by the matrix
+ * cores and scaled into a float32 sum, rounded once.  (The cores add each 8
+ * neighbouring products with their low bits cut off 2^-13 below the largest of
+ * them, these sums in float32: about 2^-15 of the sum of magnitudes, in a float32
+ * y too.)  From a single row to prompts.  N may end inside a tile.
+ *
+ * moe_pack_linear_fp8 lays W [N, K] out once: from bf16 (`w`, quantized per 128 x
+ * 128 tile as moe_pack_ffn_weights_fp8 does; a tile at the edge from the rows it
+ * has), or from codes [N, K] and scales [ceil(N/128), K/128] that exist already
+ * (a checkpoint), unchanged; the other pointers are NULL.
+ *   packed: moe_linear_fp8_packed_bytes(N, K) bytes; the 16 x 128 tile of rows
+ *     16 i .. and block b at unit (i * (K/128) + b) * 128 of 16 bytes, in it
+ *     unit 64 h + l the codes of row l % 16, columns 64 h + 16 (l / 16) .. +16;
+ *     rows past N are zero
+ *   packed_scales [ceil(N/128), K/128] float32
+ * With MOE_LINEAR_TRANSPOSE it packs W^T, the weights of the gradient with respect
+ * to x (dx = dy W): packed and packed_scales are then those of a [K, N] matrix,
+ * and N % 128 == 0 is required.  The codes are the same: a tile's scale does not
+ * depend on the direction.  Pointers 16-byte aligned (scales: 4); outputs must
+ * not alias inputs.  Requires K % 128 == 0, N and K <= 2^20.
+ *
+ *   x [M, K] uint8 and x_scales [K/128, scale_stride] float32 (scale_stride >= M)
+ *   from moe_quant_rows_fp8 or moe_rmsnorm;  y [M, N] bf16, or float32 with
+ *   MOE_LINEAR_OUT_F32;  the workspace may be NULL where the query says 0.
+ * A row's result depends on that row alone (a NaN stays in its row); equal calls
+ * give equal bits, but a row's bits may differ with M.  M = 0 enqueues nothing.
+ * Requires M < 2^31, K % 128 == 0, N and K <= 2^20; sizes that need more than 2^32
+ * threads are refused.  Pointers 16-byte aligned (x_scales, packed_scales: 4). */
+size_t moe_linear_fp8_packed_bytes(int N, int K);
+int moe_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float* scales, int N, int K,
+                        int flags, uint8_t* packed, float* packed_scales, void* stream);
+size_t moe_linear_fp8_workspace_bytes(int64_t M, int N, int K);
+int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride, int64_t M, int N,
+                   int K, const uint8_t* packed, const float* packed_scales, int flags, void* y,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the router's losses and its gradient ----------------------------------
+ * Over the n tokens with row_valid[t] != 0 (all where it is NULL), with p_t the
+ * softmax of a token's E logits and lse_t its logsumexp:
+ *   counts[e] = slots with topk_idx == e,  probs[e] = sum_t p_te / n
+ *   loss[0] = E sum_e counts[e] / (n K) probs[e]      (balance; 1 when even)
+ *   loss[1] = sum_t lse_t^2 / n                       (z)
+ *   num_tokens[0] = n
+ * n = 0 gives zeros.  A negative id is an empty slot; one >= E is not counted and
+ * raises MOE_DEVERR_EXPERT_RANGE.  Non-finite logits as in moe_route: a NaN
+ * counts as -inf, equal largest ones as equals; a token whose largest logit is
+ * not finite adds nothing to loss[1].
+ *   logits [T, E] float32;  row_valid [T] uint8 or NULL;  topk_idx [T, K] int32;
+ *   outputs loss [2] float32, counts [E] int32, probs [E] float32, num_tokens [1]
+ *   int32.  Sums have a fixed order (equal calls, equal bits).  T = 0 writes zeros.
+ * Requires 1 <= K <= min(E, 32), E <= 1024. */
+size_t moe_balance_loss_workspace_bytes(int T, int E);
+int moe_balance_loss(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx, int T,
+                     int E, int K, float* loss, int32_t* counts, float* probs, int32_t* num_tokens,
+                     void* workspace, size_t workspace_bytes, int32_t* dev_error, void* stream);
+
+/* The gradient with respect to the logits of moe_route's weights and of both
+ * losses (the choice of experts and the counts are constants):
+ *   d_logits[t, e] = sum_{k: topk_idx[t,k] = e} w_k dw_k - c_e sum_k w_k dw_k
+ *     + d_loss[0] / n * p_te (E f_e - sum_j p_tj E f_j),   f_e = counts[e] / (n K)
+ *     + d_loss[1] / n * 2 lse_t p_te
+ * w = topk_w, dw = d_topk_w; c_e is the sum of the w_k of e's slots with
+ * MOE_ROUTE_RENORM, p_te (for every e) without.  counts and num_tokens are inputs
+ * (moe_balance_loss's, or their sums over all ranks).
+ *   d_topk_w [T, K] float32 or NULL (then topk_idx and topk_w are not read);
+ *   d_loss [2] float32 or NULL (then counts and num_tokens are not read); one of
+ *   the two is needed.  logits may be NULL where no softmax over all experts is
+ *   needed (d_loss NULL, MOE_ROUTE_RENORM).  d_logits [T, E] float32 (out).
+ * Tokens with row_valid[t] == 0 get zeros.  An empty slot (id < 0) has no part,
+ * whatever its weights hold; an id >= E neither, and raises
+ * MOE_DEVERR_EXPERT_RANGE; an expert in two slots gets both parts.  A token whose
+ * largest logit is not finite gets no gradient from the losses.  T = 0 enqueues
+ * nothing.  Requires as moe_balance_loss. */
+int moe_route_backward(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx,
+                       const float* topk_w, const float* d_topk_w, int T, int E, int K, int flags,
+                       const float* d_loss, const int32_t* counts, const int32_t* num_tokens,
+                       float* d_logits, int32_t* dev_error, void* stream);
 
 /* ---- streaming copy -----------------------------------------------------
  * dst[0:bytes) = src[0:bytes) with 16-byte vector loads and stores: the
