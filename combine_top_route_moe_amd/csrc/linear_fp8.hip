@@ -13,6 +13,9 @@
 // after another (a wave's stream through K is contiguous); in a tile, half h =
 // 0, 1 and lane l = 0..63 the 16 codes of row l % 16, columns 64 h + 16 (l /
 // 16) .. +16: both halves are one operand, whichever way it is fetched.
+#include <algorithm>
+#include <cmath>
+
 #include "gemm_common.h"
 #include "reduce.h"
 
@@ -26,7 +29,11 @@ __device__ __forceinline__ i32x8_t operand(const u32x4_t& lo, const u32x4_t& hi)
 
 __device__ __forceinline__ f32x4_t mfma_codes(const i32x8_t& a, const i32x8_t& b) {
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 127, 0, 127);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
 }
 
 // Four outputs side by side of one row; `some` of them lie in the matrix.
@@ -43,9 +50,7 @@ __device__ __forceinline__ void store4(void* y, int64_t at, const f32x4_t& v, in
   } else {
     uint16_t* p = static_cast<uint16_t*>(y) + at;
     if (wide) {
-      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{
-          __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
-          __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t))};
+      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
     } else {
       for (int q = 0; q < 4; ++q)
         if (q < some) p[q] = (uint16_t)f32_to_bf16(v[q]);
@@ -53,75 +58,381 @@ __device__ __forceinline__ void store4(void* y, int64_t at, const f32x4_t& v, in
   }
 }
 
+// A wave's outputs: rows m0 + 16 j + lane % 16 of y, columns n0 + 16 i + 4 (lane / 16)
+// .. +4.  In bf16 two neighbouring i's trade places between lanes 16 apart, so that
+// each lane stores 16 bytes and 64 of a row lie together.
+template <bool F32, int kIN, int kIM>
+__device__ __forceinline__ void store_tile(void* y, const f32x4_t (&acc)[kIN][kIM], int64_t m0, int n0, int64_t M,
+                                           int N, int lane) {
+  const int g = lane >> 4;
+  if (!F32 && kIN % 2 == 0 && (N & 7) == 0) {
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) {
+      const int64_t m = m0 + 16 * j + (lane & 15);
+#pragma unroll
+      for (int i = 0; i < kIN; i += 2) {
+        const f32x4_t &p = acc[i][j], &q = acc[i + 1][j];
+        const auto lo = __builtin_amdgcn_permlane16_swap(bf16_pair(p[0], p[1]), bf16_pair(q[0], q[1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(bf16_pair(p[2], p[3]), bf16_pair(q[2], q[3]), false, false);
+        const int n = n0 + 16 * (i + (g & 1)) + 8 * (g >> 1);
+        if (m < M && n < N)
+          *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(y) + m * N + n) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kIM; ++j) {
+    const int64_t m = m0 + 16 * j + (lane & 15);
+    if (m >= M) continue;
+#pragma unroll
+    for (int i = 0; i < kIN; ++i) {
+      const int n = n0 + 16 * i + 4 * g;
+      if (n < N) store4<F32>(y, m * N + n, acc[i][j], N - n, (N & 3) == 0);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Few rows: a workgroup owns 16 rows of W and 16 MT rows of x; its waves take
-// the blocks of K in turn and add up through LDS, in order.  Bound by the
-// weights' bytes, which are read once, straight into the operand's registers.
-template <int MT, int NW, int PF, bool F32>
-__global__ void __launch_bounds__(NW * kWave) linear_rows_kernel(
-    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t sstride, int64_t M,
+// Up to 16 rows: a workgroup owns 16 rows of W; its waves take the blocks of K in
+// turn, kAhead of a wave's at a time on their way from memory straight into the
+// operands' registers (W's past the caches' order: each is read once), and add up
+// through LDS, in order.  Bound by W's bytes, and where these are few by one
+// load's way through the memory.
+template <int kNW, int kAhead, bool F32>
+__global__ void __launch_bounds__(kNW * kWave) linear_rows_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t sstride, int M,
     const uint8_t* __restrict__ wq, const float* __restrict__ wsc, int N, int nkb, void* __restrict__ y) {
-  __shared__ f32x4_t red[NW][MT][kWave];
+  __shared__ f32x4_t sums[kNW][kWave];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ct = blockIdx.x;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int64_t K = (int64_t)nkb * 128;
-  const uint8_t* xr[MT];
-  const float* sr[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t m = min(m0 + 16 * j + (lane & 15), M - 1);   // rows past the end re-read the last
-    xr[j] = x + m * K + 16 * (lane >> 4);
-    sr[j] = xs + m;
-  }
-  const u32x4_t* wp = reinterpret_cast<const u32x4_t*>(wq) + (int64_t)ct * nkb * 128 + lane;
+  const int m = min(lane & 15, M - 1);           // rows past the end re-read the last
+  const uint8_t* xr = x + (int64_t)m * nkb * 128 + 16 * (lane >> 4);
+  const u32x4_t* wr = reinterpret_cast<const u32x4_t*>(wq) + (int64_t)ct * nkb * 128 + lane;
   const float* sw = wsc + (int64_t)(ct / 8) * nkb;
 
-  u32x4_t wlo[PF], whi[PF];
+  u32x4_t wv[kAhead][2], xv[kAhead][2];
+  float sx[kAhead], s[kAhead];
   auto fill = [&](int slot, int b) {
-    const u32x4_t* p = wp + (int64_t)min(b, nkb - 1) * 128;
-    wlo[slot] = __builtin_nontemporal_load(p);
-    whi[slot] = __builtin_nontemporal_load(p + kWave);
+    if (b >= nkb) return;
+    const u32x4_t* p = wr + (int64_t)b * 128;
+    const u32x4_t* q = reinterpret_cast<const u32x4_t*>(xr + (int64_t)b * 128);
+    wv[slot][0] = __builtin_nontemporal_load(p);
+    wv[slot][1] = __builtin_nontemporal_load(p + kWave);
+    xv[slot][0] = q[0];
+    xv[slot][1] = q[4];
+    sx[slot] = xs[b * sstride + m];
+    s[slot] = sw[b];
   };
-  f32x4_t acc[MT];
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < MT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int u = 0; u < kAhead; ++u) fill(u, w + kNW * u);
+  for (int b0 = w; b0 < nkb; b0 += kNW * kAhead) {
 #pragma unroll
-  for (int s = 0; s < PF; ++s) fill(s, w + NW * s);
-  for (int b0 = w; b0 < nkb; b0 += NW * PF) {
+    for (int u = 0; u < kAhead; ++u) {
+      const int b = b0 + kNW * u;
+      if (b >= nkb) break;
+      const f32x4_t t = mfma_codes(operand(wv[u][0], wv[u][1]), operand(xv[u][0], xv[u][1]));
+      const float c = sx[u] * s[u];
+      fill(u, b + kNW * kAhead);
 #pragma unroll
-    for (int s = 0; s < PF; ++s) {
-      const int b = b0 + NW * s;
-      if (b < nkb) {
-        const float scale = sw[b];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const u32x4_t* p = reinterpret_cast<const u32x4_t*>(xr[j] + (int64_t)b * 128);
-          const f32x4_t t = mfma_codes(operand(wlo[s], whi[s]), operand(p[0], p[4]));
-          const float c = sr[j][b * sstride] * scale;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[j][q] = __builtin_fmaf(t[q], c, acc[j][q]);
-        }
-      }
-      fill(s, b + NW * PF);
+      for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], c, acc[q]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) red[w][j][lane] = acc[j];
+  sums[w][lane] = acc;
   __syncthreads();
   const int n = ct * 16 + 4 * (lane >> 4);
-  for (int j = w; j < MT; j += NW) {
-    f32x4_t v = red[0][j][lane];
+  if (w > 0 || (lane & 15) >= M || n >= N) return;
 #pragma unroll
-    for (int i = 1; i < NW; ++i) {
-      const f32x4_t a = red[i][j][lane];
+  for (int i = 1; i < kNW; ++i) {
+    const f32x4_t v = sums[i][lane];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += a[q];
-    }
-    const int64_t m = m0 + 16 * j + (lane & 15);
-    if (m < M && n < N) store4<F32>(y, m * N + n, v, N - n, (N & 3) == 0);
+    for (int q = 0; q < 4; ++q) acc[q] += v[q];
   }
+  store4<F32>(y, (int64_t)m * N + n, acc, N - n, (N & 3) == 0);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles: a workgroup of (BM / WM) x (BN / WN) waves owns BM rows of x and BN rows
+// of W, a wave WM x WN of them.  A block of K passes through LDS, in two stages:
+// W's 16 x 128 operands as they are packed; x's as 16 rows of 128 bytes, the
+// 16-byte units of row r in the order u ^ (r % 8).  Eight lanes of a load then
+// take one whole line of memory (16 rows x 64 bytes a load, the operand's own
+// order, made the 4096 x 4096 x 7168 product 145 us instead of 134), and the
+// 16 rows that are read back together still lie in different banks.
+template <int BM, int BN>
+struct LinearStage {
+  u32x4_t w[BN / 16][2 * kWave];
+  u32x4_t x[BM / 16][2 * kWave];
+  float sx[BM < 64 ? 64 : BM];
+};
+
+// What brings a block of K into a stage: pieces of 1 KB, half operands, W's first,
+// piece w + kNW n by wave w; the scales of x's rows by the first waves.  Rows past
+// the end of a matrix repeat its last ones.
+template <int BM, int BN, int kNW>
+struct LinearLoads {
+  using Stage = LinearStage<BM, BN>;
+  static constexpr int kPiecesW = BN / 8 / kNW, kPieces = (BN / 8 + BM / 8) / kNW;
+  static_assert(BN / 8 % kNW == 0 && BM / 8 % kNW == 0 && BM / 64 <= kNW, "the pieces go round");
+  const uint8_t* wbase[kPiecesW];
+  const uint8_t* xbase;
+  const float* sbase;
+  int64_t sstride;
+  uint32_t rows8;             // bytes of 8 rows of x
+  uint32_t xlane, xlast;      // this lane's offset in 8 rows, and in the last row
+  uint32_t slane, wlane, lds;
+  int w;
+
+  __device__ __forceinline__ LinearLoads(Stage* stages, const uint8_t* x, const float* xs, int64_t sstride_,
+                                         int64_t M, const uint8_t* wq, int N, int nkb, int64_t m0, int ct0, int w_,
+                                         int lane) {
+    w = w_, sstride = sstride_, lds = lds_addr(stages);
+    const int n_ct = (N + 15) / 16;
+    const uint32_t K = (uint32_t)nkb * 128;
+#pragma unroll
+    for (int n = 0; n < kPiecesW; ++n) {
+      const int p = w + kNW * n;
+      wbase[n] = wq + ((int64_t)min(ct0 + p / 2, n_ct - 1) * nkb * 2 + (p & 1)) * 1024;
+    }
+    const uint32_t unit = 16 * ((lane & 7) ^ (lane >> 3));
+    const uint32_t last = (uint32_t)min((int64_t)BM - 1, M - 1 - m0);
+    xbase = x + m0 * K;
+    rows8 = 8 * K;
+    xlane = (lane >> 3) * K + unit;
+    xlast = last * K + unit;
+    sbase = xs + m0;
+    slane = 4 * min((uint32_t)(64 * w + lane), last);
+    wlane = 16 * lane;
+  }
+  __device__ __forceinline__ void piece(int n, int b, int stage) const {
+    const int p = w + kNW * n;
+    const uint32_t at = lds + stage * (uint32_t)sizeof(Stage) + p * 1024;
+    if (n < kPiecesW)
+      dma16_at(wbase[n < kPiecesW ? n : 0] + (int64_t)b * 2048, wlane, at);
+    else
+      dma16_at(xbase + (int64_t)b * 128, min(xlane + (p - BN / 8) * rows8, xlast), at);
+  }
+  __device__ __forceinline__ void scales(int b, int stage) const {
+    if (w < (BM < 64 ? 1 : BM / 64))
+      dma4_at(sbase + b * sstride, slane,
+              lds + stage * (uint32_t)sizeof(Stage) + (BN / 8 + BM / 8) * 1024 + w * 256);
+  }
+  __device__ __forceinline__ void all(int b, int stage) const {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) piece(n, b, stage);
+    scales(b, stage);
+    asm volatile("" ::: "memory");
+  }
+};
+
+// Workgroup ids go round the 8 XCDs; each XCD takes one run of consecutive tiles,
+// and a run walks down columns of up to 8 tiles of x before the next column of
+// W, so that what an XCD works on at a time is near a square and shares its L2.
+__device__ __forceinline__ void linear_tile(int pid, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n;
+  const int xcd = pid % kNumXcd, q = total / kNumXcd, r = total % kNumXcd;
+  const int at = xcd * q + min(xcd, r) + pid / kNumXcd;
+  constexpr int kGroup = 8;
+  const int group = at / (kGroup * tiles_n), first = group * kGroup;
+  const int rows = min(kGroup, tiles_m - first), in = at - group * kGroup * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+// s_waitcnt for what a wave has to do with LDS: its own loads into it (vmcnt 0), and
+// what it has read of it (lgkmcnt 0); `&`: both.
+constexpr int kWaitLoads = 0x0f70, kWaitReads = 0xc07f;
+
+// SPLIT: part blockIdx.y of gridDim.y of K; y is then float32 [part][M][N].
+// MINW waves a SIMD leave a wave at most 256 registers: with more the compiler puts
+// the products into accumulation registers and moves each back.
+template <int BM, int BN, int WM, int WN, int kStages, int MINW, bool F32, bool SPLIT>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * kWave, MINW) linear_tile_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t sstride, int64_t M,
+    const uint8_t* __restrict__ wq, const float* __restrict__ wsc, int N, int nkb, int tiles_m, int tiles_n,
+    void* __restrict__ y) {
+  constexpr int kWavesM = BM / WM, kNW = kWavesM * (BN / WN);
+  constexpr int kIN = WN / 16, kIM = WM / 16;
+  __shared__ LinearStage<BM, BN> stages[kStages];
+  int tm, tn;
+  linear_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (w % kWavesM) * kIM, wn = (w / kWavesM) * kIN;   // in units of 16
+  const int64_t m0 = (int64_t)tm * BM;
+  const int ct0 = tn * (BN / 16);
+  const int b0 = SPLIT ? (int)((int64_t)nkb * blockIdx.y / gridDim.y) : 0;
+  const int b1 = SPLIT ? (int)((int64_t)nkb * (blockIdx.y + 1) / gridDim.y) : nkb;
+  const LinearLoads<BM, BN, kNW> loads(stages, x, xs, sstride, M, wq, N, nkb, m0, ct0, w, lane);
+  const float* sw = wsc + (int64_t)min((ct0 + wn) / 8, (N - 1) / 128) * nkb;
+  const int xlo = (lane & 15) * 8 + ((lane >> 4) ^ (lane & 7)), xhi = xlo ^ 4;
+
+  f32x4_t acc[kIN][kIM];
+#pragma unroll
+  for (int i = 0; i < kIN; ++i)
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // kStages - 1 blocks are on their way; past the end the last one again, so that a
+  // wave's loads can be counted
+#pragma unroll
+  for (int n = 0; n < kStages - 1; ++n) loads.all(min(b0 + n, b1 - 1), n);
+  int stage = 0;
+  for (int b = b0; b < b1; ++b) {
+    // this stage has landed (but for kStages - 2 blocks' loads) and the one before it
+    // has been read, by this wave and, after the barrier, by all
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((kStages - 2) * decltype(loads)::kPieces) & kWaitReads);
+    lds_barrier();
+    loads.all(min(b + kStages - 1, b1 - 1), stage == 0 ? kStages - 1 : stage - 1);
+    const LinearStage<BM, BN>& st = stages[stage];
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    const float scale = sw[b];
+    i32x8_t a[kIN];
+#pragma unroll
+    for (int i = 0; i < kIN; ++i) a[i] = operand(st.w[wn + i][lane], st.w[wn + i][kWave + lane]);
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) {
+      const i32x8_t v = operand(st.x[wm + j][xlo], st.x[wm + j][xhi]);
+      const float c = st.sx[(wm + j) * 16 + (lane & 15)] * scale;
+#pragma unroll
+      for (int i = 0; i < kIN; ++i) {
+        const f32x4_t t = mfma_codes(a[i], v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(t[q], c, acc[i][j][q]);
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(kWaitLoads);      // no load into LDS may outlive the workgroup
+  if (SPLIT) y = static_cast<float*>(y) + (int64_t)blockIdx.y * M * N;
+  store_tile<F32, kIN, kIM>(y, acc, m0 + wm * 16, (ct0 + wn) * 16, M, N, lane);
+}
+
+// Large products: 256 x 256, eight waves of 128 x 64, of which the two of a SIMD
+// take turns: one reads a whole block's operands from LDS into registers while
+// the other multiplies.  Phase 2 b: the first four waves read block b, the others
+// multiply block b - 1; phase 2 b + 1: the other way round; a barrier between
+// phases.  A stage is free once both have read it, after phase 2 b + 1: block b
+// + 2's loads go out in phase 2 b + 2 (by the first waves while they read, by the
+// others one by one between the matrix instructions) and are waited for at the
+// end of phase 2 b + 3.
+constexpr int kBig = 256;
+template <bool F32>
+__global__ void __launch_bounds__(512, 2) linear_big_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t sstride, int64_t M,
+    const uint8_t* __restrict__ wq, const float* __restrict__ wsc, int N, int nkb, int tiles_m, int tiles_n,
+    void* __restrict__ y) {
+  constexpr int kIN = 4, kIM = 8, kNW = 8;
+  // A product's multiply-adds follow its matrix instruction by kBehind others: its
+  // result takes that long (1: 592 us for 8192^3, 2: 477, 3: 451, 4: 455).
+  constexpr int kBehind = 3;
+  __shared__ LinearStage<kBig, kBig> stages[2];
+  int tm, tn;
+  linear_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (w % 2) * kIM, wn = (w / 2) * kIN;
+  const int64_t m0 = (int64_t)tm * kBig;
+  const int ct0 = tn * (kBig / 16);
+  const LinearLoads<kBig, kBig, kNW> loads(stages, x, xs, sstride, M, wq, N, nkb, m0, ct0, w, lane);
+  constexpr int kPieces = LinearLoads<kBig, kBig, kNW>::kPieces;
+  const float* sw = wsc + (int64_t)min((ct0 + wn) / 8, (N - 1) / 128) * nkb;
+  const int xlo = (lane & 15) * 8 + ((lane >> 4) ^ (lane & 7)), xhi = xlo ^ 4;
+
+  f32x4_t acc[kIN][kIM];
+#pragma unroll
+  for (int i = 0; i < kIN; ++i)
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  i32x8_t a[kIN], v[kIM];
+  float c[kIM], scale = sw[0];
+  auto read = [&](int b) __attribute__((always_inline)) {
+    const LinearStage<kBig, kBig>& st = stages[b & 1];
+#pragma unroll
+    for (int i = 0; i < kIN; ++i) a[i] = operand(st.w[wn + i][lane], st.w[wn + i][kWave + lane]);
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) v[j] = operand(st.x[wm + j][xlo], st.x[wm + j][xhi]);
+#pragma unroll
+    for (int j = 0; j < kIM; ++j) c[j] = st.sx[(wm + j) * 16 + (lane & 15)] * scale;
+    scale = sw[min(b + 1, nkb - 1)];
+  };
+  auto scaled = [&](int n, const f32x4_t& t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      acc[n % kIN][n / kIN][q] = __builtin_fmaf(t[q], c[n / kIN], acc[n % kIN][n / kIN][q]);
+  };
+  auto multiply = [&](int b, bool load) __attribute__((always_inline)) {
+    constexpr int kAll = kIN * kIM;
+    f32x4_t t[kBehind + 1];
+    const int next = min(b + 2, nkb - 1);      // (past the end: the last block again)
+    if (load) loads.scales(next, b & 1);
+#pragma unroll
+    for (int n = 0; n < kAll; ++n) {
+      if (load && n % (kAll / kPieces) == 0) loads.piece(n / (kAll / kPieces), next, b & 1);
+      t[n % (kBehind + 1)] = mfma_codes(a[n % kIN], v[n / kIN]);
+      if (n >= kBehind) scaled(n - kBehind, t[(n - kBehind) % (kBehind + 1)]);
+      __builtin_amdgcn_sched_barrier(0);       // the order as it stands here
+    }
+#pragma unroll
+    for (int n = kAll - kBehind; n < kAll; ++n) scaled(n, t[n % (kBehind + 1)]);
+  };
+
+  loads.all(0, 0);
+  __builtin_amdgcn_s_waitcnt(kWaitLoads);
+  lds_barrier();
+  if (w < kNW / 2) {
+    for (int b = 0; b < nkb; ++b) {
+      read(b);
+      loads.all(min(b + 1, nkb - 1), (b + 1) & 1);
+      __builtin_amdgcn_s_waitcnt(kWaitReads);
+      lds_barrier();
+      __builtin_amdgcn_s_setprio(1);
+      multiply(b, false);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
+      lds_barrier();
+    }
+    lds_barrier();
+  } else {
+    loads.all(min(1, nkb - 1), 1);
+    lds_barrier();
+    for (int b = 0; b < nkb; ++b) {
+      read(b);
+      __builtin_amdgcn_s_waitcnt(kWaitLoads & kWaitReads);
+      lds_barrier();
+      __builtin_amdgcn_s_setprio(1);
+      multiply(b, true);
+      __builtin_amdgcn_s_setprio(0);
+      lds_barrier();
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);    // no load into LDS may outlive the workgroup
+  }
+  store_tile<F32, kIN, kIM>(y, acc, m0 + wm * 16, (ct0 + wn) * 16, M, N, lane);
+}
+
+// y = the sum of the parts, in order, four outputs a thread.
+template <bool F32>
+__global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ parts, int n_parts,
+                                                          int64_t total, void* __restrict__ y) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= total) return;
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+  const int some = (int)min((int64_t)4, total - at);
+  const bool wide = (total & 3) == 0;
+  for (int p = 0; p < n_parts; ++p) {
+    const float* q = parts + p * total + at;
+    if (wide) {
+      const f32x4_t u = *reinterpret_cast<const f32x4_t*>(q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += u[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < some) s[k] += q[k];
+    }
+  }
+  store4<F32>(y, at, s, some, wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -213,32 +524,130 @@ int launch_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float*
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
+// ---------------------------------------------------------------------------
+// Which kernel.  Up to 16 rows: linear_rows_kernel (64 x 64 tiles, the next best
+// there: 7.9 us against 5.1 for one row of 7168 x 2048, 18 against 7 for 13 of 576
+// x 7168).  Else the tile, and the number of parts of K, with the shortest
+// estimated time: kStart for launch and fill, then per block of K the longer of
+// what one workgroup takes (its loads' way through the memory) and what a CU takes
+// for all of its tiles, measured:
+//                         us a block, one tile   us a block and tile, many
+//   64 x 64                     0.28                   0.225
+//   64 x 128                    0.40                   0.345
+//   128 x 128                   0.72                   0.55
+//   256 x 256                   1.4                    1.76
+// and for parts the join's launch and its bytes.  Both sides of a border, us: 64 x
+// 4096 x 7168 in 64 x 64 tiles 18.4, in 2 parts 14.5, in 4 12.0, in 8 14.4; 512 x
+// 4096 x 7168 in 64 x 64 28, 64 x 128 29, 128 x 128 43; 1024 x 4096 x 7168 57, 42,
+// 44; 2048 x 4096 x 7168 103, 82, 65, 256 x 256 84; 4096 x 4096 x 7168 211, 166,
+// 132, 119.
+struct LinearForm {
+  int tile, parts;              // of kTiles; parts of K
+};
+
+struct LinearTile {
+  int m, n;
+  double one, many;
+};
+constexpr LinearTile kTiles[4] = {{64, 64, 0.28, 0.225}, {64, 128, 0.40, 0.345}, {128, 128, 0.72, 0.55},
+                                  {256, 256, 1.4, 1.76}};
+constexpr int kRowsMost = 16;                      // of linear_rows_kernel
+constexpr int kPartsMost = 8;
+constexpr int64_t kPartBytes = 32 << 20;           // all parts together: more costs more than it gives
+
+static LinearForm linear_form(int64_t M, int N, int nkb) {
+  constexpr double kCUs = 256, kStart = 3.0, kJoin = 3.3, kJoinBytesPerUs = 5e6;
+  LinearForm best = {0, 1};
+  double least = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const double tiles = (double)((M + kTiles[i].m - 1) / kTiles[i].m) * ((N + kTiles[i].n - 1) / kTiles[i].n);
+    for (int parts = 1; parts <= (i < 3 ? kPartsMost : 1) && parts <= nkb; parts *= 2) {
+      const int64_t bytes = (int64_t)parts * M * N * 4;
+      if (parts > 1 && bytes > kPartBytes) break;
+      const double rounds = std::ceil(tiles * parts / kCUs);
+      double us = kStart + (double)nkb / parts * std::max(kTiles[i].one, rounds * kTiles[i].many);
+      if (parts > 1) us += kJoin + 2.0 * bytes / kJoinBytesPerUs;
+      if (us < least) least = us, best = {i, parts};
+    }
+  }
+  return best;
+}
+
+// Enough for every smaller M too.
 size_t linear_fp8_workspace_bytes(int64_t M, int N, int K) {
-  (void)M, (void)N, (void)K;
-  return 0;
+  if (M <= kRowsMost || K == 128) return 0;
+  return (size_t)std::min(kPartBytes, (int64_t)kPartsMost * 4 * M * N);
+}
+
+struct LinearCall {
+  const uint8_t* x;
+  const float* xs;
+  int64_t sstride, M;
+  const uint8_t* wq;
+  const float* wsc;
+  int N, nkb;
+  void* y;
+  void* parts;
+  hipStream_t stream;
+};
+
+template <bool F32>
+static void launch_linear_rows(const LinearCall& c) {
+  // 8 waves, 4 blocks of each on their way; of (2, 4), (4, 4), (8, 2), (8, 4), (16, 1), (16, 4)
+  // within 5 % of the best from 1 x 512 x 1024 to 16 x 7168 x 7168
+  hipLaunchKernelGGL((linear_rows_kernel<8, 4, F32>), dim3((c.N + 15) / 16), dim3(8 * kWave), 0, c.stream, c.x, c.xs,
+                     c.sstride, (int)c.M, c.wq, c.wsc, c.N, c.nkb, c.y);
+}
+
+template <int BM, int BN, int WM, int WN, int kStages, int MINW, bool F32>
+static int launch_linear_tiles(const LinearCall& c, int parts) {
+  const int64_t tm = (c.M + BM - 1) / BM, tn = (c.N + BN - 1) / BN;
+  constexpr int kThreads = (BM / WM) * (BN / WN) * kWave;
+  if (tm * tn * kThreads * parts > 0xffffffffLL) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(tm * tn), parts);
+  if (parts > 1) {
+    hipLaunchKernelGGL((linear_tile_kernel<BM, BN, WM, WN, kStages, MINW, true, true>), grid, dim3(kThreads), 0,
+                       c.stream, c.x, c.xs, c.sstride, c.M, c.wq, c.wsc, c.N, c.nkb, (int)tm, (int)tn, c.parts);
+    const int64_t total = c.M * c.N;
+    hipLaunchKernelGGL(linear_join_kernel<F32>, dim3((unsigned)((total + 1023) / 1024)), dim3(256), 0, c.stream,
+                       static_cast<const float*>(c.parts), parts, total, c.y);
+  } else {
+    hipLaunchKernelGGL((linear_tile_kernel<BM, BN, WM, WN, kStages, MINW, F32, false>), grid, dim3(kThreads), 0,
+                       c.stream, c.x, c.xs, c.sstride, c.M, c.wq, c.wsc, c.N, c.nkb, (int)tm, (int)tn, c.y);
+  }
+  return MOE_OK;
+}
+
+template <bool F32>
+static int launch_linear_big(const LinearCall& c) {
+  const int64_t tm = (c.M + kBig - 1) / kBig, tn = (c.N + kBig - 1) / kBig;
+  if (tm * tn * 512 > 0xffffffffLL) return MOE_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(linear_big_kernel<F32>, dim3((unsigned)(tm * tn)), dim3(512), 0, c.stream, c.x, c.xs, c.sstride,
+                     c.M, c.wq, c.wsc, c.N, c.nkb, (int)tm, (int)tn, c.y);
+  return MOE_OK;
+}
+
+template <bool F32>
+static int launch_linear(const LinearCall& c) {
+  if (c.M <= kRowsMost) {
+    launch_linear_rows<F32>(c);
+    return MOE_OK;
+  }
+  const LinearForm form = linear_form(c.M, c.N, c.nkb);
+  switch (form.tile) {
+    case 0: return launch_linear_tiles<64, 64, 32, 32, 4, 2, F32>(c, form.parts);
+    case 1: return launch_linear_tiles<64, 128, 32, 32, 3, 4, F32>(c, form.parts);
+    case 2: return launch_linear_tiles<128, 128, 64, 64, 2, 2, F32>(c, form.parts);
+    default: return launch_linear_big<F32>(c);
+  }
 }
 
 int launch_linear_fp8(const uint8_t* x, const float* xs, int64_t sstride, int64_t M, int N, int K,
                       const uint8_t* wq, const float* wsc, void* y, int f32, void* workspace,
                       hipStream_t stream) {
-  (void)workspace;
-  const int nkb = K / 128;
-  const int n_ct = (N + 15) / 16;
-#define MOE_ROWS(MT, NW, PF)                                                                       \
-  do {                                                                                             \
-    const int64_t my = (M + 16 * MT - 1) / (16 * MT);                                              \
-    if (my > 65535) return MOE_ERR_UNSUPPORTED;                                                    \
-    if (f32)                                                                                       \
-      hipLaunchKernelGGL((linear_rows_kernel<MT, NW, PF, true>), dim3(n_ct, (unsigned)my), dim3(NW * kWave), \
-                         0, stream, x, xs, sstride, M, wq, wsc, N, nkb, y);                        \
-    else                                                                                           \
-      hipLaunchKernelGGL((linear_rows_kernel<MT, NW, PF, false>), dim3(n_ct, (unsigned)my), dim3(NW * kWave), \
-                         0, stream, x, xs, sstride, M, wq, wsc, N, nkb, y);                        \
-  } while (0)
-  if (M <= 16) MOE_ROWS(1, 4, 4);
-  else if (M <= 32) MOE_ROWS(2, 4, 4);
-  else MOE_ROWS(4, 4, 2);
-#undef MOE_ROWS
+  const LinearCall call = {x, xs, sstride, M, wq, wsc, N, K / 128, y, workspace, stream};
+  const int st = f32 ? launch_linear<true>(call) : launch_linear<false>(call);
+  if (st != MOE_OK) return st;
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -34,7 +34,8 @@ SIZES = [
     (13, 576, 7168), (17, 129, 384), (31, 130, 512), (33, 1000, 1280), (64, 640, 2048), (65, 384, 256),
     (100, 2112, 1536), (127, 128, 4096), (128, 257, 128), (129, 512, 896), (200, 64, 8192), (255, 255, 640),
     (257, 1024, 512), (333, 4096, 2048), (512, 320, 2176), (1000, 777, 640), (1025, 2048, 256), (2048, 1280, 1024),
-    (3000, 130, 384), (2300, 4098, 512),
+    (3000, 130, 384), (2300, 4098, 512), (300, 6000, 384), (700, 3001, 512), (4101, 4098, 256), (4200, 4224, 640),
+    (16385, 1030, 128), (30, 64, 16384), (4095, 4090, 384), (3900, 3841, 640), (4096, 4096, 128),
 ]
 
 
