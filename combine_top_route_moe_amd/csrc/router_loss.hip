@@ -17,12 +17,15 @@
 // many tokens (4 E bytes read, in the gradient 4 E more written), launch bound
 // on few.  Counts are integers and every float sum has a fixed order, so equal
 // calls give equal bits.
+#include <algorithm>
+
 #include "reduce.h"
 
 namespace moe {
 
 constexpr int kLossWaves = 16;          // waves of a loss workgroup
 constexpr int kLossMaxGroups = 128;     // workgroups of the first launch at most
+constexpr int kLossOneGroup = 64;       // tokens that one workgroup takes in one launch
 
 // A token's probabilities from its logits (v: -inf where there is no expert);
 // returns logsumexp.  As in the routing, a NaN counts as -inf and a logit equal
@@ -58,15 +61,19 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ row, int E
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
-// Shares of one workgroup, in the workspace: [groups] x {E floats of sum p, E
-// int32 counts}, then [groups] float64 of sum lse^2, then [groups] int32 of n.
+// Tokens that a wave loads before it works on the first.
+template <int EPL>
+constexpr int kTokensAhead = EPL <= 2 ? 4 : EPL <= 8 ? 2 : 1;
+
+// Shares of one workgroup, in the workspace: [groups] float64 of sum lse^2, then
+// [groups] x {E floats of sum p, E int32 counts}, then [groups] int32 of n.
 struct LossShares {
+  double* z;
   float* probs;
   int32_t* counts;
-  double* z;
   int32_t* tokens;
 };
-__host__ __device__ inline LossShares loss_shares(void* ws, int groups, int E) {
+__device__ __forceinline__ LossShares loss_shares(void* ws, int groups, int E) {
   LossShares s;
   s.z = static_cast<double*>(ws);
   s.probs = reinterpret_cast<float*>(s.z + groups);
@@ -75,47 +82,38 @@ __host__ __device__ inline LossShares loss_shares(void* ws, int groups, int E) {
   return s;
 }
 
-// What the shares come to: the outputs, by one workgroup.
-__device__ __forceinline__ void write_losses(const LossShares& s, int groups, int E, int K,
-                                             float* __restrict__ loss, int32_t* __restrict__ counts,
-                                             float* __restrict__ probs, int32_t* __restrict__ tokens,
-                                             double* sums) {
-  int n = 0;
-  double z = 0.0;
-  for (int g = 0; g < groups; ++g) n += s.tokens[g], z += s.z[g];
-  const double inv = n > 0 ? 1.0 / n : 0.0;
-  double dot = 0.0;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    double p = 0.0;
-    int c = 0;
-    for (int g = 0; g < groups; ++g) p += s.probs[(size_t)g * E + e], c += s.counts[(size_t)g * E + e];
-    p *= inv;
-    counts[e] = c;
-    probs[e] = (float)p;
-    dot += p * c;
-  }
-  sums[threadIdx.x] = dot;
-  __syncthreads();
-  for (int half = blockDim.x / 2; half > 0; half /= 2) {
-    if ((int)threadIdx.x < half) sums[threadIdx.x] += sums[threadIdx.x + half];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    loss[0] = (float)(sums[0] * inv * E / K);
-    loss[1] = (float)(z * inv);
-    tokens[0] = n;
-  }
+struct LossOut {
+  float* loss;
+  int32_t* counts;
+  float* probs;
+  int32_t* tokens;
+};
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
 }
 
-template <int EPL>
+// dot = sum_e (sum p)_e counts_e
+__device__ __forceinline__ void write_losses(const LossOut& out, double dot, double z, int n, int E, int K) {
+  const double inv = n > 0 ? 1.0 / n : 0.0;
+  out.loss[0] = (float)(dot * inv * inv * E / K);
+  out.loss[1] = (float)(z * inv);
+  out.tokens[0] = n;
+}
+
+// ONE: the only workgroup, which writes the outputs; else it leaves its share.
+template <int EPL, bool ONE>
 __global__ void __launch_bounds__(kLossWaves * kWave) balance_share_kernel(
     const float* __restrict__ logits, const uint8_t* __restrict__ row_valid,
-    const int32_t* __restrict__ topk_idx, int T, int E, int K, void* ws, int32_t* __restrict__ dev_error) {
+    const int32_t* __restrict__ topk_idx, int T, int E, int K, void* ws, LossOut out,
+    int32_t* __restrict__ dev_error) {
   __shared__ float meet[kLossWaves / 2][EPL * kWave];
   __shared__ int32_t hist[EPL * kWave];
   __shared__ double zs[kLossWaves];
   __shared__ int32_t ns[kLossWaves];
-  const LossShares out = loss_shares(ws, gridDim.x, E);
+  constexpr int kTok = kTokensAhead<EPL>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int e = threadIdx.x; e < EPL * kWave; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -124,20 +122,33 @@ __global__ void __launch_bounds__(kLossWaves * kWave) balance_share_kernel(
   for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
   double z = 0.0;
   int n = 0;
-  for (int64_t t = (int64_t)blockIdx.x * kLossWaves + wave; t < T; t += (int64_t)gridDim.x * kLossWaves) {
-    if (row_valid && !row_valid[t]) continue;
-    float v[EPL];
-    load_logits<EPL>(logits + t * E, E, lane, v);
-    if (lane < K) {
-      const int id = topk_idx[t * K + lane];
-      if (id >= E) raise_error(dev_error, MOE_DEVERR_EXPERT_RANGE);
-      else if (id >= 0) atomicAdd(&hist[id], 1);
-    }
-    const float lse = softmax<EPL>(v, E, lane);
-    ++n;
-    if (finite(lse)) z += (double)lse * lse;
+  // wave w of all takes tokens w, w + waves, ..
+  const int64_t waves = (int64_t)gridDim.x * kLossWaves;
+  for (int64_t t0 = (int64_t)blockIdx.x * kLossWaves + wave; t0 < T; t0 += waves * kTok) {
+    float v[kTok][EPL];
+    int id[kTok];
+    bool real[kTok];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) acc[j] += v[j];
+    for (int u = 0; u < kTok; ++u) {
+      const int64_t t = min(t0 + u * waves, (int64_t)T - 1);
+      real[u] = t0 + u * waves < T && (!row_valid || row_valid[t]);
+      load_logits<EPL>(logits + t * E, E, lane, v[u]);
+      id[u] = real[u] && lane < K ? topk_idx[t * K + lane] : -1;
+    }
+    // (no branch on what is real: the tokens' chains of operations run side by side)
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+      const float lse = softmax<EPL>(v[u], E, lane);
+      n += real[u];
+      z += real[u] && finite(lse) ? (double)lse * lse : 0.0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) acc[j] += real[u] ? v[u][j] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+      if (id[u] >= E) raise_error(dev_error, MOE_DEVERR_EXPERT_RANGE);
+      else if (id[u] >= 0) atomicAdd(&hist[id[u]], 1);
+    }
   }
   if (lane == 0) zs[wave] = z, ns[wave] = n;
   // the waves' sums meet in halves: 8 + 8, 4 + 4, ..
@@ -152,47 +163,103 @@ __global__ void __launch_bounds__(kLossWaves * kWave) balance_share_kernel(
       for (int j = 0; j < EPL; ++j) acc[j] += meet[wave][lane + 64 * j];
     __syncthreads();
   }
-  if (wave == 0) {
+  if (wave > 0) return;
+  for (int i = 1; i < kLossWaves; ++i) z += zs[i], n += ns[i];
+  const LossShares s = loss_shares(ws, gridDim.x, E);
+  double dot = 0.0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = lane + 64 * j;
-      if (e < E) out.probs[(size_t)blockIdx.x * E + e] = acc[j], out.counts[(size_t)blockIdx.x * E + e] = hist[e];
+  for (int j = 0; j < EPL; ++j) {
+    const int e = lane + 64 * j;
+    if (e >= E) break;
+    if (ONE) {
+      out.counts[e] = hist[e];
+      out.probs[e] = n > 0 ? acc[j] / (float)n : 0.0f;
+      dot += (double)acc[j] * hist[e];
+    } else {
+      s.counts[(size_t)blockIdx.x * E + e] = hist[e];
+      s.probs[(size_t)blockIdx.x * E + e] = acc[j];
     }
-    if (lane == 0) {
-      for (int i = 1; i < kLossWaves; ++i) z += zs[i], n += ns[i];
-      out.z[blockIdx.x] = z;
-      out.tokens[blockIdx.x] = n;
-    }
+  }
+  if (ONE) dot = wave_sum_f64(dot);
+  if (lane > 0) return;
+  if (ONE) {
+    write_losses(out, dot, z, n, E, K);
+  } else {
+    s.z[blockIdx.x] = z;
+    s.tokens[blockIdx.x] = n;
   }
 }
 
-__global__ void __launch_bounds__(1024) balance_join_kernel(void* ws, int groups, int E, int K,
-                                                            float* __restrict__ loss,
-                                                            int32_t* __restrict__ counts,
-                                                            float* __restrict__ probs,
-                                                            int32_t* __restrict__ tokens) {
-  __shared__ double sums[1024];
-  write_losses(loss_shares(ws, groups, E), groups, E, K, loss, counts, probs, tokens, sums);
+// The shares' sums, by one workgroup: 1024 / kE threads an expert (kE the power of
+// two above E), each every so many shares, their sums in order.
+__global__ void __launch_bounds__(1024) balance_join_kernel(void* ws, int groups, int E, int log_kE, int K,
+                                                            LossOut out) {
+  __shared__ double ps[1024];
+  __shared__ int32_t cs[1024];
+  __shared__ double zs[16];
+  __shared__ int32_t n_all;
+  const LossShares s = loss_shares(ws, groups, E);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int kE = 1 << log_kE, e = tid & (kE - 1), slice = tid >> log_kE, slices = 1024 >> log_kE;
+  double p = 0.0;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int g = slice; g < groups; g += slices) p += s.probs[(size_t)g * E + e], c += s.counts[(size_t)g * E + e];
+  }
+  ps[tid] = p;
+  cs[tid] = c;
+  double z = 0.0;
+  if (wave == 0) {
+    int n = 0;
+    for (int g = lane; g < groups; g += kWave) z += s.z[g], n += s.tokens[g];
+    z = wave_sum_f64(z);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+    if (lane == 0) n_all = n;
+  }
+  __syncthreads();
+  const int n = n_all;
+  double dot = 0.0;
+  if (slice == 0 && e < E) {
+    for (int i = 1; i < slices; ++i) p += ps[i * kE + e], c += cs[i * kE + e];
+    out.counts[e] = c;
+    out.probs[e] = n > 0 ? (float)(p / n) : 0.0f;
+    dot = p * c;
+  }
+  dot = wave_sum_f64(dot);
+  if (lane == 0) zs[wave] = dot;
+  __syncthreads();
+  if (tid > 0) return;
+  for (int i = 1; i < 16; ++i) dot += zs[i];
+  write_losses(out, dot, z, n, E, K);
 }
 
+// Few tokens in one launch: the second costs more than the longer walk.
 static int loss_groups(int T) {
+  if (T <= kLossOneGroup) return T > 0;
   const int groups = (T + kLossWaves - 1) / kLossWaves;
   return groups < kLossMaxGroups ? groups : kLossMaxGroups;
 }
 
 size_t balance_loss_workspace_bytes(int T, int E) {
-  return (size_t)loss_groups(T) * (8 + 8 * (size_t)E + 4);
+  const int groups = loss_groups(T);
+  return groups > 1 ? (size_t)groups * (8 + 8 * (size_t)E + 4) : 0;
 }
 
 int launch_balance_loss(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx, int T,
                         int E, int K, float* loss, int32_t* counts, float* probs, int32_t* tokens,
                         void* ws, int32_t* dev_error, hipStream_t stream) {
-  const int groups = loss_groups(T), epl = (E + kWave - 1) / kWave;
-#define MOE_LOSS(N)                                                                              \
-  hipLaunchKernelGGL(balance_share_kernel<N>, dim3(groups), dim3(kLossWaves * kWave), 0, stream, \
-                     logits, row_valid, topk_idx, T, E, K, ws, dev_error)
-  if (groups == 0) {
-  } else if (epl <= 1) {
+  const int groups = std::max(1, loss_groups(T)), epl = (E + kWave - 1) / kWave;
+  const LossOut out = {loss, counts, probs, tokens};
+#define MOE_LOSS(N)                                                                                       \
+  if (groups == 1)                                                                                        \
+    hipLaunchKernelGGL((balance_share_kernel<N, true>), dim3(1), dim3(kLossWaves * kWave), 0, stream,     \
+                       logits, row_valid, topk_idx, T, E, K, ws, out, dev_error);                         \
+  else                                                                                                    \
+    hipLaunchKernelGGL((balance_share_kernel<N, false>), dim3(groups), dim3(kLossWaves * kWave), 0, stream, \
+                       logits, row_valid, topk_idx, T, E, K, ws, out, dev_error)
+  if (epl <= 1) {
     MOE_LOSS(1);
   } else if (epl <= 2) {
     MOE_LOSS(2);
@@ -204,8 +271,11 @@ int launch_balance_loss(const float* logits, const uint8_t* row_valid, const int
     MOE_LOSS(16);
   }
 #undef MOE_LOSS
-  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, stream, ws, groups, E, K, loss, counts,
-                     probs, tokens);
+  if (groups > 1) {
+    int log_kE = 0;
+    while (1 << log_kE < E) ++log_kE;
+    hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, stream, ws, groups, E, log_kE, K, out);
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

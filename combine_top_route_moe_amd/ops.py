@@ -779,16 +779,21 @@ def moe_combine_check(rows: torch.Tensor, row_of: torch.Tensor, T: int, K: int,
         _ptr(dev_error), _stream(stream)))
 
 
-def _output(want, shape, dtype: torch.dtype, device, stream, name: str):
-    """An output that the caller asks for by True, declines by False or None, or
-    passes as a buffer of that shape."""
+def _output(want, shape, dtype: torch.dtype, like: torch.Tensor, stream, name: str):
+    """(tensor, device pointer) of an output that the caller asks for by True,
+    declines by False or None, or passes as a buffer of that shape.  (A new
+    tensor needs no checks: they cost as much as its allocation.)"""
     if want is None or want is False:
-        return None
+        return None, None
     if want is True:
-        return _empty(shape, dtype, device, stream)
-    if tuple(want.shape) != tuple(shape):
+        if stream is None:
+            t = torch.empty_like(like) if (dtype, shape) == (like.dtype, like.shape) else like.new_empty(shape, dtype=dtype)
+        else:
+            t = _empty(shape, dtype, like.device, stream)
+        return t, t.data_ptr()
+    if want.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(want.shape)}")
-    return want
+    return want, _pointers(like.get_device(), (want, dtype, name))[0]
 
 
 def _gain(weight: torch.Tensor, H: int):
@@ -825,24 +830,23 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if residual is not None and residual.shape != x.shape:
         raise ValueError("residual does not match x")
     flags, wtype = _gain(weight, H)
-    raw = _one_device(stream, x, weight, residual)
-    dev = x.device
-    h = _output(residual is not None if h is None else h, (T, H), torch.bfloat16, dev, stream, "h")
-    y = _output(y, (T, H), torch.bfloat16, dev, stream, "y")
-    codes = _output(codes, (T, H), torch.uint8, dev, stream, "codes")
-    rstd = _output(rstd, (T,), torch.float32, dev, stream, "rstd")
+    raw = _one_device(stream, x)
+    px, pw, pr = _pointers(x.get_device(), (x, torch.bfloat16, "x"), (weight, wtype, "weight"),
+                           (residual, torch.bfloat16, "residual"))
+    h, ph = _output(residual is not None if h is None else h, x.shape, torch.bfloat16, x, stream, "h")
+    y, py = _output(y, x.shape, torch.bfloat16, x, stream, "y")
+    codes, pc = _output(codes, x.shape, torch.uint8, x, stream, "codes")
+    rstd, pi = _output(rstd, (T,), torch.float32, x, stream, "rstd")
+    ps = None
     if codes is None:
         if scales is not None:
             raise ValueError("scales without codes")
     elif scales is None:
-        scales = _empty((H // 128, max(T, 1)), torch.float32, dev, stream)
+        scales, ps = _output(True, (H // 128, max(T, 1)), torch.float32, x, stream, "scales")
     elif scales.dim() != 2 or scales.shape[0] != H // 128 or scales.shape[1] < T:
         raise ValueError("scales must be [H/128, >= T]")
-    px, pw, pr, ph, py, pc, ps, pi = _pointers(
-        x.get_device(), (x, torch.bfloat16, "x"), (weight, wtype, "weight"),
-        (residual, torch.bfloat16, "residual"), (h, torch.bfloat16, "h"), (y, torch.bfloat16, "y"),
-        (codes, torch.uint8, "codes"), (scales, torch.float32, "scales"),
-        (rstd, torch.float32, "rstd"))
+    else:
+        ps = _pointers(x.get_device(), (scales, torch.float32, "scales"))[0]
     check("moe_rmsnorm", load().moe_rmsnorm(
         px, pr, pw, T, H, eps, flags, ph, py, pc, ps, 0 if scales is None else scales.shape[1], pi,
         raw))
@@ -870,19 +874,18 @@ def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     if tuple(rstd.shape) != (T,):
         raise ValueError("rstd must be [T]")
     flags, wtype = _gain(weight, H)
-    raw = _one_device(stream, dy, h, weight)
-    lib = load()
-    dx = _output(True if dx is None else dx, (T, H), torch.bfloat16, dy.device, stream, "dx")
-    d_weight = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy.device, stream,
-                       "d_weight")
-    if workspace is None:
-        need = lib.moe_rmsnorm_backward_workspace_bytes(T, H)
-        workspace = _empty(max(need, 1), torch.uint8, dy.device, stream)
-    pdy, ph, pi, pw, pd, px, pdw, pws = _pointers(
+    raw = _one_device(stream, dy)
+    pdy, ph, pi, pw, pd, pws = _pointers(
         dy.get_device(), (dy, torch.bfloat16, "dy"), (h, torch.bfloat16, "h"),
         (rstd, torch.float32, "rstd"), (weight, wtype, "weight"),
-        (d_residual, torch.bfloat16, "d_residual"), (dx, torch.bfloat16, "dx"),
-        (d_weight, torch.float32, "d_weight"), (workspace, torch.uint8, "workspace"))
+        (d_residual, torch.bfloat16, "d_residual"), (workspace, torch.uint8, "workspace"))
+    lib = load()
+    dx, px = _output(True if dx is None else dx, dy.shape, torch.bfloat16, dy, stream, "dx")
+    d_weight, pdw = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy, stream,
+                            "d_weight")
+    if workspace is None:
+        need = lib.moe_rmsnorm_backward_workspace_bytes(T, H)
+        workspace, pws = _output(True, (max(need, 1),), torch.uint8, dy, stream, "workspace")
     check("moe_rmsnorm_backward", lib.moe_rmsnorm_backward(
         pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, workspace.numel(), raw))
     return dx, d_weight
@@ -981,15 +984,14 @@ def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeigh
         out_dtype = y.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"y is bfloat16 or float32, not {out_dtype}")
-    raw = _one_device(stream, x, x_scales, weights.packed)
+    raw = _one_device(stream, x, weights.packed)
+    px, ps, pws = _pointers(x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"),
+                            (workspace, torch.uint8, "workspace"))
     lib = load()
-    y = _output(True if y is None else y, (M, N), out_dtype, x.device, stream, "y")
+    y, py = _output(True if y is None else y, (M, N), out_dtype, x, stream, "y")
     if workspace is None:
         need = lib.moe_linear_fp8_workspace_bytes(M, N, K)
-        workspace = _empty(max(need, 1), torch.uint8, x.device, stream)
-    px, ps, py, pws = _pointers(
-        x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"),
-        (y, out_dtype, "y"), (workspace, torch.uint8, "workspace"))
+        workspace, pws = _output(True, (max(need, 1),), torch.uint8, x, stream, "workspace")
     check("moe_linear_fp8", lib.moe_linear_fp8(
         px, ps, x_scales.shape[1], M, N, K, weights.packed.data_ptr(), weights.scales.data_ptr(),
         MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, workspace.numel(), raw))
@@ -1031,24 +1033,24 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E, K = _router_shapes(logits.shape, topk_idx, row_valid)
-    raw = _one_device(stream, logits, topk_idx, row_valid)
-    lib, dev = load(), logits.device
-    want = (True,) * 4 if out is None else (out.loss, out.counts, out.probs, out.num_tokens)
+    raw = _one_device(stream, logits)
     f32, i32 = torch.float32, torch.int32
-    out = RouterLosses(_output(want[0], (2,), f32, dev, stream, "loss"),
-                       _output(want[1], (E,), i32, dev, stream, "counts"),
-                       _output(want[2], (E,), f32, dev, stream, "probs"),
-                       _output(want[3], (1,), i32, dev, stream, "num_tokens"))
-    if workspace is None:
-        workspace = _empty(max(lib.moe_balance_loss_workspace_bytes(T, E), 1), torch.uint8, dev, stream)
-    pl, pv, pi, po, pc, pp, pn, pws, perr = _pointers(
+    pl, pv, pi, pws, perr = _pointers(
         logits.get_device(), (logits, f32, "logits"), (row_valid, torch.uint8, "row_valid"),
-        (topk_idx, i32, "topk_idx"), (out.loss, f32, "loss"), (out.counts, i32, "counts"),
-        (out.probs, f32, "probs"), (out.num_tokens, i32, "num_tokens"),
-        (workspace, torch.uint8, "workspace"), (dev_error, i32, "dev_error"))
+        (topk_idx, i32, "topk_idx"), (workspace, torch.uint8, "workspace"),
+        (dev_error, i32, "dev_error"))
+    lib = load()
+    want = (True,) * 4 if out is None else (out.loss, out.counts, out.probs, out.num_tokens)
+    loss, po = _output(want[0], (2,), f32, logits, stream, "loss")
+    counts, pc = _output(want[1], (E,), i32, logits, stream, "counts")
+    probs, pp = _output(want[2], (E,), f32, logits, stream, "probs")
+    tokens, pn = _output(want[3], (1,), i32, logits, stream, "num_tokens")
+    if workspace is None:
+        need = lib.moe_balance_loss_workspace_bytes(T, E)
+        workspace, pws = _output(True, (max(need, 1),), torch.uint8, logits, stream, "workspace")
     check("moe_balance_loss", lib.moe_balance_loss(pl, pv, pi, T, E, K, po, pc, pp, pn, pws,
                                                    workspace.numel(), perr, raw))
-    return out
+    return RouterLosses(loss, counts, probs, tokens)
 
 
 def moe_route_backward(logits: Optional[torch.Tensor], topk_idx: torch.Tensor, topk_w: torch.Tensor,
@@ -1081,15 +1083,14 @@ def moe_route_backward(logits: Optional[torch.Tensor], topk_idx: torch.Tensor, t
             raise ValueError("d_loss needs counts and num_tokens")
         if d_loss.numel() != 2 or counts.numel() != E or num_tokens.numel() != 1:
             raise ValueError("d_loss must be [2], counts [E] and num_tokens [1]")
-    raw = _one_device(stream, topk_idx, logits, topk_w)
-    d_logits = _output(True if d_logits is None else d_logits, (T, E), torch.float32, topk_idx.device,
-                       stream, "d_logits")
+    raw = _one_device(stream, topk_idx)
     f32, i32 = torch.float32, torch.int32
-    pl, pv, pi, pw, pd, po, pc, pn, pg, perr = _pointers(
+    pl, pv, pi, pw, pd, po, pc, pn, perr = _pointers(
         topk_idx.get_device(), (logits, f32, "logits"), (row_valid, torch.uint8, "row_valid"),
         (topk_idx, i32, "topk_idx"), (topk_w, f32, "topk_w"), (d_topk_w, f32, "d_topk_w"),
         (d_loss, f32, "d_loss"), (counts, i32, "counts"), (num_tokens, i32, "num_tokens"),
-        (d_logits, f32, "d_logits"), (dev_error, i32, "dev_error"))
+        (dev_error, i32, "dev_error"))
+    d_logits, pg = _output(True if d_logits is None else d_logits, (T, E), f32, topk_idx, stream, "d_logits")
     check("moe_route_backward", load().moe_route_backward(
         pl, pv, pi, pw, pd, T, E, K, MOE_ROUTE_RENORM if renormalize else 0, po, pc, pn, pg, perr, raw))
     return d_logits
