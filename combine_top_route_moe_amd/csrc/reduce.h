@@ -35,17 +35,24 @@ __device__ __forceinline__ float lane_f32(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
-// Over the whole wave (every lane active), the result in every lane.
+// Over the whole wave (every lane active), the result in every lane: the rows of
+// 16, then row 0 into 1 and 2 into 3, then both into row 3, read from its last lane.
 __device__ __forceinline__ float wave_sum_f32(float v) {
   v = row16_sum_f32(v);
-  return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
+  return lane_f32(v, 63);
 }
 __device__ __forceinline__ float wave_top_f32(float v) {
   v = fmaxf(v, dpp16<0xB1>(v));
   v = fmaxf(v, dpp16<0x4E>(v));
   v = fmaxf(v, dpp16<0x141>(v));
   v = fmaxf(v, dpp16<0x140>(v));
-  return fmaxf(fmaxf(lane_f32(v, 0), lane_f32(v, 16)), fmaxf(lane_f32(v, 32), lane_f32(v, 48)));
+  int b = __float_as_int(v);
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, 0x142, 0xA, 0xF, false)));
+  b = __float_as_int(v);
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, 0x143, 0xC, 0xF, false)));
+  return lane_f32(v, 63);
 }
 
 // E4M3 codes of 8 values (already divided by the scale and clamped), packed

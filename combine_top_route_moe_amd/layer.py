@@ -96,6 +96,10 @@ class MoELayer:
         self.packed = False
         self.fp8_weights = False
         self.w8a8 = False
+        self.normed = None                          # rows of norm()'s first call on,
+        self.normed_q = self.normed_s = None        # their codes and scales (the FP8 path)
+        self.normed_rows = 0                        # how many rows its last call wrote,
+        self.normed_codes = False                   # and whether their codes too
         self.weights = self.shared_weights = None   # decode()'s handles of the packed weights
         self.decode_tokens = min(T, ops.MOE_DECODE_MAX_TOKENS)
         self.decode_ws = None                       # of decode()'s first call
@@ -256,8 +260,36 @@ class MoELayer:
             ops.moe_grouped_ffn(x, cu, counts, w13, w2, row_scale, y, stage | layout, ws,
                                 self.dev_error, stream=stream)
 
+    # -------------------------------------------------------------------- norm
+    def norm(self, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None,
+             h: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The norm in front of the layer (``moe_rmsnorm``): the rows x [n, H], n
+        <= T, with ``residual`` added (the sum goes to ``h``, by default to the
+        residual's own buffer), normed and weighted.  Returns them in bf16 (a
+        buffer of the layer's: the next call writes it again), for the router's
+        product, ``decode`` and ``forward``.  With n = T, ``forward(logits,
+        None)`` takes them from here; on the FP8 path (``fp8="w8a8"``) it then
+        takes the codes that this call has written along with them, which are
+        those of the unrounded rows, and quantizes nothing itself."""
+        n = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != self.H or n > self.T:
+            raise ValueError(f"x must be [n, {self.H}] with n <= {self.T}")
+        if self.normed is None:
+            self.normed = torch.empty(self.T, self.H, dtype=torch.bfloat16, device=self.device)
+        codes = self.w8a8 and n == self.T
+        if codes and self.normed_q is None:
+            self.normed_q, self.normed_s = torch.empty_like(self.hq), torch.empty_like(self.hs)
+        if h is None and residual is not None:
+            h = residual
+        ops.moe_rmsnorm(x, weight, eps, residual=residual, h=h, y=self.normed[:n],
+                        codes=self.normed_q if codes else False,
+                        scales=self.normed_s if codes else None)
+        self.normed_rows, self.normed_codes = n, codes
+        return self.normed[:n]
+
     # ------------------------------------------------------------------ stages
-    def stages(self, logits: torch.Tensor, hidden: torch.Tensor,
+    def stages(self, logits: torch.Tensor, hidden: Optional[torch.Tensor],
                row_valid: Optional[torch.Tensor] = None,
                overlap_shared: bool = False) -> List[Tuple[str, Callable[[], None]]]:
         """The layer as an ordered list of ``(name, enqueue)`` stages.  Each
@@ -266,8 +298,15 @@ class MoELayer:
         ``overlap_shared`` the shared expert is the first stage instead and
         runs on the side stream, which the current stream waits for before
         the combine (the form ``forward`` uses; a graph capture of it holds
-        the two branches)."""
+        the two branches).  ``hidden`` None: the rows of ``norm``."""
         p = self.perm
+        quantized = hidden is None and self.w8a8
+        if hidden is None:
+            if self.normed is None or self.normed_rows != self.T:
+                raise ValueError("without hidden, norm() has to have written all of the layer's rows")
+            if quantized and not self.normed_codes:
+                raise ValueError("norm() ran before the FP8 path's weights were set: call it again")
+            hidden = self.normed
         x = self.hidden_q if self.hidden_q is not None else hidden
         st = [("route", lambda: ops.moe_route(logits, self.K, row_valid, self.renormalize,
                                                self.topk_idx, self.topk_w))]
@@ -275,11 +314,13 @@ class MoELayer:
             # the dispatch quantizer for real: codes + scales of the [T, H]
             # rows; the permute moves the codes, the GEMM finds each permuted
             # row's scales through src_of
-            x = self.hq.view(torch.bfloat16)
-            x_ffn = (p.x_perm.view(torch.uint8), self.hs, p.src_of)
-            x_shared = (self.hq, self.hs, None)
-            st.append(("dispatch_quant", lambda: ops.moe_quant_rows_fp8(
-                hidden, None, self.hq, self.hs)))
+            hq, hs = (self.normed_q, self.normed_s) if quantized else (self.hq, self.hs)
+            x = hq.view(torch.bfloat16)
+            x_ffn = (p.x_perm.view(torch.uint8), hs, p.src_of)
+            x_shared = (hq, hs, None)
+            if not quantized:
+                st.append(("dispatch_quant", lambda: ops.moe_quant_rows_fp8(
+                    hidden, None, self.hq, self.hs)))
         else:
             x_ffn = p.x_perm
             x_shared = hidden
@@ -322,7 +363,7 @@ class MoELayer:
 
                 # it forks at the start, or (FP8 path) once its input rows
                 # are quantized; the side stream waits for what precedes it
-                at = [n for n, _ in st].index("dispatch_quant") + 1 if self.w8a8 else 0
+                at = [n for n, _ in st].index("dispatch_quant") + 1 if self.w8a8 and not quantized else 0
                 st.insert(at, ("shared_ffn", fork))
                 st.append(("join_shared", lambda: torch.cuda.current_stream().wait_stream(self.side)))
             else:
@@ -333,10 +374,11 @@ class MoELayer:
             self.dev_error)))
         return st
 
-    def forward(self, logits: torch.Tensor, hidden: torch.Tensor,
+    def forward(self, logits: torch.Tensor, hidden: Optional[torch.Tensor],
                 row_valid: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Run the whole layer (enqueue only; no sync, no allocation), the
-        shared expert concurrently with the routed path."""
+        shared expert concurrently with the routed path.  ``hidden`` None: on
+        the rows that ``norm`` left."""
         for _, enqueue in self.stages(logits, hidden, row_valid, overlap_shared=True):
             enqueue()
         return self.out
@@ -371,6 +413,29 @@ class MoELayer:
                        workspace=self.decode_ws, dev_error=self.dev_error)
         return self.out[:n]
 
+    # ------------------------------------------------------- the router's training
+    def balance_loss(self, logits: torch.Tensor, row_valid: Optional[torch.Tensor] = None,
+                     out: Optional[ops.RouterLosses] = None) -> ops.RouterLosses:
+        """The balance and z losses of the routes that the last call on these
+        logits left in ``topk_idx`` (``moe_balance_loss``), with the experts'
+        counts and mean probabilities."""
+        n = logits.shape[0]
+        return ops.moe_balance_loss(logits, self.topk_idx[:n], row_valid, out, dev_error=self.dev_error)
+
+    def route_backward(self, logits: torch.Tensor, d_topk_w: Optional[torch.Tensor],
+                       row_valid: Optional[torch.Tensor] = None,
+                       d_loss: Optional[torch.Tensor] = None,
+                       losses: Optional[ops.RouterLosses] = None,
+                       d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The gradient with respect to the logits of the routing weights in
+        ``topk_w`` and, with ``d_loss`` [2] and what ``balance_loss`` returned,
+        of the losses (``moe_route_backward``)."""
+        n = logits.shape[0]
+        return ops.moe_route_backward(
+            logits, self.topk_idx[:n], self.topk_w[:n], d_topk_w, row_valid, self.renormalize, d_loss,
+            None if losses is None else losses.counts,
+            None if losses is None else losses.num_tokens, d_logits, dev_error=self.dev_error)
+
     def calibrate_combine_scale(self, logits, hidden, row_valid=None) -> torch.Tensor:
         """One-time max calibration of the constant combine-row scale: run the
         layer without combine-row QDQ, take max|row| over the routed rows and
@@ -396,7 +461,7 @@ class MoELayer:
                  w_perm=p.w_perm, y_perm=self.y_perm, out=self.out)
         if self.hidden_q is not None:
             d["hidden_q"] = self.hidden_q
-        if self.w8a8:
+        if self.w8a8:   # (of rows that forward() was given: norm()'s are normed_q, normed_s)
             d["hidden_codes"], d["hidden_scales"] = self.hq, self.hs
         if self.shared_out is not None:
             d["shared"] = self.shared_out

@@ -786,14 +786,28 @@ def _output(want, shape, dtype: torch.dtype, like: torch.Tensor, stream, name: s
     if want is None or want is False:
         return None, None
     if want is True:
-        if stream is None:
-            t = torch.empty_like(like) if (dtype, shape) == (like.dtype, like.shape) else like.new_empty(shape, dtype=dtype)
-        else:
+        if stream is not None:
             t = _empty(shape, dtype, like.device, stream)
+        elif shape == like.shape:
+            t = torch.empty_like(like, dtype=dtype)
+        else:
+            t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     if want.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(want.shape)}")
     return want, _pointers(like.get_device(), (want, dtype, name))[0]
+
+
+def _scratch(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, size, *sizes):
+    """(tensor, device pointer, bytes) of a workspace: the caller's, or a new one
+    where the size query ``size(*sizes)`` says that the call needs any."""
+    if workspace is not None:
+        return workspace, _pointers(like.get_device(), (workspace, torch.uint8, "workspace"))[0], workspace.numel()
+    need = size(*sizes)
+    if need == 0:
+        return None, None, 0
+    t, p = _output(True, (need,), torch.uint8, like, stream, "workspace")
+    return t, p, need
 
 
 def _gain(weight: torch.Tensor, H: int):
@@ -875,19 +889,17 @@ def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         raise ValueError("rstd must be [T]")
     flags, wtype = _gain(weight, H)
     raw = _one_device(stream, dy)
-    pdy, ph, pi, pw, pd, pws = _pointers(
+    pdy, ph, pi, pw, pd = _pointers(
         dy.get_device(), (dy, torch.bfloat16, "dy"), (h, torch.bfloat16, "h"),
         (rstd, torch.float32, "rstd"), (weight, wtype, "weight"),
-        (d_residual, torch.bfloat16, "d_residual"), (workspace, torch.uint8, "workspace"))
+        (d_residual, torch.bfloat16, "d_residual"))
     lib = load()
     dx, px = _output(True if dx is None else dx, dy.shape, torch.bfloat16, dy, stream, "dx")
     d_weight, pdw = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy, stream,
                             "d_weight")
-    if workspace is None:
-        need = lib.moe_rmsnorm_backward_workspace_bytes(T, H)
-        workspace, pws = _output(True, (max(need, 1),), torch.uint8, dy, stream, "workspace")
+    workspace, pws, size = _scratch(workspace, dy, stream, lib.moe_rmsnorm_backward_workspace_bytes, T, H)
     check("moe_rmsnorm_backward", lib.moe_rmsnorm_backward(
-        pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, workspace.numel(), raw))
+        pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, size, raw))
     return dx, d_weight
 
 
@@ -985,16 +997,13 @@ def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeigh
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"y is bfloat16 or float32, not {out_dtype}")
     raw = _one_device(stream, x, weights.packed)
-    px, ps, pws = _pointers(x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"),
-                            (workspace, torch.uint8, "workspace"))
+    px, ps = _pointers(x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"))
     lib = load()
     y, py = _output(True if y is None else y, (M, N), out_dtype, x, stream, "y")
-    if workspace is None:
-        need = lib.moe_linear_fp8_workspace_bytes(M, N, K)
-        workspace, pws = _output(True, (max(need, 1),), torch.uint8, x, stream, "workspace")
+    workspace, pws, size = _scratch(workspace, x, stream, lib.moe_linear_fp8_workspace_bytes, M, N, K)
     check("moe_linear_fp8", lib.moe_linear_fp8(
         px, ps, x_scales.shape[1], M, N, K, weights.packed.data_ptr(), weights.scales.data_ptr(),
-        MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, workspace.numel(), raw))
+        MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, size, raw))
     return y
 
 
@@ -1035,21 +1044,18 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     T, E, K = _router_shapes(logits.shape, topk_idx, row_valid)
     raw = _one_device(stream, logits)
     f32, i32 = torch.float32, torch.int32
-    pl, pv, pi, pws, perr = _pointers(
+    pl, pv, pi, perr = _pointers(
         logits.get_device(), (logits, f32, "logits"), (row_valid, torch.uint8, "row_valid"),
-        (topk_idx, i32, "topk_idx"), (workspace, torch.uint8, "workspace"),
-        (dev_error, i32, "dev_error"))
+        (topk_idx, i32, "topk_idx"), (dev_error, i32, "dev_error"))
     lib = load()
     want = (True,) * 4 if out is None else (out.loss, out.counts, out.probs, out.num_tokens)
     loss, po = _output(want[0], (2,), f32, logits, stream, "loss")
     counts, pc = _output(want[1], (E,), i32, logits, stream, "counts")
     probs, pp = _output(want[2], (E,), f32, logits, stream, "probs")
     tokens, pn = _output(want[3], (1,), i32, logits, stream, "num_tokens")
-    if workspace is None:
-        need = lib.moe_balance_loss_workspace_bytes(T, E)
-        workspace, pws = _output(True, (max(need, 1),), torch.uint8, logits, stream, "workspace")
-    check("moe_balance_loss", lib.moe_balance_loss(pl, pv, pi, T, E, K, po, pc, pp, pn, pws,
-                                                   workspace.numel(), perr, raw))
+    workspace, pws, size = _scratch(workspace, logits, stream, lib.moe_balance_loss_workspace_bytes, T, E)
+    check("moe_balance_loss", lib.moe_balance_loss(pl, pv, pi, T, E, K, po, pc, pp, pn, pws, size, perr,
+                                                   raw))
     return RouterLosses(loss, counts, probs, tokens)
 
 

@@ -102,7 +102,10 @@ def test_sizes(lib):
     for T, H in ((1, 128), (10 ** 6, 2048), (10 ** 6, 8192), (10 ** 6, 32768)):
         assert 4 * H <= lib.moe_rmsnorm_backward_workspace_bytes(T, H) <= 4096 * 4 * H
     assert lib.moe_balance_loss_workspace_bytes(0, 64) == 0 and lib.moe_balance_loss_workspace_bytes(9, 2000) == 0
-    assert lib.moe_balance_loss_workspace_bytes(1, 64) >= 64 * 8 + 12
+    sizes = [lib.moe_balance_loss_workspace_bytes(T, 64) for T in (1, 64, 65, 1000, 10 ** 4, 10 ** 6)]
+    assert sizes[0] == 0 and sizes == sorted(sizes) and sizes[2] > 0 and sizes[-1] < 1 << 20
+    sizes = [lib.moe_linear_fp8_workspace_bytes(M, 576, 7168) for M in (1, 16, 17, 64, 500, 5000, 10 ** 6)]
+    assert sizes[1] == 0 and sizes == sorted(sizes) and sizes[-1] == 32 << 20    # one for all smaller batches
     assert lib.moe_linear_fp8_workspace_bytes(0, 128, 128) == 0 and lib.moe_linear_fp8_workspace_bytes(1, 1, 100) == 0
 
 
@@ -116,7 +119,7 @@ def _loss(lib, **kw):
     (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(K=0), INVALID), (dict(K=9), INVALID),
     (dict(E=2000), UNSUPPORTED), (dict(E=64, K=33), UNSUPPORTED), (dict(loss=None), INVALID), (dict(counts=None), INVALID),
     (dict(probs=None), INVALID), (dict(n=None), INVALID), (dict(logits=None), INVALID), (dict(idx=None), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(ws=P + 8), WORKSPACE), (dict(bytes=8), WORKSPACE),
+    (dict(T=4000, ws=None), WORKSPACE), (dict(T=4000, ws=P + 8), WORKSPACE), (dict(T=4000, bytes=8), WORKSPACE),
 ])
 def test_loss_refusals(lib, kw, status):
     assert _loss(lib, **kw) == status
