@@ -52,6 +52,7 @@ int launch_decode(const float*, const uint8_t*, const uint16_t*, int, int, int, 
                   uint16_t*, void*, int32_t*, hipStream_t);
 int launch_rmsnorm(const uint16_t*, const uint16_t*, const void*, int, int64_t, int, float,
                    uint16_t*, uint16_t*, uint8_t*, float*, int64_t, float*, hipStream_t);
+bool norm_one_launch(int64_t, const uint16_t*, const uint16_t*);
 size_t rmsnorm_backward_workspace_bytes(int64_t, int);
 int launch_rmsnorm_backward(const uint16_t*, const uint16_t*, const float*, const void*, int,
                             int64_t, int, const uint16_t*, uint16_t*, float*, void*, hipStream_t);
@@ -566,7 +567,7 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
   if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(d_residual) ||
       !aligned16(dx))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = rmsnorm_backward_workspace_bytes(T, H);
+  const size_t need = norm_one_launch(T, dy, dx) ? 0 : rmsnorm_backward_workspace_bytes(T, H);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
   return launch_rmsnorm_backward(dy, h, rstd, weight, flags & MOE_NORM_WEIGHT_F32, T, H, d_residual,

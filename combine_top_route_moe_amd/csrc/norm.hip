@@ -167,9 +167,64 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
   }
 }
 
-// One workgroup walks the rows blockIdx.x, blockIdx.x + gridDim.x, .. (in
-// groups of kRows) and keeps its share of dw in registers; `partial`
-// [gridDim.x, H] takes the shares, which norm_dw_kernel adds up in order.
+// A row's part in dx, and with kDw in the thread's sums of dw: what both forms of the
+// gradient do with it.
+template <int kWaves, int kVecs, bool kWF32, bool kDw>
+__device__ __forceinline__ void backward_row(const uint16_t* dy, const uint16_t* h, float r, const void* weight,
+                                             int64_t t, int nvec, int tid, int wave, const uint16_t* d_residual,
+                                             uint16_t* dx, float* part, float (&dw)[kVecs][8]) {
+  constexpr int kThreads = kWaves * kWave;
+  const uint4* dyr = reinterpret_cast<const uint4*>(dy) + t * nvec;
+  const uint4* hr = reinterpret_cast<const uint4*>(h) + t * nvec;
+  const uint4* dr = reinterpret_cast<const uint4*>(d_residual) + t * nvec;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 a[kVecs], b[kVecs], d[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = tid + i * kThreads;
+    const bool in = c < nvec;
+    a[i] = in ? load_row(dyr + c) : zero;
+    b[i] = in ? load_row(hr + c) : zero;
+    d[i] = in && d_residual ? load_row(dr + c) : zero;
+  }
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = tid + i * kThreads;
+    if (c >= nvec) break;
+    float g[8], f[8], w[8];
+    unpack8(a[i], g);
+    unpack8(b[i], f);
+    load_gain<kWF32>(weight, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float hat = f[j] * r;
+      if (kDw) dw[i][j] = __builtin_fmaf(g[j], hat, dw[i][j]);
+      dot = __builtin_fmaf(g[j] * w[j], hat, dot);
+    }
+  }
+  dot = row_sum<kWaves>(dot, part, wave) / (float)(nvec * 8);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = tid + i * kThreads;
+    if (c >= nvec) break;
+    float g[8], f[8], w[8], e[8];
+    unpack8(a[i], g);
+    unpack8(b[i], f);
+    unpack8(d[i], e);
+    load_gain<kWF32>(weight, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = r * __builtin_fmaf(-dot, f[j] * r, g[j] * w[j]);
+      g[j] = d_residual ? v + e[j] : v;
+    }
+    store_row(reinterpret_cast<uint4*>(dx) + t * nvec + c, to_bf16x8(g));
+  }
+}
+
+// Many rows: one workgroup walks the rows blockIdx.x, blockIdx.x + gridDim.x, .. (in
+// groups of kRows) and keeps its share of dw in registers; `partial` [gridDim.x, H]
+// takes the shares, which norm_dw_kernel adds up in order.
 template <int kWaves, int kVecs, bool kWF32>
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_kernel(
     const uint16_t* dy, const uint16_t* __restrict__ h, const float* __restrict__ rstd,
@@ -182,62 +237,16 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_ke
   const int wave = threadIdx.x >> 6;
   const int tid = kWaves == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int nvec = H / 8;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   float dw[kVecs][8];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  int flip = 0;
-  for (int64_t t = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); t < T; t += (int64_t)gridDim.x * kRows) {
-    const uint4* dyr = reinterpret_cast<const uint4*>(dy) + t * nvec;
-    const uint4* hr = reinterpret_cast<const uint4*>(h) + t * nvec;
-    const uint4* dr = reinterpret_cast<const uint4*>(d_residual) + t * nvec;
-    const float r = rstd[t];
-    uint4 a[kVecs], b[kVecs], d[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = tid + i * kThreads;
-      const bool in = c < nvec;
-      a[i] = in ? load_row(dyr + c) : zero;
-      b[i] = in ? load_row(hr + c) : zero;
-      d[i] = in && d_residual ? load_row(dr + c) : zero;
-    }
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = tid + i * kThreads;
-      if (c >= nvec) break;
-      float g[8], f[8], w[8];
-      unpack8(a[i], g);
-      unpack8(b[i], f);
-      load_gain<kWF32>(weight, c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float hat = f[j] * r;
-        dw[i][j] = __builtin_fmaf(g[j], hat, dw[i][j]);
-        dot = __builtin_fmaf(g[j] * w[j], hat, dot);
-      }
-    }
-    dot = row_sum<kWaves>(dot, part[flip], wave) / (float)H;
-    flip ^= 1;                          // the next row's sums go to the other buffer: one barrier a row
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = tid + i * kThreads;
-      if (c >= nvec) break;
-      float g[8], f[8], w[8], e[8];
-      unpack8(a[i], g);
-      unpack8(b[i], f);
-      unpack8(d[i], e);
-      load_gain<kWF32>(weight, c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = r * __builtin_fmaf(-dot, f[j] * r, g[j] * w[j]);
-        g[j] = d_residual ? v + e[j] : v;
-      }
-      store_row(reinterpret_cast<uint4*>(dx) + t * nvec + c, to_bf16x8(g));
-    }
-  }
+  int flip = 0;                         // the next row's sums go to the other buffer: one barrier a row
+  for (int64_t t = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); t < T;
+       t += (int64_t)gridDim.x * kRows, flip ^= 1)
+    backward_row<kWaves, kVecs, kWF32, true>(dy, h, rstd[t], weight, t, nvec, tid, wave, d_residual, dx, part[flip],
+                                             dw);
   float* out = partial + (int64_t)blockIdx.x * H;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -262,6 +271,53 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_ke
       reinterpret_cast<float4*>(out)[2 * c + 1] = hi;
     }
   }
+}
+
+// Few rows, in one launch: the first `row_blocks` workgroups write dx, the others dw,
+// 64 channels each over all rows: they read dy and h again, from the caches, and
+// need no row's sum (r is given).  dx must not be dy here.
+template <int kWaves, int kVecs, bool kWF32>
+__global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_few_kernel(
+    const uint16_t* dy, const uint16_t* __restrict__ h, const float* __restrict__ rstd,
+    const void* __restrict__ weight, int T, int H, const uint16_t* d_residual, uint16_t* dx,
+    float* __restrict__ d_weight, int row_blocks) {
+  constexpr int kRows = kWaves == 1 ? 4 : 1;
+  constexpr int kSlices = (kWaves == 16 ? 1024 : 256) / 8;
+  __shared__ float part[kWaves];
+  __shared__ float sums[kSlices][64];
+  const int nvec = H / 8;
+  if ((int)blockIdx.x < row_blocks) {
+    const int wave = threadIdx.x >> 6;
+    const int t = blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
+    if (t >= T) return;
+    float none[kVecs][8];
+    backward_row<kWaves, kVecs, kWF32, false>(dy, h, rstd[t], weight, t, nvec,
+                                              kWaves == 1 ? threadIdx.x & 63 : threadIdx.x, wave, d_residual, dx,
+                                              part, none);
+    return;
+  }
+  const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int c = ((int)blockIdx.x - row_blocks) * 8 + col;
+  const uint4* dyc = reinterpret_cast<const uint4*>(dy) + c;
+  const uint4* hc = reinterpret_cast<const uint4*>(h) + c;
+  float dw[8] = {};
+#pragma unroll 4
+  for (int t = slice; t < T; t += kSlices) {
+    float g[8], f[8];
+    unpack8(dyc[(int64_t)t * nvec], g);
+    unpack8(hc[(int64_t)t * nvec], f);
+    const float r = rstd[t];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(g[j], f[j] * r, dw[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[slice][8 * col + j] = dw[j];
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < kSlices; ++i) s += sums[i][threadIdx.x];
+  d_weight[((int)blockIdx.x - row_blocks) * 64 + threadIdx.x] = s;
 }
 
 // dw[c] = sum over the n shares, four channels a thread, 32 threads along the
@@ -336,6 +392,13 @@ static int64_t norm_shares(int64_t T, int H) {
   return rows < most ? rows : most;
 }
 
+// One launch for few rows; one launch against two, us: 333 x 2048 4.5 and 9.2, 1024 x
+// 512 5.6 and 6.3, 1024 x 2048 6.9 and 9.5, 1024 x 7168 19 and 27, 1024 x 16384 39
+// and 36, 2048 x 512 8.6 and 7.4, 2048 x 4096 27 and 24.
+bool norm_one_launch(int64_t T, const uint16_t* dy, const uint16_t* dx) {
+  return T > 0 && T <= MOE_NORM_FEW_ROWS && dx != dy;
+}
+
 size_t rmsnorm_backward_workspace_bytes(int64_t T, int H) {
   return (size_t)norm_shares(T, H) * H * sizeof(float);
 }
@@ -344,6 +407,20 @@ int launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* 
                             const void* weight, int wf32, int64_t T, int H,
                             const uint16_t* d_residual, uint16_t* dx, float* dw, void* workspace,
                             hipStream_t stream) {
+  if (norm_one_launch(T, dy, dx)) {
+    norm_form(H, [&](auto waves, auto vecs) {
+      constexpr int W = decltype(waves)::value, V = decltype(vecs)::value;
+      const int rows = (int)(W == 1 ? (T + 3) / 4 : T);
+      const dim3 grid(rows + H / 64), block(W == 16 ? 1024 : 256);
+      if (wf32)
+        hipLaunchKernelGGL((rmsnorm_backward_few_kernel<W, V, true>), grid, block, 0, stream, dy, h, rstd, weight,
+                           (int)T, H, d_residual, dx, dw, rows);
+      else
+        hipLaunchKernelGGL((rmsnorm_backward_few_kernel<W, V, false>), grid, block, 0, stream, dy, h, rstd, weight,
+                           (int)T, H, d_residual, dx, dw, rows);
+    });
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  }
   const int shares = (int)norm_shares(T, H);
   float* partial = static_cast<float*>(workspace);
   if (shares)

@@ -27,6 +27,7 @@ MOE_FP8_LAYOUT_K128 = 1
 MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4, MOE_W_NVFP4 = 0, 1, 2, 3
 MOE_DECODE_MAX_TOKENS = 64
 MOE_NORM_WEIGHT_F32 = 1
+MOE_NORM_FEW_ROWS = 1024
 MOE_LINEAR_TRANSPOSE, MOE_LINEAR_OUT_F32 = 1, 2
 
 
@@ -897,7 +898,9 @@ def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     dx, px = _output(True if dx is None else dx, dy.shape, torch.bfloat16, dy, stream, "dx")
     d_weight, pdw = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy, stream,
                             "d_weight")
-    workspace, pws, size = _scratch(workspace, dy, stream, lib.moe_rmsnorm_backward_workspace_bytes, T, H)
+    pws, size = None, 0
+    if T > MOE_NORM_FEW_ROWS or px == pdy:
+        workspace, pws, size = _scratch(workspace, dy, stream, lib.moe_rmsnorm_backward_workspace_bytes, T, H)
     check("moe_rmsnorm_backward", lib.moe_rmsnorm_backward(
         pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, size, raw))
     return dx, d_weight

@@ -87,6 +87,7 @@ enum { MOE_W_BF16 = 0,                /* expert-weight formats: bf16, packed  */
        MOE_W_NVFP4 = 3 };             /* E2M1 codes, E4M3 scales of 16        */
 
 enum { MOE_NORM_WEIGHT_F32 = 1 };     /* moe_rmsnorm: a float32 gain, not bf16 */
+enum { MOE_NORM_FEW_ROWS = 1024 };    /* moe_rmsnorm_backward without workspace */
 enum { MOE_LINEAR_TRANSPOSE = 1,      /* moe_pack_linear_fp8: pack W^T        */
        MOE_LINEAR_OUT_F32 = 2 };      /* moe_linear_fp8: y in float32         */
 

@@ -48,8 +48,9 @@ def _norm_back(lib, **kw):
     (dict(T=-1), INVALID), (dict(flags=4), INVALID), (dict(H=100), UNSUPPORTED), (dict(T=1 << 40), UNSUPPORTED),
     (dict(dw=None), INVALID), (dict(dw=P + 4), INVALID), (dict(dy=None), INVALID), (dict(h=None), INVALID),
     (dict(rstd=None), INVALID), (dict(w=None), INVALID), (dict(dx=None), INVALID), (dict(dx=2 * P), INVALID),
-    (dict(dy=P + 2), INVALID), (dict(dres=P + 2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=P + 8), WORKSPACE),
-    (dict(bytes=256 * 4 - 1), WORKSPACE), (dict(dx=2 * P, ws=None), INVALID),
+    (dict(dy=P + 2), INVALID), (dict(dres=P + 2), INVALID), (dict(T=2000, ws=None), WORKSPACE),
+    (dict(T=2000, ws=P + 8), WORKSPACE), (dict(T=2000, bytes=256 * 4 - 1), WORKSPACE), (dict(dx=2 * P, ws=None), INVALID),
+    (dict(dx=P, ws=None), WORKSPACE),                                # in place: never without
 ])
 def test_norm_gradient_refusals(lib, kw, status):
     assert _norm_back(lib, **kw) == status
