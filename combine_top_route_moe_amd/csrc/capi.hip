@@ -121,7 +121,7 @@ const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size or bad flag)";
-    case MOE_ERR_UNSUPPORTED: return "unsupported shape (H and I must be multiples of 128; E, G <= 1024; K <= 32; moe_decode: T <= 64)";
+    case MOE_ERR_UNSUPPORTED: return "unsupported shape (H and I must be multiples of 128; E, G <= 1024; K <= 32; moe_decode: T <= 64; moe_rmsnorm: H <= 32768)";
     case MOE_ERR_WORKSPACE: return "workspace smaller than the size query requires";
     case MOE_ERR_HIP: return "HIP runtime error or kernel launch failure";
     case MOE_ERR_DEVICE: return "the current device is not a gfx950 (MI355X-class) GPU";

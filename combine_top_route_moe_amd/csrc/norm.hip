@@ -80,7 +80,9 @@ __device__ __forceinline__ uint4 to_bf16x8(const float* v) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A workgroup of 4 waves (16 for the longest rows) holds 4 / kWaves rows.
+// A workgroup of 4 waves (16 for the longest rows) holds 4 / kWaves rows.  4096 x 7168
+// with the residual, bf16 rows and codes 48 us, 5.6 TB/s; 16384 x 4096 without the
+// bf16 rows 76 us, 6.2 TB/s (a copy of 1 GiB: 5.85).
 // x, residual and h may be one buffer: a thread stores what it has read.
 template <int kWaves, int kVecs, bool kWF32>
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
@@ -224,7 +226,7 @@ __device__ __forceinline__ void backward_row(const uint16_t* dy, const uint16_t*
 
 // Many rows: one workgroup walks the rows blockIdx.x, blockIdx.x + gridDim.x, .. (in
 // groups of kRows) and keeps its share of dw in registers; `partial` [gridDim.x, H]
-// takes the shares, which norm_dw_kernel adds up in order.
+// takes the shares, which norm_dw_kernel adds up in order.  16384 x 4096 98 + 5 us.
 template <int kWaves, int kVecs, bool kWF32>
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_kernel(
     const uint16_t* dy, const uint16_t* __restrict__ h, const float* __restrict__ rstd,

@@ -218,3 +218,34 @@ def test_the_norm_feeds_the_product():
     s = v.reshape(T, -1, 128).abs().amax(2).repeat_interleave(128, 1) / 448
     off = torch.maximum(v.abs() * 2.0 ** -4, s * 2.0 ** -10) * 1.001
     within(y, v @ W.t(), (off @ W.abs().t() + product_slack(v, W)) * (1 + BF16) + BF16 * (v @ W.t()).abs() + 1e-5)
+
+
+def _random_codes(*shape):
+    """E4M3 codes without NaN, made on the GPU."""
+    return torch.randint(0, 0x70, shape, dtype=torch.uint8, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+
+
+def test_rows_past_32_bits():
+    """4.4e9 codes of x: the last rows against the same rows alone (bit for bit: both
+    calls take the same tiles)."""
+    M, N, K = 1_100_000, 130, 4096
+    x, xs = _random_codes(M, K), torch.ones(K // 128, M, device="cuda")
+    _, _, wq, ws = _case(1, N, K)
+    weights = ops.linear_weights_from_codes(wq.cuda(), ws.cuda())
+    y = ops.moe_linear_fp8(x, xs, weights)
+    tail = x[-5:].contiguous()
+    check(y[-5:], tail.cpu(), torch.ones(K // 128, 5), wq, ws)
+    check(y[:5], x[:5].cpu(), torch.ones(K // 128, 5), wq, ws)
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_weights_past_32_bits(M):
+    """4.5e9 codes of W: its last rows."""
+    N, K = 1 << 20, 4352
+    codes, scales = _random_codes(N, K), torch.rand(N // 128, K // 128, device="cuda") + 0.5
+    weights = ops.linear_weights_from_codes(codes, scales)
+    xq, xs, _, _ = _case(M, 16, K)
+    y = ops.moe_linear_fp8(xq.cuda(), xs.cuda(), weights)
+    last = slice(N - 128, N)
+    check(y[:, last], xq, xs, codes[last].cpu(), scales[-1:].cpu())
+    check(y[:, :128], xq, xs, codes[:128].cpu(), scales[:1].cpu())

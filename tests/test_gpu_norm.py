@@ -249,3 +249,19 @@ def test_on_another_stream():
     for a, b in ((out.y, here.y), (out.codes, here.codes), (out.scales, here.scales), (dx, hx), (dw, hw)):
         assert torch.equal(a, b)
     assert float(e4m3(out.codes).abs().max()) == 448
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 channels: the last rows, forward and backward, against the same rows alone."""
+    T, H = 270_000, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.ones(H, device="cuda")
+    out = ops.moe_rmsnorm(x, w, EPS, y=False, codes=True, rstd=True)
+    some = ops.moe_rmsnorm(x[-3:].contiguous(), w, EPS, codes=True, rstd=True)
+    assert torch.equal(out.codes[-3:], some.codes) and torch.equal(out.scales[:, -3:], some.scales)
+    assert torch.equal(out.rstd[-3:], some.rstd)
+    del out.codes
+    dx, dw = ops.moe_rmsnorm_backward(x, x, out.rstd, w)
+    few, _ = ops.moe_rmsnorm_backward(x[-3:].contiguous(), x[-3:].contiguous(), some.rstd, w)
+    assert torch.equal(dx[-3:], few) and torch.isfinite(dw).all()

@@ -261,3 +261,20 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(other, call()))
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 logits: the counts of all, and the gradient of the last tokens."""
+    T, E = 2_200_000, 1024
+    logits = torch.zeros(T, E, device="cuda")
+    logits[-4:] = torch.randn(4, E, generator=gen(1)).cuda()
+    idx = torch.full((T, 1), 3, dtype=torch.int32, device="cuda")
+    idx[-1] = 1023
+    r = ops.moe_balance_loss(logits, idx)
+    assert int(r.num_tokens) == T and int(r.counts[3]) == T - 1 and int(r.counts[1023]) == 1
+    d = torch.tensor([float(T), float(T)], device="cuda")
+    g = ops.moe_route_backward(logits, idx, torch.ones(T, 1, device="cuda"), None, d_loss=d, counts=r.counts,
+                               num_tokens=r.num_tokens)
+    want, bound = _gradient64(logits[-4:].cpu(), None, idx[-4:].cpu(), None, None, True, d.cpu(), r.counts.cpu(), T)
+    # (the routing has one slot: K of the formula is idx's)
+    within(g[-4:], want, bound)
