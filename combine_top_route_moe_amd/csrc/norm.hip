@@ -3,11 +3,12 @@
 //
 // Forward, per row of H channels (float32 between the two roundings):
 //   h = bf16(x + residual)                       (x itself without a residual)
-//   r = 1 / sqrt(sum(h^2) / H + eps),  v = (h r) w
+//   r = 1 / sqrt(sum(h^2) / H + eps),  p = h w,  v = p r
 //   y = bf16(v);  per 128 channels s = amax |v| / 448, code = e4m3(v / s)
 // h is rounded before it is normed because that rounded value is what the
 // stream keeps: the gradient, which starts from the stored h, is then exactly
-// the forward's.  The codes come from v and not from y: one rounding less.
+// the forward's.  p is exact for a bf16 w.  The codes come from the unrounded row,
+// as 448 p / amax |p|: r falls out of the quotient.
 //
 // Gradient, with hat = h r and g = dy w:
 //   dh = r (g - hat sum(g hat) / H) (+ the stream's own gradient),
@@ -138,29 +139,43 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
     const int c = tid + i * kThreads;
     if (c >= nvec) break;               // (all 16 lanes of a block together: nvec % 16 == 0)
     if (h_out) store_row(reinterpret_cast<uint4*>(h_out) + t * nvec + c, hv[i]);
-    float v[8], w[8];
-    unpack8(hv[i], v);
+    float p[8], w[8];
+    unpack8(hv[i], p);
     load_gain<kWF32>(weight, c, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
-    if (y) store_row(reinterpret_cast<uint4*>(y) + t * nvec + c, to_bf16x8(v));
+    for (int j = 0; j < 8; ++j) p[j] *= w[j];
+    if (y) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[j] * r;
+      store_row(reinterpret_cast<uint4*>(y) + t * nvec + c, to_bf16x8(v));
+    }
     if (codes) {
-      // |v| compared as integers: the order of the magnitudes, a NaN above all,
+      // |p| compared as integers: the order of the magnitudes, a NaN above all,
       // so that a block with a NaN gets a NaN scale instead of losing it
       uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-      m = row16_max_u32(m);
-      const float s = __uint_as_float(m) / 448.0f;
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(p[j]) & 0x7fffffffu);
+      const float top = __uint_as_float(row16_max_u32(m));
+      const float s = top * r / 448.0f;
       uint2 q = make_uint2(0, 0);
       if (!(s <= 0.0f)) {
-        // the quotient by the reciprocal: one more rounding (2^-24) before that to
-        // 3 bits; scales whose reciprocal leaves the range divide
-        const float inv = 1.0f / s;
+        const float inv = 448.0f / top, inv_top = inv * (1.0f / 448.0f);
+        if (top >= 0x1p-90f) {
+          // 448 p / top from the quotient's reciprocal, put right by its residual: off
+          // by half a step of float32 before the rounding to 3 bits
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = __builtin_amdgcn_fmed3f(rcp_scale_ok(s) ? v[j] * inv : v[j] / s, -448.0f, 448.0f);
-        q = e4m3x8(v);
+          for (int j = 0; j < 8; ++j) {
+            const float u = p[j] * inv;
+            p[j] = __builtin_fmaf(-__builtin_fmaf(u, top, -448.0f * p[j]), inv_top, u);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = p[j] / top * 448.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_fmed3f(p[j], -448.0f, 448.0f);
+        q = e4m3x8(p);
         if (s != s) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
       }
       reinterpret_cast<uint2*>(codes)[t * nvec + c] = q;

@@ -582,12 +582,13 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
 /* ---- norm of the residual stream, with codes ------------------------------
  * In front of the layer, per row t of H channels (float32 between roundings):
  *   h = bf16(x + residual), x itself without a residual
- *   r = 1 / sqrt(sum(h^2) / H + eps),   v = (h r) weight
+ *   r = 1 / sqrt(sum(h^2) / H + eps),   v = (h weight) r
  *   y = bf16(v)                                                  (the router's rows)
  *   s = fl32(amax |v| / 448) per 128 channels, codes = e4m3(v / s)  (the experts')
  * h is rounded before it is normed: it is what the stream keeps and what the
- * gradient starts from.  The codes are those of v, not of the rounded y; the
- * quotient is taken through float32, to nearest even, saturating at 448.
+ * gradient starts from.  The codes are those of v, not of the rounded y; v / s is
+ * taken as the float32 nearest to 448 (h weight) / amax |h weight|, its code to
+ * nearest even.
  *   x [T, H] bf16;  residual [T, H] bf16 or NULL;  weight [H] bf16, or float32
  *   with MOE_NORM_WEIGHT_F32;  outputs, each may be NULL but not all: h [T, H]
  *   bf16;  y [T, H] bf16;  codes [T, H] uint8 with scales [H/128, scale_stride]
