@@ -530,8 +530,9 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
                               dev_error, as_stream(stream));
 }
 
+// (a workgroup of 256 threads for 4 rows, for one, or of 1024 for one: below 2^32 threads)
 static bool norm_size_ok(int64_t T, int H) {
-  return H % 128 == 0 && H <= 32768 && T <= (H <= 2048 ? 1 << 26 : H <= 8192 ? 1 << 24 : 1 << 22);
+  return H % 128 == 0 && H <= 32768 && T < (H <= 2048 ? (1 << 26) - 3 : H <= 8192 ? 1 << 24 : 1 << 22);
 }
 
 int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,

@@ -418,28 +418,31 @@ __global__ void __launch_bounds__(512, 2) linear_big_kernel(
   store_tile<F32, kIN, kIM>(y, acc, m0 + wm * 16, (ct0 + wn) * 16, M, N, lane);
 }
 
-// y = the sum of the parts, in order, four outputs a thread.
-template <bool F32>
-__global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ parts, int n_parts,
-                                                          int64_t total, void* __restrict__ y) {
+// y = the sum of the parts, in order, four outputs a thread, all parts' loads on
+// their way before the first addition.
+template <int kParts, bool F32>
+__global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ parts, int64_t total,
+                                                          void* __restrict__ y) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (at >= total) return;
-  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
   const int some = (int)min((int64_t)4, total - at);
   const bool wide = (total & 3) == 0;
-  for (int p = 0; p < n_parts; ++p) {
+  f32x4_t u[kParts];
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
     const float* q = parts + p * total + at;
     if (wide) {
-      const f32x4_t u = *reinterpret_cast<const f32x4_t*>(q);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] += u[k];
+      u[p] = *reinterpret_cast<const f32x4_t*>(q);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < some) s[k] += q[k];
+      for (int k = 0; k < 4; ++k) u[p][k] = q[min(k, some - 1)];
     }
   }
-  store4<F32>(y, at, s, some, wide);
+#pragma unroll
+  for (int p = 1; p < kParts; ++p)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[0][k] += u[p][k];
+  store4<F32>(y, at, u[0], some, wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -543,34 +546,37 @@ int launch_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float*
 //   64 x 128                    0.40                   0.345
 //   128 x 128                   0.72                   0.55
 //   256 x 256                   1.4                    1.76
-// and for parts the join's launch and its bytes.  Both sides of a border, us: 64 x
-// 4096 x 7168 in 64 x 64 tiles 18.4, in 2 parts 14.5, in 4 12.0, in 8 14.4; 512 x
-// 4096 x 7168 in 64 x 64 28, 64 x 128 29, 128 x 128 43; 1024 x 4096 x 7168 57, 42,
-// 44; 2048 x 4096 x 7168 103, 82, 65, 256 x 256 84; 4096 x 4096 x 7168 211, 166,
+// and for parts the join's launch and its bytes.  Over 230 products of 17 to 8192
+// rows, N from 64 to 8192 and K from 256 to 8192 the form it takes is 1.4 % slower
+// in the geometric mean than the fastest of all eleven.  Both sides of a border, us:
+// 64 x 4096 x 7168 in 64 x 64 tiles 18.4, in 2 parts 14.5, in 4 12.0, in 8 14.4;
+// 512 x 4096 x 7168 in 64 x 64 28, 64 x 128 29, 128 x 128 43; 1024 x 4096 x 7168 57,
+// 42, 44; 2048 x 4096 x 7168 103, 82, 65, 256 x 256 84; 4096 x 4096 x 7168 211, 166,
 // 132, 119.
 struct LinearForm {
   int tile, parts;              // of kTiles; parts of K
 };
 
 struct LinearTile {
-  int m, n;
+  int m, n, threads;
   double one, many;
 };
-constexpr LinearTile kTiles[4] = {{64, 64, 0.28, 0.225}, {64, 128, 0.40, 0.345}, {128, 128, 0.72, 0.55},
-                                  {256, 256, 1.4, 1.76}};
+constexpr LinearTile kTiles[4] = {{64, 64, 256, 0.28, 0.225}, {64, 128, 512, 0.40, 0.345},
+                                  {128, 128, 256, 0.72, 0.55}, {256, 256, 512, 1.4, 1.76}};
+constexpr double kThreadsMost = 0xffffffffu;       // of a launch
 constexpr int kRowsMost = 16;                      // of linear_rows_kernel
-constexpr int kPartsMost = 8;
+constexpr int kPartsMost = 8;                      // 2, 4 or 8 (linear_join_kernel)
 constexpr int64_t kPartBytes = 32 << 20;           // all parts together: more costs more than it gives
 
 static LinearForm linear_form(int64_t M, int N, int nkb) {
   constexpr double kCUs = 256, kStart = 3.0, kJoin = 3.3, kJoinBytesPerUs = 5e6;
-  LinearForm best = {0, 1};
+  LinearForm best = {3, 1};
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
     const double tiles = (double)((M + kTiles[i].m - 1) / kTiles[i].m) * ((N + kTiles[i].n - 1) / kTiles[i].n);
     for (int parts = 1; parts <= (i < 3 ? kPartsMost : 1) && parts <= nkb; parts *= 2) {
       const int64_t bytes = (int64_t)parts * M * N * 4;
-      if (parts > 1 && bytes > kPartBytes) break;
+      if ((parts > 1 && bytes > kPartBytes) || tiles * parts * kTiles[i].threads > kThreadsMost) break;
       const double rounds = std::ceil(tiles * parts / kCUs);
       double us = kStart + (double)nkb / parts * std::max(kTiles[i].one, rounds * kTiles[i].many);
       if (parts > 1) us += kJoin + 2.0 * bytes / kJoinBytesPerUs;
@@ -616,8 +622,14 @@ static int launch_linear_tiles(const LinearCall& c, int parts) {
     hipLaunchKernelGGL((linear_tile_kernel<BM, BN, WM, WN, kStages, MINW, true, true>), grid, dim3(kThreads), 0,
                        c.stream, c.x, c.xs, c.sstride, c.M, c.wq, c.wsc, c.N, c.nkb, (int)tm, (int)tn, c.parts);
     const int64_t total = c.M * c.N;
-    hipLaunchKernelGGL(linear_join_kernel<F32>, dim3((unsigned)((total + 1023) / 1024)), dim3(256), 0, c.stream,
-                       static_cast<const float*>(c.parts), parts, total, c.y);
+    const dim3 blocks((unsigned)((total + 1023) / 1024));
+    const float* from = static_cast<const float*>(c.parts);
+    if (parts == 2)
+      hipLaunchKernelGGL((linear_join_kernel<2, F32>), blocks, dim3(256), 0, c.stream, from, total, c.y);
+    else if (parts == 4)
+      hipLaunchKernelGGL((linear_join_kernel<4, F32>), blocks, dim3(256), 0, c.stream, from, total, c.y);
+    else
+      hipLaunchKernelGGL((linear_join_kernel<8, F32>), blocks, dim3(256), 0, c.stream, from, total, c.y);
   } else {
     hipLaunchKernelGGL((linear_tile_kernel<BM, BN, WM, WN, kStages, MINW, F32, false>), grid, dim3(kThreads), 0,
                        c.stream, c.x, c.xs, c.sstride, c.M, c.wq, c.wsc, c.N, c.nkb, (int)tm, (int)tn, c.y);

@@ -597,8 +597,8 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
  * h may be x's or residual's buffer and y may be x's.  An all-zero block gets
  * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) must be within
  * float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd, scales: 4).
- * Requires H % 128 == 0, H <= 32768, eps > 0 and finite; sizes that need more
- * than 2^32 threads are refused (T <= 2^26 at H <= 2048, 2^24 to 8192, else 2^22). */
+ * Requires H % 128 == 0, H <= 32768, eps > 0 and finite; sizes that need 2^32
+ * threads are refused (T < 2^26 - 3 up to H = 2048, 2^24 up to 8192, else 2^22). */
 int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,
                 float eps, int flags, uint16_t* h, uint16_t* y, uint8_t* codes, float* scales,
                 int64_t scale_stride, float* rstd, void* stream);
