@@ -608,7 +608,7 @@ int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride
   if (K % 128 || N > kLinearMost || K > kLinearMost || M > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!x || !x_scales || !packed || !packed_scales || !y) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(packed) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || y == x) return MOE_ERR_INVALID_ARG;
   const size_t need = linear_fp8_workspace_bytes(M, N, K);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
@@ -642,7 +642,7 @@ int moe_route_backward(const float* logits, const uint8_t* row_valid, const int3
   if (T < 0 || E < 1 || K < 1 || K > E || (flags & ~MOE_ROUTE_RENORM)) return MOE_ERR_INVALID_ARG;
   if (K > 32 || E > 1024) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
-  if (!d_logits || (!d_topk_w && !d_loss)) return MOE_ERR_INVALID_ARG;
+  if (!d_logits || d_logits == logits || (!d_topk_w && !d_loss)) return MOE_ERR_INVALID_ARG;
   if (d_topk_w && (!topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
   if (d_loss && (!counts || !num_tokens)) return MOE_ERR_INVALID_ARG;
   if (!logits && (d_loss || !(flags & MOE_ROUTE_RENORM))) return MOE_ERR_INVALID_ARG;

@@ -453,13 +453,13 @@ __global__ void __launch_bounds__(256) pack_linear_kernel(
     const uint16_t* __restrict__ wide, const uint8_t* __restrict__ codes, const float* __restrict__ scales,
     int N, int K, uint8_t* __restrict__ packed, float* __restrict__ packed_scales) {
   __shared__ __attribute__((aligned(16))) uint8_t tile[128][144];
-  __shared__ float top[4];
+  __shared__ uint32_t top[4];
   const int nb = blockIdx.y, kb = blockIdx.x, n_nb = gridDim.y, n_kb = gridDim.x;
   const int64_t row0 = (int64_t)nb * 128;
   float s;
   if (QUANT) {
     uint4 v[8];
-    float m = 0.0f;
+    uint32_t m = 0;                     // |w| as integers: the order of the magnitudes, a NaN above all
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = threadIdx.x + 256 * i, r = c >> 4;
@@ -468,12 +468,15 @@ __global__ void __launch_bounds__(256) pack_linear_kernel(
       float f[8];
       unpack8(v[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
     }
-    m = wave_top_f32(m);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, kWave));
     if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
     __syncthreads();
-    s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) / 448.0f;
+    m = max(max(top[0], top[1]), max(top[2], top[3]));
+    const bool finite = m < 0x7f800000u;         // else no scale: the tile is NaN, not some finite number
+    s = finite ? __uint_as_float(m) / 448.0f : __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = threadIdx.x + 256 * i;
@@ -481,7 +484,8 @@ __global__ void __launch_bounds__(256) pack_linear_kernel(
       unpack8(v[i], f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = s > 0.0f ? fminf(fmaxf(f[j] / s, -448.0f), 448.0f) : 0.0f;
-      *reinterpret_cast<uint2*>(&tile[c >> 4][8 * (c & 15)]) = e4m3x8(f);
+      *reinterpret_cast<uint2*>(&tile[c >> 4][8 * (c & 15)]) =
+          finite ? e4m3x8(f) : make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
     }
   } else {
     s = scales[(int64_t)nb * n_kb + kb];

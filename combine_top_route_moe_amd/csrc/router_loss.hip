@@ -15,8 +15,8 @@
 // One wave per token, expert lane + 64 j in register j: a token's logits are
 // read once, maximum, sum and products stay in registers.  Bound by vector
 // instructions on many tokens (16384 of 128 experts: losses 6.8 + 5.6 us, gradient
-// 10.4; their bytes alone would take 1.3 and 3.2), by the launch on few.  Counts are integers and every float sum has a fixed order, so equal
-// calls give equal bits.
+// 10.4; their bytes alone would take 1.3 and 3.2), by the launch on few.  Counts are
+// integers and every float sum has a fixed order, so equal calls give equal bits.
 #include <algorithm>
 
 #include "reduce.h"

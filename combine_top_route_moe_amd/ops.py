@@ -811,8 +811,15 @@ def _scratch(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, size
     return t, p, need
 
 
+def _int32(*sizes: int) -> None:
+    """Refuses what the C interface would take modulo 2^32."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _gain(weight: torch.Tensor, H: int):
     """(flags, dtype) of a norm's weight [H]."""
+    _int32(H)
     if tuple(weight.shape) != (H,):
         raise ValueError(f"weight: expected shape ({H},), got {tuple(weight.shape)}")
     if weight.dtype == torch.float32:
@@ -869,6 +876,7 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 
 def moe_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
+    _int32(H)
     return load().moe_rmsnorm_backward_workspace_bytes(T, H)
 
 
@@ -929,6 +937,7 @@ class LinearWeights:
 
 
 def moe_linear_fp8_packed_bytes(N: int, K: int) -> int:
+    _int32(N, K)
     return load().moe_linear_fp8_packed_bytes(N, K)
 
 
@@ -975,6 +984,7 @@ def linear_weights_from_codes(codes: torch.Tensor, scales: torch.Tensor, transpo
 
 
 def moe_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    _int32(N, K)
     return load().moe_linear_fp8_workspace_bytes(M, N, K)
 
 
@@ -1021,11 +1031,13 @@ class RouterLosses:
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
+    _int32(T, E)
     return load().moe_balance_loss_workspace_bytes(T, E)
 
 
 def _router_shapes(logits_shape, topk_idx, row_valid, *slots):
     T, E = logits_shape
+    _int32(T, E)
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError("topk_idx must be [T, K]")
     for t in slots:

@@ -611,7 +611,8 @@ int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight,
  * none) that of the h that went on down the stream.
  *   dy, h [T, H] bf16;  rstd [T] float32;  weight as above;  dx [T, H] bf16,
  *   which may be dy's or d_residual's buffer;  d_weight [H] float32 (written, not
- *   added to).  T = 0 writes zeros to d_weight.  Requires as moe_rmsnorm. */
+ *   added to).  T = 0 writes zeros to d_weight.  Up to MOE_NORM_FEW_ROWS rows the
+ *   workspace may be NULL unless dx is dy's buffer.  Requires as moe_rmsnorm. */
 size_t moe_rmsnorm_backward_workspace_bytes(int64_t T, int H);
 int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,
                          const void* weight, int64_t T, int H, int flags,
@@ -629,7 +630,7 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *
  * moe_pack_linear_fp8 lays W [N, K] out once: from bf16 (`w`, quantized per 128 x
  * 128 tile as moe_pack_ffn_weights_fp8 does; a tile at the edge from the rows it
- * has), or from codes [N, K] and scales [ceil(N/128), K/128] that exist already
+ * has; one with an infinity or NaN gets a NaN scale and NaN codes), or from codes [N, K] and scales [ceil(N/128), K/128] that exist already
  * (a checkpoint), unchanged; the other pointers are NULL.
  *   packed: moe_linear_fp8_packed_bytes(N, K) bytes; the 16 x 128 tile of rows
  *     16 i .. and block b at unit (i * (K/128) + b) * 128 of 16 bytes, in it
@@ -644,7 +645,8 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *
  *   x [M, K] uint8 and x_scales [K/128, scale_stride] float32 (scale_stride >= M)
  *   from moe_quant_rows_fp8 or moe_rmsnorm;  y [M, N] bf16, or float32 with
- *   MOE_LINEAR_OUT_F32;  the workspace may be NULL where the query says 0.
+ *   MOE_LINEAR_OUT_F32, not x's buffer;  the workspace may be NULL where the query
+ *   says 0.
  * A row's result depends on that row alone (a NaN stays in its row); equal calls
  * give equal bits, but a row's bits may differ with M.  M = 0 enqueues nothing.
  * Requires M < 2^31, K % 128 == 0, N and K <= 2^20; sizes that need more than 2^32
@@ -688,7 +690,8 @@ int moe_balance_loss(const float* logits, const uint8_t* row_valid, const int32_
  *   d_topk_w [T, K] float32 or NULL (then topk_idx and topk_w are not read);
  *   d_loss [2] float32 or NULL (then counts and num_tokens are not read); one of
  *   the two is needed.  logits may be NULL where no softmax over all experts is
- *   needed (d_loss NULL, MOE_ROUTE_RENORM).  d_logits [T, E] float32 (out).
+ *   needed (d_loss NULL, MOE_ROUTE_RENORM).  d_logits [T, E] float32 (out), not
+ *   logits' buffer.
  * Tokens with row_valid[t] == 0 get zeros.  An empty slot (id < 0) has no part,
  * whatever its weights hold; an id >= E neither, and raises
  * MOE_DEVERR_EXPERT_RANGE; an expert in two slots gets both parts.  A token whose

@@ -75,7 +75,7 @@ def test_pack_refusals(lib, kw, status):
 
 
 def _linear(lib, **kw):
-    a = dict(x=P, xs=P, stride=40, M=40, N=256, K=512, packed=P, scales=P, flags=0, y=P, ws=P, bytes=1 << 40)
+    a = dict(x=P, xs=P, stride=40, M=40, N=256, K=512, packed=P, scales=P, flags=0, y=2 * P, ws=P, bytes=1 << 40)
     a.update(kw)
     return lib.moe_linear_fp8(*a.values(), None)
 
@@ -86,7 +86,7 @@ def _linear(lib, **kw):
     (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(K=(1 << 20) + 128), UNSUPPORTED),
     (dict(M=1 << 31, stride=1 << 31), UNSUPPORTED), (dict(x=None), INVALID), (dict(xs=None), INVALID),
     (dict(packed=None), INVALID), (dict(scales=None), INVALID), (dict(y=None), INVALID), (dict(x=P + 8), INVALID),
-    (dict(y=P + 2), INVALID), (dict(packed=P + 4), INVALID), (dict(M=0, x=None, y=None, ws=None), OK),
+    (dict(y=P + 2), INVALID), (dict(y=P), INVALID), (dict(packed=P + 4), INVALID), (dict(M=0, x=None, y=None, ws=None), OK),
     (dict(M=(1 << 31) - 1, stride=1 << 31, N=1 << 20, K=128), UNSUPPORTED),
 ])
 def test_linear_refusals(lib, kw, status):
@@ -127,14 +127,14 @@ def test_loss_refusals(lib, kw, status):
 
 
 def _back(lib, **kw):
-    a = dict(logits=P, valid=None, idx=P, w=P, dw=P, T=4, E=8, K=2, flags=1, d=P, counts=P, n=P, out=P, err=None)
+    a = dict(logits=P, valid=None, idx=P, w=P, dw=P, T=4, E=8, K=2, flags=1, d=P, counts=P, n=P, out=2 * P, err=None)
     a.update(kw)
     return lib.moe_route_backward(*a.values(), None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), INVALID), (dict(K=9), INVALID), (dict(flags=2), INVALID), (dict(E=1025), UNSUPPORTED),
-    (dict(E=64, K=33), UNSUPPORTED), (dict(out=None), INVALID), (dict(dw=None, d=None), INVALID), (dict(w=None), INVALID),
+    (dict(E=64, K=33), UNSUPPORTED), (dict(out=None), INVALID), (dict(out=P), INVALID), (dict(dw=None, d=None), INVALID), (dict(w=None), INVALID),
     (dict(idx=None), INVALID), (dict(counts=None), INVALID), (dict(n=None), INVALID), (dict(logits=None), INVALID),
     (dict(logits=None, d=None, flags=0), INVALID), (dict(T=0, logits=None, out=None), OK),
 ])
@@ -180,3 +180,19 @@ def test_binding_checks():
         ops.moe_route_backward(torch.zeros(4, 8), idx, k, k, d_loss=torch.ones(2))
     with pytest.raises(ValueError, match="one shape"):
         ops.moe_route_backward(torch.zeros(4, 8), idx, k, torch.zeros(4, 3))
+
+
+def test_sizes_past_the_interface():
+    """What a 32-bit argument would take modulo 2^32 (tensors without memory of that size)."""
+    far = (1 << 32) + 128
+    with pytest.raises(ValueError, match="below 2"):
+        ops.moe_rmsnorm(torch.zeros(1, 1, dtype=BF).expand(1, far), torch.zeros(1).expand(far))
+    with pytest.raises(ValueError, match="below 2"):
+        ops.moe_balance_loss(torch.zeros(1, 1).expand(far, 8), torch.zeros(1, 1, dtype=I32).expand(far, 2))
+    with pytest.raises(ValueError, match="below 2"):
+        ops.moe_route_backward(torch.zeros(1, 1).expand(far, 8), *(torch.zeros(1, 1).expand(far, 2),) * 3)
+    for size in (lambda: ops.moe_linear_fp8_packed_bytes(far, 128), lambda: ops.moe_linear_fp8_workspace_bytes(1, 16, far),
+                 lambda: ops.moe_rmsnorm_backward_workspace_bytes(1, far),
+                 lambda: ops.moe_balance_loss_workspace_bytes(far, 8)):
+        with pytest.raises(ValueError, match="below 2"):
+            size()

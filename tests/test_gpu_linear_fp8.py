@@ -86,6 +86,23 @@ def test_packing_bf16(N, K):
         assert torch.equal(s2.cpu().reshape(ws.shape), ws)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_packing_what_is_not_finite(bad):
+    """Its tile has no scale: NaN, and so has every output that the tile is part of."""
+    w = (0.02 * torch.randn(384, 512, generator=gen(5))).bfloat16()
+    clean = ops.linear_weights(w.cuda())
+    w[200, 300] = bad
+    a = ops.linear_weights(w.cuda())
+    assert torch.isnan(a.scales[1, 2]) and (_unpack(a)[128:256, 256:384] == 0x7F).all()
+    rest = torch.ones(3, 4, dtype=torch.bool)
+    rest[1, 2] = False
+    assert torch.equal(a.scales.cpu()[rest], clean.scales.cpu()[rest])
+    x = ops.moe_quant_rows_fp8(torch.randn(40, 512, generator=gen(6)).bfloat16().cuda())
+    y, z = ops.moe_linear_fp8(*x, a), ops.moe_linear_fp8(*x, clean)
+    assert torch.isnan(y[:, 128:256]).all()
+    assert torch.equal(y[:, :128], z[:, :128]) and torch.equal(y[:, 256:], z[:, 256:])
+
+
 def test_rows_past_n_are_zero():
     _, _, wq, ws = _case(1, 20, 128)
     packed = ops.linear_weights_from_codes(wq.cuda(), ws.cuda()).packed.cpu().reshape(2, 2, 4, 16, 16)
