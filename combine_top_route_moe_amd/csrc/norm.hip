@@ -7,8 +7,8 @@
 //   y = bf16(v);  per 128 channels s = amax |v| / 448, code = e4m3(v / s)
 // h is rounded before it is normed because that rounded value is what the
 // stream keeps: the gradient, which starts from the stored h, is then exactly
-// the forward's.  p is exact for a bf16 w.  The codes come from the unrounded row,
-// as 448 p / amax |p|: r falls out of the quotient.
+// the forward's.  The codes come from the unrounded row,
+// as 448 p / amax |p|: r falls out of the quotient, which is rounded once.
 //
 // Gradient, with hat = h r and g = dy w:
 //   dh = r (g - hat sum(g hat) / H) (+ the stream's own gradient),
@@ -79,6 +79,46 @@ __device__ __forceinline__ uint4 to_bf16x8(const float* v) {
   for (int j = 0; j < 4; ++j)
     o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * j], v[2 * j + 1]}, b2));
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Codes of 448 h w / (the block's largest h w) for a float32 gain, whose products have
+// 32 bits.  p (the rounded products) times 448 / top is off by 4 roundings, 2^-22; where
+// both ends of twice that give the same codes, those are the nearest to the unrounded
+// quotient.  Else (0.6 % of the waves) it is rounded to odd in float32, from where the
+// rounding to nearest goes the same way: the residuals of the quotient, before and after
+// its correction, are put together from exact parts, and the second is 0 where the
+// quotient lies half way between two codes, else its sign shows the side.
+__device__ __forceinline__ uint2 codes_f32(const float (&p)[8], const uint4& h, const void* weight, int c, float top) {
+  const float inv = 448.0f / top;
+  float u[8], o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = p[j] * (inv * (1.0f - 0x1p-21f)), o[j] = p[j] * (inv * (1.0f + 0x1p-21f));
+  uint2 q = e4m3x8(u);
+  const uint2 over = e4m3x8(o);
+  if (__any(q.x != over.x || q.y != over.y)) {
+    float lo[8], w[8], top_lo = -__builtin_inff();
+    unpack8(h, lo);
+    load_gain<true>(weight, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {       // h w = p + lo; top_lo of the products that share the largest p
+      lo[j] = __builtin_fmaf(lo[j], w[j], -p[j]);
+      top_lo = fabsf(p[j]) == top ? fmaxf(top_lo, __builtin_copysignf(1.0f, p[j]) * lo[j]) : top_lo;
+    }
+    top_lo = row16_top_f32(top_lo);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v0 = p[j] * inv, a = 448.0f * p[j];
+      const float rest = __builtin_fmaf(448.0f, lo[j], __builtin_fmaf(448.0f, p[j], -a));
+      const float left0 = __builtin_fmaf(-v0, top, a) + __builtin_fmaf(-v0, top_lo, rest);
+      const float v = __builtin_fmaf(left0, 1.0f / top, v0);
+      const float left = __builtin_fmaf(-v, top, a) + __builtin_fmaf(-v, top_lo, rest);
+      const uint32_t bits = __float_as_uint(v);
+      const int step = ((int)(__float_as_uint(left) ^ bits) >> 31) | 1;     // away from 0 or towards it
+      u[j] = __uint_as_float(left != 0.0f && !(bits & 1) ? bits + step : bits);
+    }
+    q = e4m3x8(u);
+  }
+  return q;
 }
 
 // A workgroup of 4 waves (16 for the longest rows) holds 4 / kWaves rows.  4096 x 7168
@@ -160,23 +200,29 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
       const float s = top * r / 448.0f;
       uint2 q = make_uint2(0, 0);
       if (!(s <= 0.0f)) {
-        const float inv = 448.0f / top, inv_top = inv * (1.0f / 448.0f);
-        if (top >= 0x1p-90f) {
-          // 448 p / top from the quotient's reciprocal, put right by its residual: off
-          // by half a step of float32 before the rounding to 3 bits
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float u = p[j] * inv;
-            p[j] = __builtin_fmaf(-__builtin_fmaf(u, top, -448.0f * p[j]), inv_top, u);
-          }
+        const bool plain = top >= 0x1p-90f && top <= 0x1p110f;
+        if (kWF32 && plain) {
+          q = codes_f32(p, hv[i], weight, c, top);
         } else {
+          const float inv = 448.0f / top, inv_top = inv * (1.0f / 448.0f);
+          if (plain) {
+            // 448 p / top from the quotient's reciprocal, put right by its residual: the
+            // nearest float32.  p has 16 bits and 448 p / top, where it is not half way
+            // between two codes, is 2^-21 away from there: the code is the nearest too.
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = p[j] / top * 448.0f;
+            for (int j = 0; j < 8; ++j) {
+              const float u = p[j] * inv;
+              p[j] = __builtin_fmaf(-__builtin_fmaf(u, top, -448.0f * p[j]), inv_top, u);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = p[j] / top * 448.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_fmed3f(p[j], -448.0f, 448.0f);
+          q = e4m3x8(p);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_fmed3f(p[j], -448.0f, 448.0f);
-        q = e4m3x8(p);
-        if (s != s) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (!(s < __builtin_inff())) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
       }
       reinterpret_cast<uint2*>(codes)[t * nvec + c] = q;
       if ((c & 15) == 0) scales[(int64_t)(c / 16) * sstride + t] = s;

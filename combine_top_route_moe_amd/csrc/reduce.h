@@ -31,6 +31,13 @@ __device__ __forceinline__ float row16_sum_f32(float v) {
   return v + dpp16<0x140>(v);
 }
 
+__device__ __forceinline__ float row16_top_f32(float v) {
+  v = fmaxf(v, dpp16<0xB1>(v));
+  v = fmaxf(v, dpp16<0x4E>(v));
+  v = fmaxf(v, dpp16<0x141>(v));
+  return fmaxf(v, dpp16<0x140>(v));
+}
+
 __device__ __forceinline__ float lane_f32(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
@@ -44,10 +51,7 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return lane_f32(v, 63);
 }
 __device__ __forceinline__ float wave_top_f32(float v) {
-  v = fmaxf(v, dpp16<0xB1>(v));
-  v = fmaxf(v, dpp16<0x4E>(v));
-  v = fmaxf(v, dpp16<0x141>(v));
-  v = fmaxf(v, dpp16<0x140>(v));
+  v = row16_top_f32(v);
   int b = __float_as_int(v);
   v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, 0x142, 0xA, 0xF, false)));
   b = __float_as_int(v);

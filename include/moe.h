@@ -586,17 +586,17 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
  *   y = bf16(v)                                                  (the router's rows)
  *   s = fl32(amax |v| / 448) per 128 channels, codes = e4m3(v / s)  (the experts')
  * h is rounded before it is normed: it is what the stream keeps and what the
- * gradient starts from.  The codes are those of v, not of the rounded y; v / s is
- * taken as the float32 nearest to 448 (h weight) / amax |h weight|, its code to
- * nearest even.
+ * gradient starts from.  The codes are those of v, not of the rounded y, and of
+ * 448 (h weight) / amax |h weight| without a rounding: the nearest code, half way to
+ * the even one (with amax outside 2^-90 .. 2^110 the quotient is rounded twice).
  *   x [T, H] bf16;  residual [T, H] bf16 or NULL;  weight [H] bf16, or float32
  *   with MOE_NORM_WEIGHT_F32;  outputs, each may be NULL but not all: h [T, H]
  *   bf16;  y [T, H] bf16;  codes [T, H] uint8 with scales [H/128, scale_stride]
  *   float32 (K-block-major, as moe_quant_rows_fp8 writes them; scale_stride >=
  *   T; columns past T are left as they are);  rstd [T] float32, r.
  * h may be x's or residual's buffer and y may be x's.  An all-zero block gets
- * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) must be within
- * float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd, scales: 4).
+ * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) and h weight must
+ * be within float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd, scales: 4).
  * Requires H % 128 == 0, H <= 32768, eps > 0 and finite; sizes that need 2^32
  * threads are refused (T < 2^26 - 3 up to H = 2048, 2^24 up to 8192, else 2^22). */
 int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,

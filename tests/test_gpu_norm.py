@@ -60,6 +60,31 @@ def test_forward(T, H, residual, f32):
     check_forward(out, *_formula(x, res, w))
 
 
+def _nearest_codes(p):
+    """E4M3 values nearest to 448 p / amax |p| per 128 channels, half way to the even one.
+    p in float64 is exact (8 + 24 bits), and so are both sides of the comparison with
+    a midpoint: 448 p has 41 bits, a midpoint of 5 times the largest 37."""
+    T, H = p.shape
+    t = p.reshape(T, H // 128, 128)
+    top = t.abs().amax(2, keepdim=True)
+    q = (448 * t).abs() / torch.where(top > 0, top, torch.ones_like(top))
+    step = torch.exp2((torch.frexp(q).exponent - 4).clamp(min=-9).double())
+    low = torch.floor(q / step)
+    over = (448 * t).abs() - (low + 0.5) * step * top
+    return ((low + ((over > 0) | ((over == 0) & (low % 2 == 1)))) * step * t.sign()).reshape(T, H)
+
+
+@pytest.mark.parametrize("T,H", [(333, 640), (64, 7168), (5, 16384), (4097, 256)])
+@pytest.mark.parametrize("gain", ["bf16", "f32", "f32 of few bits", "ones"])
+def test_codes_are_the_nearest(T, H, gain):
+    """Not one code on the wrong side, half-way quotients included (a bf16 gain and a gain
+    of few bits have thousands of them)."""
+    x, _, w = _inputs(T, H, f32=True)
+    w = {"bf16": w.bfloat16(), "f32": w, "f32 of few bits": w.bfloat16().float(), "ones": torch.ones(H)}[gain]
+    out = ops.moe_rmsnorm(x.cuda(), w.cuda(), EPS, y=False, codes=True)
+    assert torch.equal(e4m3(out.codes.cpu()).double(), _nearest_codes(x.double() * w.double()))
+
+
 @pytest.mark.parametrize("want", ["y", "codes", "rstd", "h"])
 def test_one_output(want):
     x, res, w = _inputs(37, 1024)
