@@ -568,7 +568,6 @@ struct LinearTile {
 constexpr LinearTile kTiles[4] = {{64, 64, 256, 0.28, 0.225}, {64, 128, 512, 0.40, 0.345},
                                   {128, 128, 256, 0.72, 0.55}, {256, 256, 512, 1.4, 1.76}};
 constexpr double kThreadsMost = 0xffffffffu;       // of a launch
-constexpr int kRowsMost = 16;                      // of linear_rows_kernel
 constexpr int kPartsMost = 8;                      // 2, 4 or 8 (linear_join_kernel)
 constexpr int64_t kPartBytes = 32 << 20;           // all parts together: more costs more than it gives
 
@@ -592,7 +591,7 @@ static LinearForm linear_form(int64_t M, int N, int nkb) {
 
 // Enough for every smaller M too.
 size_t linear_fp8_workspace_bytes(int64_t M, int N, int K) {
-  if (M <= kRowsMost || K == 128) return 0;
+  if (M <= MOE_LINEAR_FEW_ROWS || K == 128) return 0;
   return (size_t)std::min(kPartBytes, (int64_t)kPartsMost * 4 * M * N);
 }
 
@@ -652,7 +651,7 @@ static int launch_linear_big(const LinearCall& c) {
 
 template <bool F32>
 static int launch_linear(const LinearCall& c) {
-  if (c.M <= kRowsMost) {
+  if (c.M <= MOE_LINEAR_FEW_ROWS) {
     launch_linear_rows<F32>(c);
     return MOE_OK;
   }

@@ -26,7 +26,6 @@ namespace moe {
 constexpr int kLossWaves = 16;          // waves of a loss workgroup
 constexpr int kLossMaxGroups = 256;     // workgroups of the first launch at most,
 constexpr int kLossMaxShares = 32768;   // and their shares of experts: one workgroup joins them
-constexpr int kLossOneGroup = 64;       // tokens that one workgroup takes in one launch
 
 // exp, log and reciprocal in float32 by the hardware's own: exp(x) = 2^(x log2 e) to
 // (|x| + 2) 2^-24 relative, as far as the rounding of x = l - l_max has left it exact;
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(void* ws, int groups
 
 // Few tokens in one launch: the second costs more than the longer walk.
 static int loss_groups(int T, int E) {
-  if (T <= kLossOneGroup) return T > 0;
+  if (T <= MOE_LOSS_FEW_TOKENS) return T > 0;
   return std::min({(T - 1) / kLossWaves + 1, kLossMaxGroups, std::max(32, kLossMaxShares / E)});
 }
 

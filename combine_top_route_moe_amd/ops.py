@@ -29,6 +29,7 @@ MOE_DECODE_MAX_TOKENS = 64
 MOE_NORM_WEIGHT_F32 = 1
 MOE_NORM_FEW_ROWS = 1024
 MOE_LINEAR_TRANSPOSE, MOE_LINEAR_OUT_F32 = 1, 2
+MOE_LINEAR_FEW_ROWS, MOE_LOSS_FEW_TOKENS = 16, 64
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -907,7 +908,7 @@ def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     d_weight, pdw = _output(True if d_weight is None else d_weight, (H,), torch.float32, dy, stream,
                             "d_weight")
     pws, size = None, 0
-    if T > MOE_NORM_FEW_ROWS or px == pdy:
+    if T > MOE_NORM_FEW_ROWS or px == pdy or workspace is not None:
         workspace, pws, size = _scratch(workspace, dy, stream, lib.moe_rmsnorm_backward_workspace_bytes, T, H)
     check("moe_rmsnorm_backward", lib.moe_rmsnorm_backward(
         pdy, ph, pi, pw, T, H, flags, pd, px, pdw, pws, size, raw))
@@ -1013,7 +1014,9 @@ def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeigh
     px, ps = _pointers(x.get_device(), (x, torch.uint8, "x"), (x_scales, torch.float32, "x_scales"))
     lib = load()
     y, py = _output(True if y is None else y, (M, N), out_dtype, x, stream, "y")
-    workspace, pws, size = _scratch(workspace, x, stream, lib.moe_linear_fp8_workspace_bytes, M, N, K)
+    pws, size = None, 0
+    if M > MOE_LINEAR_FEW_ROWS or workspace is not None:
+        workspace, pws, size = _scratch(workspace, x, stream, lib.moe_linear_fp8_workspace_bytes, M, N, K)
     check("moe_linear_fp8", lib.moe_linear_fp8(
         px, ps, x_scales.shape[1], M, N, K, weights.packed.data_ptr(), weights.scales.data_ptr(),
         MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, size, raw))
@@ -1068,7 +1071,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     counts, pc = _output(want[1], (E,), i32, logits, stream, "counts")
     probs, pp = _output(want[2], (E,), f32, logits, stream, "probs")
     tokens, pn = _output(want[3], (1,), i32, logits, stream, "num_tokens")
-    workspace, pws, size = _scratch(workspace, logits, stream, lib.moe_balance_loss_workspace_bytes, T, E)
+    pws, size = None, 0
+    if T > MOE_LOSS_FEW_TOKENS or workspace is not None:
+        workspace, pws, size = _scratch(workspace, logits, stream, lib.moe_balance_loss_workspace_bytes, T, E)
     check("moe_balance_loss", lib.moe_balance_loss(pl, pv, pi, T, E, K, po, pc, pp, pn, pws, size, perr,
                                                    raw))
     return RouterLosses(loss, counts, probs, tokens)

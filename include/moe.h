@@ -90,6 +90,8 @@ enum { MOE_NORM_WEIGHT_F32 = 1 };     /* moe_rmsnorm: a float32 gain, not bf16 *
 enum { MOE_NORM_FEW_ROWS = 1024 };    /* moe_rmsnorm_backward without workspace */
 enum { MOE_LINEAR_TRANSPOSE = 1,      /* moe_pack_linear_fp8: pack W^T        */
        MOE_LINEAR_OUT_F32 = 2 };      /* moe_linear_fp8: y in float32         */
+enum { MOE_LINEAR_FEW_ROWS = 16 };    /* moe_linear_fp8 without workspace     */
+enum { MOE_LOSS_FEW_TOKENS = 64 };    /* moe_balance_loss without workspace   */
 
 /* The packed weights of G experts (device pointers) in one of the formats
  * above; the struct itself is host memory, read during the call only.
@@ -595,8 +597,9 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
  *   float32 (K-block-major, as moe_quant_rows_fp8 writes them; scale_stride >=
  *   T; columns past T are left as they are);  rstd [T] float32, r.
  * h may be x's or residual's buffer and y may be x's.  An all-zero block gets
- * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) and h weight must
- * be within float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd, scales: 4).
+ * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) and h weight must be
+ * within float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd,
+ * scales: 4).
  * Requires H % 128 == 0, H <= 32768, eps > 0 and finite; sizes that need 2^32
  * threads are refused (T < 2^26 - 3 up to H = 2048, 2^24 up to 8192, else 2^22). */
 int moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t T, int H,
@@ -630,8 +633,9 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *
  * moe_pack_linear_fp8 lays W [N, K] out once: from bf16 (`w`, quantized per 128 x
  * 128 tile as moe_pack_ffn_weights_fp8 does; a tile at the edge from the rows it
- * has; one with an infinity or NaN gets a NaN scale and NaN codes), or from codes [N, K] and scales [ceil(N/128), K/128] that exist already
- * (a checkpoint), unchanged; the other pointers are NULL.
+ * has; one with an infinity or NaN gets a NaN scale and NaN codes), or from codes
+ * [N, K] and scales [ceil(N/128), K/128] that exist already (a checkpoint),
+ * unchanged; the other pointers are NULL.
  *   packed: moe_linear_fp8_packed_bytes(N, K) bytes; the 16 x 128 tile of rows
  *     16 i .. and block b at unit (i * (K/128) + b) * 128 of 16 bytes, in it
  *     unit 64 h + l the codes of row l % 16, columns 64 h + 16 (l / 16) .. +16;
@@ -646,7 +650,7 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *   x [M, K] uint8 and x_scales [K/128, scale_stride] float32 (scale_stride >= M)
  *   from moe_quant_rows_fp8 or moe_rmsnorm;  y [M, N] bf16, or float32 with
  *   MOE_LINEAR_OUT_F32, not x's buffer;  the workspace may be NULL where the query
- *   says 0.
+ *   says 0, as it does up to MOE_LINEAR_FEW_ROWS rows.
  * A row's result depends on that row alone (a NaN stays in its row); equal calls
  * give equal bits, but a row's bits may differ with M.  M = 0 enqueues nothing.
  * Requires M < 2^31, K % 128 == 0, N and K <= 2^20; sizes that need more than 2^32
@@ -673,6 +677,7 @@ int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride
  *   logits [T, E] float32;  row_valid [T] uint8 or NULL;  topk_idx [T, K] int32;
  *   outputs loss [2] float32, counts [E] int32, probs [E] float32, num_tokens [1]
  *   int32.  Sums have a fixed order (equal calls, equal bits).  T = 0 writes zeros.
+ *   Up to MOE_LOSS_FEW_TOKENS tokens the workspace may be NULL.
  * Requires 1 <= K <= min(E, 32), E <= 1024. */
 size_t moe_balance_loss_workspace_bytes(int T, int E);
 int moe_balance_loss(const float* logits, const uint8_t* row_valid, const int32_t* topk_idx, int T,

@@ -103,6 +103,8 @@ def test_sizes(lib):
     for T, H in ((1, 128), (10 ** 6, 2048), (10 ** 6, 8192), (10 ** 6, 32768)):
         assert 4 * H <= lib.moe_rmsnorm_backward_workspace_bytes(T, H) <= 4096 * 4 * H
     assert lib.moe_balance_loss_workspace_bytes(0, 64) == 0 and lib.moe_balance_loss_workspace_bytes(9, 2000) == 0
+    assert lib.moe_balance_loss_workspace_bytes(ops.MOE_LOSS_FEW_TOKENS, 1024) == 0
+    assert lib.moe_linear_fp8_workspace_bytes(ops.MOE_LINEAR_FEW_ROWS, 8192, 8192) == 0
     sizes = [lib.moe_balance_loss_workspace_bytes(T, 64) for T in (1, 64, 65, 1000, 10 ** 4, 10 ** 6)]
     assert sizes[0] == 0 and sizes == sorted(sizes) and sizes[2] > 0 and sizes[-1] < 1 << 20
     sizes = [lib.moe_linear_fp8_workspace_bytes(M, 576, 7168) for M in (1, 16, 17, 64, 500, 5000, 10 ** 6)]
