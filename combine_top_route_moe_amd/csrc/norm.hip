@@ -18,6 +18,7 @@
 // in registers between the reduction and its use.  One row belongs to kWaves
 // waves (1, 4 or 16 by H, four 16-byte vectors a thread at most), so that the
 // loads of a whole row are in flight at once and no loop runs over it.
+#include <algorithm>
 #include <type_traits>
 
 #include "reduce.h"
@@ -230,35 +231,77 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_kernel(
   }
 }
 
+// The thread's vectors of a gain as they lie in memory: it uses them for every row, twice.
+// (With 16 waves of four vectors there are no registers for them: read again each time.)
+template <int kWaves, int kVecs, bool kWF32>
+struct Gain {
+  static constexpr bool kHeld = kWaves < 16 || kVecs < 4;
+  static constexpr int kUnits = kWF32 ? 2 : 1;
+  const uint4* p;
+  uint4 v[kHeld ? kVecs : 1][kUnits];
+  __device__ __forceinline__ Gain(const void* weight, int tid, int nvec)
+      : p(static_cast<const uint4*>(weight) + (int64_t)tid * kUnits) {
+    if (!kHeld) return;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        v[kHeld ? i : 0][u] = tid + i * kWaves * kWave < nvec ? p[i * kWaves * kWave * kUnits + u]
+                                                              : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(int i, float (&w)[8]) const {
+    uint4 u[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) u[k] = kHeld ? v[kHeld ? i : 0][k] : p[i * kWaves * kWave * kUnits + k];
+    if (kWF32) {
+      const uint4 &a = u[0], &b = u[kUnits - 1];
+      w[0] = __uint_as_float(a.x), w[1] = __uint_as_float(a.y), w[2] = __uint_as_float(a.z);
+      w[3] = __uint_as_float(a.w), w[4] = __uint_as_float(b.x), w[5] = __uint_as_float(b.y);
+      w[6] = __uint_as_float(b.z), w[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(u[0], w);
+    }
+  }
+};
+
+// The thread's vectors of a row of dy, h and d_residual.
+template <int kWaves, int kVecs>
+struct BackwardRow {
+  uint4 dy[kVecs], h[kVecs], dres[kVecs];
+  __device__ __forceinline__ void load(const uint16_t* dy_, const uint16_t* h_, const uint16_t* d_residual, int64_t t,
+                                       bool real, int nvec, int tid) {
+    const uint4* a = reinterpret_cast<const uint4*>(dy_) + t * nvec;
+    const uint4* b = reinterpret_cast<const uint4*>(h_) + t * nvec;
+    const uint4* d = reinterpret_cast<const uint4*>(d_residual) + t * nvec;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = tid + i * kWaves * kWave;
+      const bool in = real && c < nvec;
+      dy[i] = in ? load_row(a + c) : zero;
+      h[i] = in ? load_row(b + c) : zero;
+      dres[i] = in && d_residual ? load_row(d + c) : zero;
+    }
+  }
+};
+
 // A row's part in dx, and with kDw in the thread's sums of dw: what both forms of the
 // gradient do with it.
 template <int kWaves, int kVecs, bool kWF32, bool kDw>
-__device__ __forceinline__ void backward_row(const uint16_t* dy, const uint16_t* h, float r, const void* weight,
-                                             int64_t t, int nvec, int tid, int wave, const uint16_t* d_residual,
-                                             uint16_t* dx, float* part, float (&dw)[kVecs][8]) {
+__device__ __forceinline__ void backward_row(const BackwardRow<kWaves, kVecs>& row, float r,
+                                             const Gain<kWaves, kVecs, kWF32>& gain, int64_t t, int nvec, int tid,
+                                             int wave, bool d_residual, uint16_t* dx, float* part,
+                                             float (&dw)[kVecs][8]) {
   constexpr int kThreads = kWaves * kWave;
-  const uint4* dyr = reinterpret_cast<const uint4*>(dy) + t * nvec;
-  const uint4* hr = reinterpret_cast<const uint4*>(h) + t * nvec;
-  const uint4* dr = reinterpret_cast<const uint4*>(d_residual) + t * nvec;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 a[kVecs], b[kVecs], d[kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int c = tid + i * kThreads;
-    const bool in = c < nvec;
-    a[i] = in ? load_row(dyr + c) : zero;
-    b[i] = in ? load_row(hr + c) : zero;
-    d[i] = in && d_residual ? load_row(dr + c) : zero;
-  }
   float dot = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = tid + i * kThreads;
     if (c >= nvec) break;
     float g[8], f[8], w[8];
-    unpack8(a[i], g);
-    unpack8(b[i], f);
-    load_gain<kWF32>(weight, c, w);
+    unpack8(row.dy[i], g);
+    unpack8(row.h[i], f);
+    gain.get(i, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float hat = f[j] * r;
@@ -272,10 +315,10 @@ __device__ __forceinline__ void backward_row(const uint16_t* dy, const uint16_t*
     const int c = tid + i * kThreads;
     if (c >= nvec) break;
     float g[8], f[8], w[8], e[8];
-    unpack8(a[i], g);
-    unpack8(b[i], f);
-    unpack8(d[i], e);
-    load_gain<kWF32>(weight, c, w);
+    unpack8(row.dy[i], g);
+    unpack8(row.h[i], f);
+    unpack8(row.dres[i], e);
+    gain.get(i, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float v = r * __builtin_fmaf(-dot, f[j] * r, g[j] * w[j]);
@@ -287,8 +330,9 @@ __device__ __forceinline__ void backward_row(const uint16_t* dy, const uint16_t*
 
 // Many rows: one workgroup walks the rows blockIdx.x, blockIdx.x + gridDim.x, .. (in
 // groups of kRows) and keeps its share of dw in registers; `partial` [gridDim.x, H]
-// takes the shares, which norm_dw_kernel adds up in order.  16384 x 4096 98 + 5 us.
-template <int kWaves, int kVecs, bool kWF32>
+// takes the shares, which norm_dw_kernel adds up in order.  kAhead: the next row is
+// loaded before this one is worked on.  16384 x 4096 85 + 5 us.
+template <int kWaves, int kVecs, bool kWF32, bool kAhead>
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_kernel(
     const uint16_t* dy, const uint16_t* __restrict__ h, const float* __restrict__ rstd,
     const void* __restrict__ weight, int64_t T, int H, const uint16_t* d_residual, uint16_t* dx,
@@ -305,11 +349,24 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_ke
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  const Gain<kWaves, kVecs, kWF32> gain(weight, tid, nvec);
   int flip = 0;                         // the next row's sums go to the other buffer: one barrier a row
-  for (int64_t t = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); t < T;
-       t += (int64_t)gridDim.x * kRows, flip ^= 1)
-    backward_row<kWaves, kVecs, kWF32, true>(dy, h, rstd[t], weight, t, nvec, tid, wave, d_residual, dx, part[flip],
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t t = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
+  BackwardRow<kWaves, kVecs> row, next;
+  float r = 0.0f, next_r = 0.0f;
+  auto load = [&](BackwardRow<kWaves, kVecs>& to, float& to_r, int64_t at) __attribute__((always_inline)) {
+    to.load(dy, h, d_residual, at, at < T, nvec, tid);
+    to_r = rstd[min(at, T - 1)];
+  };
+  if (kAhead) load(row, r, t);
+  for (; t < T; t += step, flip ^= 1) {
+    if (kAhead) load(next, next_r, t + step);
+    else load(row, r, t);
+    backward_row<kWaves, kVecs, kWF32, true>(row, r, gain, t, nvec, tid, wave, d_residual != nullptr, dx, part[flip],
                                              dw);
+    if (kAhead) row = next, r = next_r;
+  }
   float* out = partial + (int64_t)blockIdx.x * H;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -353,10 +410,12 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_fe
     const int wave = threadIdx.x >> 6;
     const int t = blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
     if (t >= T) return;
+    const int tid = kWaves == 1 ? threadIdx.x & 63 : threadIdx.x;
     float none[kVecs][8];
-    backward_row<kWaves, kVecs, kWF32, false>(dy, h, rstd[t], weight, t, nvec,
-                                              kWaves == 1 ? threadIdx.x & 63 : threadIdx.x, wave, d_residual, dx,
-                                              part, none);
+    BackwardRow<kWaves, kVecs> row;
+    row.load(dy, h, d_residual, t, true, nvec, tid);
+    backward_row<kWaves, kVecs, kWF32, false>(row, rstd[t], Gain<kWaves, kVecs, kWF32>(weight, tid, nvec), t, nvec,
+                                              tid, wave, d_residual != nullptr, dx, part, none);
     return;
   }
   const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
@@ -384,24 +443,30 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 256) rmsnorm_backward_fe
 }
 
 // dw[c] = sum over the n shares, four channels a thread, 32 threads along the
-// shares (each every 32nd, ascending), their sums added in order.
+// shares (each every 32nd, ascending), of whose sums those of a wave meet in pairs,
+// then the four waves' in order.
 __global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ partial, int n, int H,
                                                       float* __restrict__ dw) {
-  __shared__ float4 sums[32][8];
+  __shared__ float4 sums[4][8];
   const int col = threadIdx.x & 7, slice = threadIdx.x >> 3;
   const int c = blockIdx.x * 8 + col;   // of H / 4
   float4 s = make_float4(0, 0, 0, 0);
   const float4* p = reinterpret_cast<const float4*>(partial) + c;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = slice; i < n; i += 32) {
     const float4 v = p[(int64_t)i * (H / 4)];
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
-  sums[slice][col] = s;
+#pragma unroll
+  for (int off = 8; off < 64; off *= 2) {
+    s.x += __shfl_xor(s.x, off, kWave), s.y += __shfl_xor(s.y, off, kWave);
+    s.z += __shfl_xor(s.z, off, kWave), s.w += __shfl_xor(s.w, off, kWave);
+  }
+  if ((slice & 7) == 0) sums[slice >> 3][col] = s;
   __syncthreads();
   if (slice) return;
 #pragma unroll
-  for (int i = 1; i < 32; ++i) {
+  for (int i = 1; i < 4; ++i) {
     const float4 v = sums[i][col];
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
@@ -444,15 +509,25 @@ int launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weig
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-// Workgroups of the gradient.  Each leaves H floats of dw behind, so no more than keep
-// the memory busy: 512, 768, 1024 and 1536 take 55.8, 54.4, 62.3, 61.3 us for 4096 x
-// 7168, 102.9, 104.7, 100.7, 106.4 for 16384 x 4096, 58.6, 54.7, 61.6, 58.3 for
-// 16384 x 2048.  (Loading the next row ahead gained nothing in any of them.)
+// Workgroups of the gradient at most.  Each leaves H floats of dw behind, so no more than
+// keep the memory busy, and the CUs evenly: 256, 384, 512, 640 and 768 take 55.8, 49.3,
+// 48.2, 53.4, 50.9 us for 4096 x 7168, 108, 92, 95, 105, 101 for 16384 x 4096, 57, 53, 51.5,
+// 56, 52.7 for 16384 x 2048.
 static int64_t norm_shares(int64_t T, int H) {
   const int waves = norm_waves(H);
   const int64_t rows = waves == 1 ? (T + 3) / 4 : T;
-  const int64_t most = waves == 16 ? 256 : 768;
+  const int64_t most = waves == 16 ? 256 : 512;
   return rows < most ? rows : most;
+}
+
+// With the next row ahead 256 are enough, us against 512 without: 16384 x 4096 89 and 95,
+// 4096 x 7168 47.2 and 48.6, 16384 x 2048 49.8 and 51.8, 8192 x 1024 18.1 and 19.1; without
+// d_residual 16384 x 2048 40.9 and 41.2, but 16384 x 4096 78 and 72, 8192 x 6144 68 and 59;
+// 16384 x 768 25.1 and 24.5, 20000 x 512 34 and 20.5; 16 waves no difference.
+constexpr int kAheadShares = 256;
+static bool norm_ahead(int H, bool d_residual) {
+  const int waves = norm_waves(H);
+  return H >= 1024 && (waves == 1 || (waves == 4 && d_residual));
 }
 
 // One launch for few rows; one launch against two, us: 333 x 2048 4.5 and 9.2, 1024 x
@@ -484,18 +559,26 @@ int launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* 
     });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
   }
-  const int shares = (int)norm_shares(T, H);
+  const bool ahead = norm_ahead(H, d_residual);
+  const int most = (int)norm_shares(T, H), shares = ahead ? std::min(most, kAheadShares) : most;
   float* partial = static_cast<float*>(workspace);
+  auto launch = [&](auto waves, auto vecs, auto next) {
+    constexpr int W = decltype(waves)::value, V = decltype(vecs)::value;
+    constexpr bool A = decltype(next)::value;
+    const dim3 grid(shares), block(W == 16 ? 1024 : 256);
+    if (wf32)
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<W, V, true, A>), grid, block, 0, stream, dy, h, rstd, weight, T, H,
+                         d_residual, dx, partial);
+    else
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<W, V, false, A>), grid, block, 0, stream, dy, h, rstd, weight, T, H,
+                         d_residual, dx, partial);
+  };
   if (shares)
     norm_form(H, [&](auto waves, auto vecs) {
-      constexpr int W = decltype(waves)::value, V = decltype(vecs)::value;
-      const dim3 grid(shares), block(W == 16 ? 1024 : 256);
-      if (wf32)
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<W, V, true>), grid, block, 0, stream, dy, h, rstd, weight, T, H,
-                           d_residual, dx, partial);
-      else
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<W, V, false>), grid, block, 0, stream, dy, h, rstd, weight, T, H,
-                           d_residual, dx, partial);
+      if constexpr (decltype(waves)::value < 16 && decltype(vecs)::value > 1) {
+        if (ahead) return launch(waves, vecs, std::true_type());
+      }
+      launch(waves, vecs, std::false_type());
     });
   hipLaunchKernelGGL(norm_dw_kernel, dim3(H / 32), dim3(256), 0, stream, partial, shares, H, dw);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;

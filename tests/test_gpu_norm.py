@@ -178,7 +178,8 @@ def _gradient64(dy, h, r, w, dh):
     return dx, dx.abs() * (BF16 + U) + slack * (1 + BF16) + TINY, (dy.double() * hat).sum(0), (dy.double() * hat).abs().sum(0)
 
 
-@pytest.mark.parametrize("T,H", SHAPES + [(20000, 128), (1500, 4096), (300, 9216), (1024, 384), (1025, 384), (700, 16384)])
+@pytest.mark.parametrize("T,H", SHAPES + [(20000, 128), (1500, 4096), (300, 9216), (1024, 384), (1025, 384),
+                                        (700, 16384), (5000, 1024), (3000, 1536), (1300, 7168), (1030, 2176), (1100, 20480)])
 @pytest.mark.parametrize("residual,f32", [(True, True), (False, False)])
 def test_backward(T, H, residual, f32):
     x, res, w = _inputs(T, H, f32=f32)
@@ -191,8 +192,8 @@ def test_backward(T, H, residual, f32):
     want, bound, want_w, size = _gradient64(dy, x, r, w, dh)
     within(dx, want, bound, "dx")
     # up to 1024 rows each 32nd in a thread (32 additions), 32 threads (wide rows: 8 and 128);
-    # else at most 8 rows of a workgroup's share one after another up to 20000 rows, four
-    # waves, 768 / 32 shares in a thread and 32 threads; two roundings of a term
+    # else at most 12 rows of a workgroup's share one after another up to 20000 rows, four
+    # waves, 512 / 32 shares in a thread and 32 threads; two roundings of a term
     within(dw, want_w, (8 + 128 + 2) * U * size + 2.0 ** -140, "dw")
 
 
@@ -218,7 +219,7 @@ def test_backward_against_differences():
 
 
 @pytest.mark.parametrize("where", ["dy", "d_residual"])
-@pytest.mark.parametrize("T,H", [(9, 1024), (9, 4096)])
+@pytest.mark.parametrize("T,H", [(9, 1024), (9, 4096), (3000, 1024), (1300, 4096)])
 def test_backward_in_place(where, T, H):
     x, dy, w = _inputs(T, H)
     dh = torch.randn(T, H, generator=gen(6)).bfloat16()
