@@ -100,6 +100,7 @@ class MoELayer:
         self.normed_q = self.normed_s = None        # their codes and scales (the FP8 path)
         self.normed_rows = 0                        # how many rows its last call wrote,
         self.normed_codes = False                   # and whether their codes too
+        self.dispatched = None                      # the codes and scales that the last forward ran on
         self.weights = self.shared_weights = None   # decode()'s handles of the packed weights
         self.decode_tokens = min(T, ops.MOE_DECODE_MAX_TOKENS)
         self.decode_ws = None                       # of decode()'s first call
@@ -230,6 +231,7 @@ class MoELayer:
             raise ValueError("the FP8 path quantizes the dispatch rows itself (no FP4 dispatch)")
         self.hq = torch.empty(T, H, dtype=torch.uint8, device=dev)
         self.hs = torch.empty(H // 128, max(T, 1), dtype=torch.float32, device=dev)
+        self.dispatched = self.hq, self.hs
         # the permutation moves the codes: x_perm holds [cap, H] bytes as
         # [cap, H/2] 2-byte units (the maps are those of any permute)
         self.perm = ops.alloc_permuted(T, K, H // 2, self.El, self.capacity, dev)
@@ -334,10 +336,16 @@ class MoELayer:
             st.append(("dispatch_qdq", lambda: ops.moe_fake_quant_rows(
                 hidden, self.hidden_q, None, ops.MOE_FQ_BLOCK, self.dispatch_block)))
         fuse = self.fuse_dispatch and not self.w8a8
-        st.append(("permute", lambda: ops.moe_permute(
-            self.topk_idx, self.topk_w, x, self.El, self.expert_begin, self.pad_pow2,
-            self.capacity, p, self.perm_ws, self.dev_error, dispatch_fp8=fuse,
-            num_experts=self.E)))
+        dispatched = (hq, hs) if self.w8a8 else None
+
+        def permute():
+            ops.moe_permute(self.topk_idx, self.topk_w, x, self.El, self.expert_begin, self.pad_pow2,
+                            self.capacity, p, self.perm_ws, self.dev_error, dispatch_fp8=fuse,
+                            num_experts=self.E)
+            if dispatched:
+                self.dispatched = dispatched
+
+        st.append(("permute", permute))
         st.append(("ffn_gate_up", lambda: self._ffn(
             x_ffn, p.cu_seqlens, p.counts, self.w13, self.w2, p.w_perm, self.y_perm,
             ops.MOE_FFN_GATE_UP, self.ffn_ws)))
@@ -455,14 +463,17 @@ class MoELayer:
         return self.combine_scale
 
     def stage_outputs(self) -> Dict[str, torch.Tensor]:
+        """The buffers that the stages wrote, by name.  On the FP8 path
+        ``hidden_codes`` and ``hidden_scales`` are those that the last forward
+        ran on, its own or ``norm``'s (of captured forwards, the last captured)."""
         p = self.perm
         d = dict(topk_idx=self.topk_idx, topk_w=self.topk_w, counts=p.counts,
                  cu_seqlens=p.cu_seqlens, x_perm=p.x_perm, row_of=p.row_of, src_of=p.src_of,
                  w_perm=p.w_perm, y_perm=self.y_perm, out=self.out)
         if self.hidden_q is not None:
             d["hidden_q"] = self.hidden_q
-        if self.w8a8:   # (of rows that forward() was given: norm()'s are normed_q, normed_s)
-            d["hidden_codes"], d["hidden_scales"] = self.hq, self.hs
+        if self.w8a8:
+            d["hidden_codes"], d["hidden_scales"] = self.dispatched
         if self.shared_out is not None:
             d["shared"] = self.shared_out
         return d

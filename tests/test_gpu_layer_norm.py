@@ -128,3 +128,16 @@ def test_a_block_in_training_captured_and_replayed():
     want = rows64(n.codes, n.scales) @ tiles64(wq[:E], ws).t()
     assert float((logits.cpu().double() - want).norm() / want.norm()) < 1e-3      # 2^-11 of the sum, at worst
     assert int(losses.counts.sum()) == T * K
+
+
+def test_stage_outputs_after_the_norm_hold_its_codes():
+    layer, (x, res, w, logits) = _layer("w8a8", True), _inputs()
+    n = ops.moe_rmsnorm(x, w, codes=True)
+    layer.norm(x, w)
+    layer.forward(logits, None)
+    outs = layer.stage_outputs()
+    assert torch.equal(outs["hidden_codes"], n.codes) and torch.equal(outs["hidden_scales"], n.scales)
+    layer.forward(logits, res)
+    codes, scales = ops.moe_quant_rows_fp8(res)
+    outs = layer.stage_outputs()
+    assert torch.equal(outs["hidden_codes"], codes) and torch.equal(outs["hidden_scales"], scales)
