@@ -300,14 +300,20 @@ class MoELayer:
         ``overlap_shared`` the shared expert is the first stage instead and
         runs on the side stream, which the current stream waits for before
         the combine (the form ``forward`` uses; a graph capture of it holds
-        the two branches).  ``hidden`` None: the rows of ``norm``."""
+        the two branches).  ``hidden`` None: the rows of ``norm``, which has to
+        have written all of them now and whenever a stage that reads them runs."""
         p = self.perm
-        quantized = hidden is None and self.w8a8
-        if hidden is None:
+        from_norm = hidden is None
+        quantized = from_norm and self.w8a8
+
+        def ready():
             if self.normed is None or self.normed_rows != self.T:
                 raise ValueError("without hidden, norm() has to have written all of the layer's rows")
             if quantized and not self.normed_codes:
                 raise ValueError("norm() ran before the FP8 path's weights were set: call it again")
+
+        if from_norm:
+            ready()
             hidden = self.normed
         x = self.hidden_q if self.hidden_q is not None else hidden
         st = [("route", lambda: ops.moe_route(logits, self.K, row_valid, self.renormalize,
@@ -380,6 +386,9 @@ class MoELayer:
         st.append(("combine", lambda: ops.moe_combine(
             self.y_perm, p.row_of, self.T, self.K, self.shared_out, fp8_scale, self.out,
             self.dev_error)))
+        if from_norm:                     # norm() may have run again since
+            reads = ("dispatch_qdq", "permute", "shared_ffn")
+            st = [(n, (lambda f: lambda: (ready(), f()))(f) if n in reads else f) for n, f in st]
         return st
 
     def forward(self, logits: torch.Tensor, hidden: Optional[torch.Tensor],

@@ -70,3 +70,46 @@ def test_stage_outputs_names_the_codes_that_the_forward_ran_on(calls):
     assert "hidden_codes" not in layer.stage_outputs()
     _set(layer, "w8a8")
     assert codes() == [layer.hq.data_ptr(), layer.hs.data_ptr()]    # new buffers
+
+
+@pytest.mark.parametrize("fp8", [False, "w8a8"])
+@pytest.mark.parametrize("overlap", [False, True])
+def test_a_list_of_stages_does_not_run_on_other_rows_than_it_was_made_for(calls, fp8, overlap):
+    """What norm() wrote is looked at when a stage reads it, not only when the list is made."""
+    layer = _layer(fp8)
+    layer.norm(X, W)
+    stages = dict(layer.stages(LOGITS, None, overlap_shared=overlap))
+    layer.norm(X[:5], W)                                            # a few tokens, for decode()
+    calls.clear()
+    for name in ("permute", "shared_ffn"):
+        with pytest.raises(ValueError, match="all of the layer's rows"):
+            stages[name]()
+    assert not calls
+    layer.norm(X, W)
+    for enqueue in stages.values():
+        enqueue()
+    assert calls.count("moe_permute") == 1 and calls.count("ffn") == 3
+
+
+def test_a_list_of_stages_on_codes_does_not_run_on_rows_without(calls):
+    layer = _layer("w8a8")
+    layer.norm(X, W)
+    stages = dict(layer.stages(LOGITS, None))
+    layer.w8a8 = False                                              # (as other weights leave it)
+    layer.norm(X, W)
+    with pytest.raises(ValueError, match="call it again"):
+        stages["permute"]()
+
+
+def test_a_list_of_stages_on_given_rows_does_not_look_at_the_norm(calls):
+    layer = _layer(dispatch_fp4="mxfp4")
+    layer.norm(X[:5], W)
+    for _, enqueue in layer.stages(LOGITS, X):
+        enqueue()
+    with pytest.raises(ValueError, match="all of the layer's rows"):
+        layer.stages(LOGITS, None)
+    layer.norm(X, W)
+    stages = dict(layer.stages(LOGITS, None))
+    layer.norm(X[:5], W)
+    with pytest.raises(ValueError, match="all of the layer's rows"):
+        stages["dispatch_qdq"]()
