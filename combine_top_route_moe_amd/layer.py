@@ -265,7 +265,8 @@ class MoELayer:
     # -------------------------------------------------------------------- norm
     def norm(self, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
              residual: Optional[torch.Tensor] = None,
-             h: Optional[torch.Tensor] = None) -> torch.Tensor:
+             h: Optional[torch.Tensor] = None,
+             rstd: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The norm in front of the layer (``moe_rmsnorm``): the rows x [n, H], n
         <= T, with ``residual`` added (the sum goes to ``h``, by default to the
         residual's own buffer), normed and weighted.  Returns them in bf16 (a
@@ -273,7 +274,8 @@ class MoELayer:
         product, ``decode`` and ``forward``.  With n = T, ``forward(logits,
         None)`` takes them from here; on the FP8 path (``fp8="w8a8"``) it then
         takes the codes that this call has written along with them, which are
-        those of the unrounded rows, and quantizes nothing itself."""
+        those of the unrounded rows, and quantizes nothing itself.  ``rstd`` [n]
+        takes what the norm's gradient starts from beside h (``moe_rmsnorm_backward``)."""
         n = x.shape[0]
         if x.dim() != 2 or x.shape[1] != self.H or n > self.T:
             raise ValueError(f"x must be [n, {self.H}] with n <= {self.T}")
@@ -286,7 +288,7 @@ class MoELayer:
             h = residual
         ops.moe_rmsnorm(x, weight, eps, residual=residual, h=h, y=self.normed[:n],
                         codes=self.normed_q if codes else False,
-                        scales=self.normed_s if codes else None)
+                        scales=self.normed_s if codes else None, rstd=rstd)
         self.normed_rows, self.normed_codes = n, codes
         return self.normed[:n]
 

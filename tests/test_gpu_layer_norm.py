@@ -141,3 +141,19 @@ def test_stage_outputs_after_the_norm_hold_its_codes():
     codes, scales = ops.moe_quant_rows_fp8(res)
     outs = layer.stage_outputs()
     assert torch.equal(outs["hidden_codes"], codes) and torch.equal(outs["hidden_scales"], scales)
+
+
+@pytest.mark.parametrize("fp8", [False, "w8a8"])
+@pytest.mark.parametrize("n", [5, T])
+def test_the_gradient_of_the_layers_norm(fp8, n):
+    """One norm a step: its gradient starts from what the layer's call wrote."""
+    layer, (x, res, w, _) = _layer(fp8), _inputs()
+    dy = torch.randn(n, H, generator=gen(7)).bfloat16().cuda()
+    want = ops.moe_rmsnorm(x[:n], w, residual=res[:n], rstd=True)
+    rstd, h = torch.full((T,), 7.0, device="cuda"), torch.empty(n, H, dtype=torch.bfloat16, device="cuda")
+    rows = layer.norm(x[:n], w, residual=res[:n], h=h, rstd=rstd[:n])
+    assert torch.equal(rows, want.y) and torch.equal(rstd[:n], want.rstd) and (rstd[n:] == 7).all()
+    for a, b in zip(ops.moe_rmsnorm_backward(dy, h, rstd[:n], w), ops.moe_rmsnorm_backward(dy, want.h, want.rstd, w)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="rstd"):
+        layer.norm(x[:n], w, rstd=rstd[: n - 1])
