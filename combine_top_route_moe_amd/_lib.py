@@ -74,6 +74,7 @@ SIGNATURES = {
     "moe_linear_fp8_packed_bytes": (_c_size, [_c_int, _c_int]),
     "moe_pack_linear_fp8": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "moe_linear_fp8_workspace_bytes": (_c_size, [_c_i64, _c_int, _c_int]),
+    "moe_linear_fp8_parts": (_c_int, [_c_i64, _c_int, _c_int, _vp]),
     "moe_linear_fp8": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp, _vp, _c_int, _vp,
                                 _vp, _c_size, _vp]),
     "moe_balance_loss_workspace_bytes": (_c_size, [_c_int, _c_int]),

@@ -58,6 +58,7 @@ int launch_rmsnorm_backward(const uint16_t*, const uint16_t*, const float*, cons
                             int64_t, int, const uint16_t*, uint16_t*, float*, void*, hipStream_t);
 int launch_pack_linear_fp8(const uint16_t*, const uint8_t*, const float*, int, int, int, uint8_t*,
                            float*, hipStream_t);
+int linear_fp8_parts(int64_t, int, int, int32_t*);
 size_t linear_fp8_workspace_bytes(int64_t, int, int);
 int launch_linear_fp8(const uint8_t*, const float*, int64_t, int64_t, int, int, const uint8_t*,
                       const float*, void*, int, void*, hipStream_t);
@@ -594,10 +595,16 @@ int moe_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float* sc
                                 packed_scales, as_stream(stream));
 }
 
+static bool linear_size_ok(int64_t M, int N, int K) {
+  return M >= 1 && M <= 0x7fffffffLL && N >= 1 && K >= 1 && K % 128 == 0 && N <= kLinearMost && K <= kLinearMost;
+}
+
 size_t moe_linear_fp8_workspace_bytes(int64_t M, int N, int K) {
-  if (M < 1 || M > 0x7fffffffLL || N < 1 || K < 1 || K % 128 || N > kLinearMost || K > kLinearMost)
-    return 0;
-  return linear_fp8_workspace_bytes(M, N, K);
+  return linear_size_ok(M, N, K) ? linear_fp8_workspace_bytes(M, N, K) : 0;
+}
+
+int moe_linear_fp8_parts(int64_t M, int N, int K, int32_t* tile) {
+  return linear_size_ok(M, N, K) ? linear_fp8_parts(M, N, K, tile) : 0;
 }
 
 int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride, int64_t M, int N,
@@ -609,7 +616,8 @@ int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride
   if (M == 0) return MOE_OK;
   if (!x || !x_scales || !packed || !packed_scales || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || y == x) return MOE_ERR_INVALID_ARG;
-  const size_t need = linear_fp8_workspace_bytes(M, N, K);
+  const int parts = linear_fp8_parts(M, N, K, nullptr);
+  const size_t need = parts > 1 ? (size_t)parts * M * N * sizeof(float) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
   return launch_linear_fp8(x, x_scales, scale_stride, M, N, K, packed, packed_scales, y,

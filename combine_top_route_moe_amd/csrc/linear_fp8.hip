@@ -589,6 +589,17 @@ static LinearForm linear_form(int64_t M, int N, int nkb) {
   return best;
 }
 
+// Parts of K of a product, and its workgroups' tile: {rows, columns}.
+int linear_fp8_parts(int64_t M, int N, int K, int32_t* tile) {
+  const bool few = M <= MOE_LINEAR_FEW_ROWS;
+  const LinearForm form = few ? LinearForm{0, 1} : linear_form(M, N, K / 128);
+  if (tile) {
+    tile[0] = few ? MOE_LINEAR_FEW_ROWS : kTiles[form.tile].m;
+    tile[1] = few ? 16 : kTiles[form.tile].n;
+  }
+  return form.parts;
+}
+
 // Enough for every smaller M too.
 size_t linear_fp8_workspace_bytes(int64_t M, int N, int K) {
   if (M <= MOE_LINEAR_FEW_ROWS || K == 128) return 0;

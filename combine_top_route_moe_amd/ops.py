@@ -989,6 +989,20 @@ def moe_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
     return load().moe_linear_fp8_workspace_bytes(M, N, K)
 
 
+def moe_linear_fp8_parts(M: int, N: int, K: int):
+    """``(parts, (rows, columns))``: in how many parts of K a product runs, and a
+    workgroup's tile."""
+    _int32(N, K)
+    tile = (ctypes.c_int32 * 2)()
+    return load().moe_linear_fp8_parts(M, N, K, tile), tuple(tile)
+
+
+def _parts_bytes(M: int, N: int, K: int) -> int:
+    """What a product of M rows uses of a workspace."""
+    parts = load().moe_linear_fp8_parts(M, N, K, None)
+    return 4 * parts * M * N if parts > 1 else 0
+
+
 def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeights,
                    y: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -1016,7 +1030,7 @@ def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: LinearWeigh
     y, py = _output(True if y is None else y, (M, N), out_dtype, x, stream, "y")
     pws, size = None, 0
     if M > MOE_LINEAR_FEW_ROWS or workspace is not None:
-        workspace, pws, size = _scratch(workspace, x, stream, lib.moe_linear_fp8_workspace_bytes, M, N, K)
+        workspace, pws, size = _scratch(workspace, x, stream, _parts_bytes, M, N, K)
     check("moe_linear_fp8", lib.moe_linear_fp8(
         px, ps, x_scales.shape[1], M, N, K, weights.packed.data_ptr(), weights.scales.data_ptr(),
         MOE_LINEAR_OUT_F32 if out_dtype == torch.float32 else 0, py, pws, size, raw))

@@ -649,8 +649,12 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *
  *   x [M, K] uint8 and x_scales [K/128, scale_stride] float32 (scale_stride >= M)
  *   from moe_quant_rows_fp8 or moe_rmsnorm;  y [M, N] bf16, or float32 with
- *   MOE_LINEAR_OUT_F32, not x's buffer;  the workspace may be NULL where the query
- *   says 0, as it does up to MOE_LINEAR_FEW_ROWS rows.
+ *   MOE_LINEAR_OUT_F32, not x's buffer;  workspace: what the query says is enough
+ *   for every smaller M too.  Where moe_linear_fp8_parts says 1 none is used and it may
+ *   be NULL (so always up to MOE_LINEAR_FEW_ROWS rows), else parts M N floats are.
+ * moe_linear_fp8_parts: in how many parts of K a product runs, each summed by
+ * itself and all added in order; tile (2 numbers, or NULL) the rows of x and of W that a
+ * workgroup takes.  0 for sizes that are refused.
  * A row's result depends on that row alone (a NaN stays in its row); equal calls
  * give equal bits, but a row's bits may differ with M.  M = 0 enqueues nothing.
  * Requires M < 2^31, K % 128 == 0, N and K <= 2^20; sizes that need more than 2^32
@@ -659,6 +663,7 @@ size_t moe_linear_fp8_packed_bytes(int N, int K);
 int moe_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float* scales, int N, int K,
                         int flags, uint8_t* packed, float* packed_scales, void* stream);
 size_t moe_linear_fp8_workspace_bytes(int64_t M, int N, int K);
+int moe_linear_fp8_parts(int64_t M, int N, int K, int32_t* tile);
 int moe_linear_fp8(const uint8_t* x, const float* x_scales, int64_t scale_stride, int64_t M, int N,
                    int K, const uint8_t* packed, const float* packed_scales, int flags, void* y,
                    void* workspace, size_t workspace_bytes, void* stream);

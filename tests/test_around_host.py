@@ -198,3 +198,27 @@ def test_sizes_past_the_interface():
                  lambda: ops.moe_balance_loss_workspace_bytes(far, 8)):
         with pytest.raises(ValueError, match="below 2"):
             size()
+
+
+def test_a_product_uses_what_its_parts_take():
+    """The size query is enough for what a product uses, and only that is asked of a caller."""
+    lib = _lib.load()
+    several = 0
+    for M in (1, 16, 17, 40, 64, 128, 333, 1000, 4096):
+        for N in (1, 64, 333, 576, 2048, 4096, 8192):
+            for K in (128, 256, 1024, 2048, 7168):
+                parts, (rows, columns) = ops.moe_linear_fp8_parts(M, N, K)
+                assert parts in (1, 2, 4, 8) and parts <= K // 128 and rows >= 16 and columns >= 16
+                if parts > 1:
+                    several += 1
+                    need = 4 * parts * M * N
+                    assert need <= lib.moe_linear_fp8_workspace_bytes(M, N, K)
+                    kw = dict(M=M, N=N, K=K, stride=M)
+                    for bad in (dict(ws=None), dict(bytes=need - 1), dict(ws=P + 8)):
+                        assert _linear(lib, **kw, **bad) == WORKSPACE
+    assert several > 20
+    assert ops.moe_linear_fp8_parts(16, 8192, 8192) == (1, (16, 16))
+    for sizes in ((0, 128, 128), (1 << 31, 128, 128), (1, 0, 128), (1, 128, 130), (1, (1 << 20) + 1, 128)):
+        assert ops.moe_linear_fp8_parts(*sizes) == (0, (0, 0))
+    with pytest.raises(ValueError, match="below 2"):
+        ops.moe_linear_fp8_parts(1, 1 << 32, 128)

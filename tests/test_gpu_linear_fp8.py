@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from combine_top_route_moe_amd import ops
+from combine_top_route_moe_amd._lib import load
 from tests.around_util import BF16, TINY, U, e4m3, gen, product_slack, quant_rows, quant_tiles, rows64, tiles64, within
 
 pytestmark = pytest.mark.gpu
@@ -266,3 +267,22 @@ def test_weights_past_32_bits(M):
     last = slice(N - 128, N)
     check(y[:, last], xq, xs, codes[last].cpu(), scales[-1:].cpu())
     check(y[:, :128], xq, xs, codes[:128].cpu(), scales[:1].cpu())
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 64, 128), (333, 4096, 2048), (2048, 1280, 1024)])
+def test_without_a_workspace_where_none_is_used(M, N, K):
+    """In one part: the C call takes NULL, the binding allocates the output alone."""
+    xq, xs, wq, ws = _case(M, N, K)
+    weights = ops.linear_weights_from_codes(wq.cuda(), ws.cuda())
+    assert ops.moe_linear_fp8_parts(M, N, K)[0] == 1
+    x, s, y = xq.cuda(), xs.cuda(), torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    status = load().moe_linear_fp8(x.data_ptr(), s.data_ptr(), M, M, N, K, weights.packed.data_ptr(),
+                                   weights.scales.data_ptr(), 0, y.data_ptr(), None, 0,
+                                   torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    made = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]  # noqa: E731
+    before = made()
+    z = ops.moe_linear_fp8(x, s, weights)
+    assert made() == before + 1
+    assert torch.equal(y, z)
+    check(y, xq, xs, wq, ws)
