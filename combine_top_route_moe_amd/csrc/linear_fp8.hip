@@ -549,14 +549,17 @@ int launch_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float*
 //   64 x 64                     0.28                   0.225
 //   64 x 128                    0.40                   0.345
 //   128 x 128                   0.72                   0.55
-//   256 x 256                   1.4                    1.76
-// and for parts the join's launch and its bytes.  Over 230 products of 17 to 8192
-// rows, N from 64 to 8192 and K from 256 to 8192 the form it takes is 1.4 % slower
-// in the geometric mean than the fastest of all eleven.  Both sides of a border, us:
-// 64 x 4096 x 7168 in 64 x 64 tiles 18.4, in 2 parts 14.5, in 4 12.0, in 8 14.4;
-// 512 x 4096 x 7168 in 64 x 64 28, 64 x 128 29, 128 x 128 43; 1024 x 4096 x 7168 57,
-// 42, 44; 2048 x 4096 x 7168 103, 82, 65, 256 x 256 84; 4096 x 4096 x 7168 211, 166,
-// 132, 119.
+//   256 x 256                   1.15                   1.65
+// and for parts the join's launch and its bytes.  A CU holds one 256 x 256 workgroup,
+// so that every round of them fills (and drains) for itself, kFill, and a block of the
+// last takes from the first figure, with a few CUs at work, to the second, with all of
+// them at the clock that the power limit leaves.  Over 230 products of 17 to 8192
+// rows, N from 64 to 8192 and K from 256 to 8192 the form it takes is 1.8 % slower
+// in the geometric mean than the fastest.  Both sides of a border, us (N = 4096, K = 7168):
+// 64 rows in 64 x 64 tiles 18.2, in 2 parts 13.8, in 4 11.5, in 8 13.4; 512 rows in
+// 64 x 64 26, 64 x 128 28, 128 x 128 39; 1024 rows 50, 41, 43; 2048 rows 99, 79, 63,
+// 256 x 256 83; 2304 rows 108, 95, 92, 80; 4096 rows 200, 159, 126, 100; 5120 rows 240,
+// 191, 162, 167.
 struct LinearForm {
   int tile, parts;              // of kTiles; parts of K
 };
@@ -564,15 +567,16 @@ struct LinearForm {
 struct LinearTile {
   int m, n, threads;
   double one, many;
+  bool alone;                   // one workgroup a CU
 };
-constexpr LinearTile kTiles[4] = {{64, 64, 256, 0.28, 0.225}, {64, 128, 512, 0.40, 0.345},
-                                  {128, 128, 256, 0.72, 0.55}, {256, 256, 512, 1.4, 1.76}};
+constexpr LinearTile kTiles[4] = {{64, 64, 256, 0.28, 0.225, false}, {64, 128, 512, 0.40, 0.345, false},
+                                  {128, 128, 256, 0.72, 0.55, false}, {256, 256, 512, 1.15, 1.65, true}};
 constexpr double kThreadsMost = 0xffffffffu;       // of a launch
 constexpr int kPartsMost = 8;                      // 2, 4 or 8 (linear_join_kernel)
 constexpr int64_t kPartBytes = 32 << 20;           // all parts together: more costs more than it gives
 
 static LinearForm linear_form(int64_t M, int N, int nkb) {
-  constexpr double kCUs = 256, kStart = 3.0, kJoin = 3.3, kJoinBytesPerUs = 5e6;
+  constexpr double kCUs = 256, kStart = 3.0, kFill = 6.0, kJoin = 3.3, kJoinBytesPerUs = 5e6;
   LinearForm best = {3, 1};
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
@@ -581,7 +585,10 @@ static LinearForm linear_form(int64_t M, int N, int nkb) {
       const int64_t bytes = (int64_t)parts * M * N * 4;
       if ((parts > 1 && bytes > kPartBytes) || tiles * parts * kTiles[i].threads > kThreadsMost) break;
       const double rounds = std::ceil(tiles * parts / kCUs);
-      double us = kStart + (double)nkb / parts * std::max(kTiles[i].one, rounds * kTiles[i].many);
+      const double one = kTiles[i].one, many = kTiles[i].many, last = tiles * parts / kCUs - (rounds - 1);
+      const double block = kTiles[i].alone ? (rounds - 1) * many + one + last * (many - one)
+                                           : std::max(one, rounds * many);
+      double us = (kTiles[i].alone ? kFill * rounds : kStart) + (double)nkb / parts * block;
       if (parts > 1) us += kJoin + 2.0 * bytes / kJoinBytesPerUs;
       if (us < least) least = us, best = {i, parts};
     }

@@ -1,0 +1,25 @@
+"""Which form of moe_linear_fp8 runs (no GPU needed)."""
+
+import pytest
+
+from combine_top_route_moe_amd import ops
+
+
+@pytest.mark.parametrize("M,N,K,tile", [
+    # 256 x 256 tiles on some of the 256 CUs, us of them and of 128 x 128 tiles
+    (1024, 8192, 2048, 128),       # 128 tiles: 29.0, 22.0
+    (1536, 6000, 4096, 256),       # 144: 48.0, 53.3
+    (2048, 4096, 7168, 128),       # 128: 82.0, 61.8
+    (2304, 4096, 7168, 256),       # 144: 82.6, 91.3
+    (2816, 4096, 7168, 256),       # 176: 90.3, 95.6
+    (2048, 6000, 4096, 256),       # 192: 52.6, 58.3
+    # on all of them, and on some of them once more
+    (4096, 4096, 7168, 256),       # 256: 98.8, 123
+    (2304, 8192, 2048, 128),       # 288: 56.2, 48.1
+    (5120, 4096, 7168, 128),       # 320: 166, 159
+    (3328, 8192, 2048, 256),       # 416: 60.6, 64.7
+    (6144, 4096, 7168, 256),       # 384: 172, 183
+    (8192, 4096, 7168, 256),       # 512: 186, 236
+])
+def test_large_tiles_by_how_many_of_them_run(M, N, K, tile):
+    assert ops.moe_linear_fp8_parts(M, N, K) == (1, (tile, tile))
