@@ -3,6 +3,7 @@
 import pytest
 
 from combine_top_route_moe_amd import ops
+from tests.linear_forms import FORMS
 
 
 @pytest.mark.parametrize("M,N,K,tile", [
@@ -23,3 +24,16 @@ from combine_top_route_moe_amd import ops
 ])
 def test_large_tiles_by_how_many_of_them_run(M, N, K, tile):
     assert ops.moe_linear_fp8_parts(M, N, K) == (1, (tile, tile))
+
+
+@pytest.mark.parametrize("M,N,K,tile,parts", FORMS)
+def test_the_products_that_are_tested_reach_every_form(M, N, K, tile, parts):
+    assert ops.moe_linear_fp8_parts(M, N, K) == (parts, tile)
+
+
+def test_no_form_is_left_out():
+    kinds = {(tile, parts) for *_, tile, parts in FORMS}
+    assert kinds >= {((64, 64), 2), ((64, 64), 4), ((64, 64), 8), ((64, 128), 2), ((64, 128), 4), ((64, 128), 8),
+                     ((128, 128), 2), ((128, 128), 4), ((128, 128), 8)} | {((m, n), 1) for m, n in ((64, 64), (64, 128), (128, 128), (256, 256))}
+    for parts in (2, 4, 8):
+        assert {min(M * N % 4, 1) for M, N, _, _, p in FORMS if p == parts} == {0, 1}
