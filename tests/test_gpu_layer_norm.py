@@ -157,3 +157,75 @@ def test_the_gradient_of_the_layers_norm(fp8, n):
         assert torch.equal(a, b)
     with pytest.raises(ValueError, match="rstd"):
         layer.norm(x[:n], w, rstd=rstd[: n - 1])
+
+
+KINDS = [dict(dispatch_block=128), dict(combine_qdq=True), dict(dispatch_fp4="mxfp4"), dict(combine_fp4="mxfp4"),
+         dict(fp8=True), dict(fp4="mxfp4"), dict(fp4="nvfp4"), dict(pack=False)]
+
+
+def _layer_of(kw, shared=True):
+    kw, g = dict(kw), gen(1)
+    weights = {k: kw.pop(k) for k in ("fp8", "fp4", "pack") if k in kw}
+    layer = MoELayer(T, H, E, K, I, shared_I=I if shared else 0, **kw)
+    w = lambda *s: (0.05 * torch.randn(*s, generator=g)).bfloat16().cuda()  # noqa: E731
+    layer.set_weights(w(E, 2 * I, H), w(E, H, I), *((w(2 * I, H), w(H, I)) if shared else ()), **weights)
+    return layer
+
+
+@pytest.mark.parametrize("kw", KINDS, ids=lambda kw: "-".join(f"{k}={v}" for k, v in kw.items()))
+@pytest.mark.parametrize("shared", [False, True])
+def test_norm_then_forward_of_any_kind(kw, shared):
+    """Quantizers of the dispatched and of the combined rows, weights of every format: on the
+    norm's rows as on the same rows given."""
+    layer, (x, res, w, logits) = _layer_of(kw, shared), _inputs()
+    valid = torch.ones(T, dtype=torch.uint8, device="cuda")
+    valid[[3, 50]] = 0
+    rows = ops.moe_rmsnorm(x, w, residual=res).y
+    if layer.combine_scale is not None:
+        layer.calibrate_combine_scale(logits, rows, valid)
+    want = layer.forward(logits, rows, valid).clone()
+    assert want.any()
+    layer.norm(x, w, residual=res)
+    layer.out.zero_()
+    assert torch.equal(layer.forward(logits, None, valid), want) and int(layer.dev_error) == 0
+
+
+def _router_check(layer, logits, valid, n):
+    """The layer's losses and gradient against those of the operators on its routes."""
+    idx, top = layer.topk_idx[:n].clone(), layer.topk_w[:n].clone()
+    if valid is not None:
+        assert (idx[valid == 0] == -1).all() and (valid == 0).any()
+    want = ops.moe_balance_loss(logits, idx, valid)
+    got = layer.balance_loss(logits, valid)
+    for name in ("loss", "counts", "probs", "num_tokens"):
+        assert torch.equal(getattr(got, name), getattr(want, name)), name
+    real = n if valid is None else int(valid.sum())
+    assert int(got.num_tokens) == real and int(got.counts.sum()) == real * K
+    dw, d = torch.randn(n, K, generator=gen(4)).cuda(), torch.tensor([0.1, 0.01], device="cuda")
+    a = layer.route_backward(logits, dw, valid, d_loss=d, losses=got)
+    b = ops.moe_route_backward(logits, idx, top, dw, valid, d_loss=d, counts=want.counts, num_tokens=want.num_tokens)
+    assert torch.equal(a, b) and a.shape == (n, E) and a.any()
+    if valid is not None:
+        assert not a[valid == 0].any()
+    with pytest.raises(ValueError, match="counts"):
+        layer.route_backward(logits, dw, valid, d_loss=d)
+
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("n", [1, 7, 64, T])
+def test_the_routers_training_behind_forward_and_decode(n, padded):
+    """With padding, and for fewer tokens than the layer's: decode's."""
+    layer, (x, _, _, logits) = _layer(shared=True), _inputs()
+    valid = None
+    if padded:
+        valid = torch.ones(n, dtype=torch.uint8, device="cuda")
+        valid[n // 2] = 0
+    if n == T:
+        layer.forward(logits, x, valid)
+    else:
+        layer.decode(logits[:n], x[:n], valid)
+    if padded and n == 1:                                            # no token at all
+        losses = layer.balance_loss(logits[:1], valid)
+        assert not losses.loss.any() and not losses.counts.any() and int(losses.num_tokens) == 0
+        return
+    _router_check(layer, logits[:n].contiguous(), valid, n)
