@@ -590,7 +590,8 @@ int moe_pack_linear_fp8(const uint16_t* w, const uint8_t* codes, const float* sc
   if ((flags & MOE_LINEAR_TRANSPOSE) && N % 128) return MOE_ERR_UNSUPPORTED;
   if (!w == !codes || !codes != !scales || !packed || !packed_scales) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w) || !aligned16(codes) || !aligned16(packed)) return MOE_ERR_INVALID_ARG;
-  if (packed == codes || packed_scales == scales) return MOE_ERR_INVALID_ARG;
+  if (packed == codes || packed == reinterpret_cast<const uint8_t*>(w) || packed_scales == scales)
+    return MOE_ERR_INVALID_ARG;
   return launch_pack_linear_fp8(w, codes, scales, N, K, flags & MOE_LINEAR_TRANSPOSE, packed,
                                 packed_scales, as_stream(stream));
 }

@@ -222,3 +222,8 @@ def test_a_product_uses_what_its_parts_take():
         assert ops.moe_linear_fp8_parts(*sizes) == (0, (0, 0))
     with pytest.raises(ValueError, match="below 2"):
         ops.moe_linear_fp8_parts(1, 1 << 32, 128)
+
+
+def test_packing_on_the_weights_is_refused(lib):
+    """Workgroups would read what others have written; codes and scales are refused as well."""
+    assert _pack(lib, packed=P) == INVALID
