@@ -596,7 +596,8 @@ int moe_combine_check(const uint16_t* rows, int64_t num_rows, const int32_t* row
  *   bf16;  y [T, H] bf16;  codes [T, H] uint8 with scales [H/128, scale_stride]
  *   float32 (K-block-major, as moe_quant_rows_fp8 writes them; scale_stride >=
  *   T; columns past T are left as they are);  rstd [T] float32, r.
- * h may be x's or residual's buffer and y may be x's.  An all-zero block gets
+ * h may be x's or residual's buffer and y may be x's; no other output may lie on an input
+ * or on another output.  An all-zero block gets
  * codes 0 and scale 0, one with a NaN a NaN scale; sum(h^2) and h weight must be
  * within float32.  T = 0 enqueues nothing.  Pointers 16-byte aligned (rstd,
  * scales: 4).
