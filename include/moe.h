@@ -655,7 +655,7 @@ int moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rst
  *   be NULL (so always up to MOE_LINEAR_FEW_ROWS rows), else parts M N floats are.
  * moe_linear_fp8_parts: in how many parts of K a product runs, each summed by
  * itself and all added in order; tile (2 numbers, or NULL) the rows of x and of W that a
- * workgroup takes.  0 for sizes that are refused.
+ * workgroup takes.  0 where M, N or K is out of the ranges below.
  * A row's result depends on that row alone (a NaN stays in its row); equal calls
  * give equal bits, but a row's bits may differ with M.  M = 0 enqueues nothing.
  * Requires M < 2^31, K % 128 == 0, N and K <= 2^20; sizes that need more than 2^32
